@@ -10,6 +10,11 @@
  *   eagle_tree_attn   tree-masked attention of the tree nodes over the KV prefix
  *   eagle_verify      greedy or speculative-sampling verification walk
  * and eagle_step runs the four in order (or replays them as one graph).
+ * Around them, for a serving loop whose KV cache is paged and held in 8 bits:
+ *   eagle_page_map, eagle_page_release   pages of a free list to requests and back
+ *   eagle_rope                           rotary positions of q and k
+ *   eagle_kv8_append, eagle_kv8_commit   keys and values into the 8-bit cache
+ *   eagle_tree_attn_kv8                  the tree attention over that cache
  *
  * Sources (the pages the method is taken from):
  *   [EAGLE-2] "論文解説: EAGLE-2 - 動的ドラフトツリーによるLLM推論の高速化"
@@ -58,7 +63,8 @@ typedef enum {
   EAGLE_ERR_UNSUPPORTED = -2,
   EAGLE_ERR_CUDA = -3,
   EAGLE_ERR_WORKSPACE = -4,
-  EAGLE_ERR_TIMEOUT = -5
+  EAGLE_ERR_TIMEOUT = -5,
+  EAGLE_ERR_PAGES = -6
 } eagle_status;
 
 typedef enum { EAGLE_F32 = 0, EAGLE_BF16 = 1 } eagle_dtype;
@@ -463,6 +469,212 @@ int eagle_kv_commit(const void *k_tree, const void *v_tree, int dtype, int B,
                     int max_pages, int page_size, int num_pages,
                     int32_t *kv_len, int32_t *slot_mapping, int32_t *status,
                     eagle_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages for new tokens: block tables and slot maps from request lengths.
+ * The explainers name the KV cache of the serving systems but no layout; this
+ * is the bookkeeping behind the block tables that eagle_tree_attn_paged,
+ * eagle_kv_commit and the 8-bit cache below read, kept on the device so that
+ * a step needs no host round trip.
+ * With P = page_size, need_b = ceil((kv_len[b] + new_len[b]) / P) and
+ * add_b = max(0, need_b - page_count[b]): request b gets add_b pages from the
+ * free list, a stack whose top is free_pages[free_count - 1].  The j-th page
+ * taken over all requests (requests in order, logical pages in order) is
+ * free_pages[free_count - 1 - j]; it is written to
+ * block_table[b, page_count[b] ...], page_count[b] becomes
+ * max(page_count[b], need_b) and free_count drops by the pages taken.  The
+ * new tokens are numbered request by request: token t of request b is its
+ * position kv_len[b] + (t - new_start[b]), and
+ *   slot_map[t] = block_table[b, position / P] * P + position % P,
+ * -1 for T > t >= the number of new tokens.
+ *   kv_len       device int32 [B]: tokens already in each request's cache
+ *   new_len      device int32 [B]: tokens about to be written (0 allowed);
+ *                before a tree step, the most the verification can accept
+ *   block_table  device int32 [B, max_pages]  (in/out; other entries stay)
+ *   page_count   device int32 [B]             (in/out: pages mapped)
+ *   free_pages   device int32 [num_pages]     (in; distinct page numbers
+ *                below free_count)
+ *   free_count   device int32 [1]             (in/out)
+ *   slot_map     device int32 [T]             (out; may be NULL with T = 0)
+ *   new_start    device int32 [B+1]           (out; may be NULL): sums of
+ *                new_len before each request, then the total
+ *   status       device int32 (out; may be NULL): EAGLE_ERR_PAGES when the
+ *                free list holds too few pages; EAGLE_ERR_INVALID for a
+ *                negative length, a request beyond max_pages pages, a
+ *                page_count outside [0, max_pages], a free_count outside
+ *                [0, num_pages], or more than T new tokens with a slot_map.
+ *                Nothing is written then.  A page number outside
+ *                [0, num_pages) in either list gives slot -1 and
+ *                EAGLE_ERR_INVALID.
+ * Limits: 1 <= B <= 4096; page rules as for eagle_tree_attn_paged;
+ * num_pages * page_size < 2^31.
+ * ------------------------------------------------------------------------ */
+int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B,
+                   int page_size, int max_pages, int num_pages,
+                   int32_t *block_table, int32_t *page_count,
+                   const int32_t *free_pages, int32_t *free_count,
+                   int32_t *slot_map, int T, int32_t *new_start,
+                   int32_t *status, eagle_stream_t stream);
+
+/* Pages back to the free list.  Request b keeps its first
+ * min(page_count[b], ceil(keep_len[b] / P)) pages (keep_len 0: none; its
+ * kv_len: what it uses now) and gives back the others; a negative keep_len
+ * leaves it as it is.  Of R pages given back, in the order in which
+ * eagle_page_map takes them, the k-th goes to
+ * free_pages[free_count + R - 1 - k]: releasing what a map took restores the
+ * stack.  Their block_table entries become -1, page_count the pages kept,
+ * free_count grows by R.
+ *   keep_len     device int32 [B]; the other arrays as in eagle_page_map
+ *   status       EAGLE_ERR_INVALID (nothing written) for a page_count outside
+ *                [0, max_pages], a free_count below 0 or a free list that
+ *                would exceed num_pages entries.
+ * Limits as for eagle_page_map. */
+int eagle_page_release(const int32_t *keep_len, int B, int page_size,
+                       int max_pages, int num_pages, int32_t *block_table,
+                       int32_t *page_count, int32_t *free_pages,
+                       int32_t *free_count, int32_t *status,
+                       eagle_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions of queries and keys, into the tree attention's layouts.
+ * The target's layers rotate the pair (x_a, x_b) number j of each head by the
+ * angle position * inv_freq[j] before the attention:
+ *   x_a' = factor * (x_a cos - x_b sin),  x_b' = factor * (x_b cos + x_a sin)
+ * for j < rot_dim / 2; the pair is (j, j + rot_dim/2) or, with `interleaved`,
+ * (2j, 2j + 1).  Columns rot_dim .. dh-1 are copied.  The position of node i
+ * of sequence b is pos_base[b] + pos_off[b, i] + shift (pos_base NULL: 0;
+ * pos_off NULL: i); for a tree whose root is the last prefix position, as
+ * eagle_kv_commit has it, pass kv_len, node_depth and shift = -1.
+ *   q, k, v    dtype, node (b, i) starts at element (b*n + i) * ld_q (ld_k,
+ *              ld_v), its heads dh apart: slices of one fused projection do.
+ *              v may be NULL (then v_tree is unused)
+ *   inv_freq   device double [rot_dim/2] (eagle_rope_freqs computes them)
+ *   pos_base   device int32 [B] or NULL;  pos_off  device int32 [B, n] or NULL
+ *   q_out      dtype [B, n, Hq, dh]   (out; may be q itself when ld_q = Hq*dh)
+ *   k_tree     dtype [B, Hkv, n, dh]  (out)
+ *   v_tree     dtype [B, Hkv, n, dh]  (out: v in that layout)
+ * Other outputs must not overlap the inputs.  Angles are reduced in 64-bit
+ * fixed point (turns), so far positions lose nothing; cos, sin and the
+ * rotation are float32, rounded once to the output type.
+ * Limits: n >= 1; B*n <= 2^24; Hq, Hkv >= 1; rot_dim even, 2 <= rot_dim <=
+ * dh <= 512; dh*elemsize and ld*elemsize multiples of 16 bytes, tensors
+ * 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B,
+               int n, int Hq, int Hkv, int dh, int64_t ld_q, int64_t ld_k,
+               int64_t ld_v, const double *inv_freq, int rot_dim,
+               int interleaved, float factor, const int32_t *pos_base,
+               const int32_t *pos_off, int shift, void *q_out, void *k_tree,
+               void *v_tree, eagle_stream_t stream);
+
+/* The frequencies of eagle_rope, computed on the host in double:
+ * f_j = theta^(-2j / rot_dim), stretched for contexts longer than the
+ * orig_len tokens a model was trained on:
+ *   EAGLE_ROPE_PLAIN   f_j
+ *   EAGLE_ROPE_LINEAR  f_j / stretch
+ *   EAGLE_ROPE_BANDS   by the turns t_j = orig_len f_j / 2pi that pair j makes
+ *                      over the trained context: f_j / stretch at t_j <= low,
+ *                      f_j at t_j >= high, linear in t_j between
+ *   EAGLE_ROPE_YARN    the same ends at low and high turns, but linear in the
+ *                      pair's index between, and *factor =
+ *                      0.1 ln(stretch) + 1 (1 for the others)
+ *   inv_freq  HOST double [rot_dim/2] (out);  factor  HOST float (out; may be
+ *             NULL)
+ * Limits: rot_dim even, >= 2; theta > 1; stretch >= 1; BANDS and YARN:
+ * orig_len >= 1, 0 < low < high. */
+#define EAGLE_ROPE_PLAIN 0
+#define EAGLE_ROPE_LINEAR 1
+#define EAGLE_ROPE_BANDS 2
+#define EAGLE_ROPE_YARN 3
+int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch,
+                     int orig_len, double low, double high, double *inv_freq,
+                     float *factor);
+
+/* ------------------------------------------------------------------------
+ * The paged KV cache in 8 bits.
+ *   k_pages, v_pages  uint8 [num_pages, Hkv, page_size, dh]: e4m3 numbers
+ *   k_scale, v_scale  float [num_pages, Hkv]: one scale for each page and head,
+ *                     a power of two in [2^-64, 2^64]
+ * A cache value is its e4m3 number times its page's scale.  The scale is 2^e
+ * with the least e for which every row written to the page so far fits:
+ * max |x| <= 448 * 2^e.  A power of two costs no precision in a floating
+ * format (x / 2^e is exact, so a value is rounded once, to nearest even) and
+ * leaves a cache value exact in 16 bits.  When later rows need a larger scale the
+ * page's earlier rows are re-encoded; that too is exact but for numbers below
+ * 2^-6 of the new scale.
+ * Rows are written in order: a page's row 0 starts the page afresh (its old
+ * scale and rows count no more), any other row joins the rows before it.
+ * A value that is not finite is stored as NaN, counts for no maximum and sets
+ * EAGLE_ERR_INVALID; one beyond 448 * 2^64 is stored as the largest number.
+ *
+ * eagle_kv8_append writes T tokens (a prompt's, or one per sequence) to
+ * the slots of eagle_page_map:
+ *   k, v      dtype; token t's head h starts at element
+ *             t*token_stride + h*head_stride
+ *   slot_map  device int32 [T]: page * page_size + row; negative entries are
+ *             skipped.  The tokens of one page are neighbours in slot_map with
+ *             consecutive rows (as eagle_page_map lists them): a neighbour in
+ *             the same page that breaks the sequence is skipped and sets
+ *             EAGLE_ERR_INVALID, as does a slot past the pool.  A page that is
+ *             listed in two places of slot_map ends up unspecified.
+ *   status    device int32 (out; may be NULL)
+ * Limits: T >= 0; dh a multiple of 16, at most 512; strides * elemsize multiples of 16
+ * bytes, tensors 16-byte aligned; page_size a power of two in [16, 4096];
+ * num_pages * page_size < 2^31; Hkv <= 32767.
+ * ------------------------------------------------------------------------ */
+int eagle_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv,
+                     int dh, int64_t token_stride, int64_t head_stride,
+                     const int32_t *slot_map, uint8_t *k_pages,
+                     uint8_t *v_pages, float *k_scale, float *v_scale,
+                     int page_size, int num_pages, int32_t *status,
+                     eagle_stream_t stream);
+
+/* eagle_kv_commit into the 8-bit cache: the accepted path's rows of
+ * k_tree/v_tree [B, Hkv, n, dh] join the cache at kv_len[b] .., kv_len[b]
+ * grows by accept_len[b].  Arguments, slot_mapping and device errors as in
+ * eagle_kv_commit with a block table.  Limits: those of eagle_kv_commit and
+ * of eagle_kv8_append. */
+int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B,
+                     int n, int Hkv, int dh, const int32_t *accept_len,
+                     const int32_t *path_nodes, int D, uint8_t *k_pages,
+                     uint8_t *v_pages, float *k_scale, float *v_scale,
+                     const int32_t *block_table, int max_pages, int page_size,
+                     int num_pages, int32_t *kv_len, int32_t *slot_mapping,
+                     int32_t *status, eagle_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Stage 3 over the 8-bit paged cache.
+ * The computation of eagle_tree_attn_paged with the prefix's keys and values
+ * read from the 8-bit cache above; queries and tree K/V stay bf16.  n = 1
+ * (mask word 1) is plain decoding of one token per sequence.
+ *   k_pages, v_pages, k_scale, v_scale   as above; scales that are not powers
+ *              of two in range are read as the power of two below, clamped
+ *   block_table, max_pages, page_size, num_pages, kv_len, k_tree, v_tree,
+ *   mask, scale, out, lse, workspace      as in eagle_tree_attn_paged
+ *   status     EAGLE_ERR_INVALID for a block-table entry outside
+ *              [0, num_pages) on a page that the prefix uses (page 0 is read
+ *              in its place), EAGLE_ERR_TIMEOUT as in eagle_tree_attn
+ * A row without any key (kv_len 0, empty mask row) gives zeros and lse =
+ * -inf.  Rows of a page at or beyond kv_len may be read but never
+ * count, whatever they hold.  q, k_tree and v_tree must be finite, and so must
+ * every mask-excluded row of the tree.
+ * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};
+ * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31.
+ * ------------------------------------------------------------------------ */
+size_t eagle_tree_attn_kv8_workspace_size(int dtype, int B, int n, int Hq,
+                                          int Hkv, int dh, int max_pages,
+                                          int page_size);
+
+int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages,
+                        const uint8_t *v_pages, const float *k_scale,
+                        const float *v_scale, const int32_t *block_table,
+                        int max_pages, int page_size, int num_pages,
+                        const int32_t *kv_len, const void *k_tree,
+                        const void *v_tree, const uint64_t *mask, int dtype,
+                        int B, int n, int Hq, int Hkv, int dh, float scale,
+                        void *out, float *lse, int32_t *status,
+                        void *workspace, size_t workspace_bytes,
+                        eagle_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The whole step in one call, and as one recorded graph.

@@ -18,6 +18,13 @@ library is missing or a call reports an error, an exception is raised.
     verify_noalloc -> eagle_verify_noalloc (the same without a caller workspace)
     verify_draft -> eagle_verify_draft (sampling walk against draft distributions q)
     selftest_wait -> eagle_selftest_wait (a bounded device wait that must give up)
+    page_map / page_release -> eagle_page_map, eagle_page_release (pages of a
+                   free list to requests and back; slots of new tokens)
+    rope        -> eagle_rope         (rotary positions, into the attention's layouts;
+                   rope_freqs -> eagle_rope_freqs)
+    kv8_append / kv8_commit -> eagle_kv8_append, eagle_kv8_commit (keys and
+                   values into the paged cache of e4m3 numbers)
+    tree_attn_kv8 -> eagle_tree_attn_kv8 (tree attention over that cache)
     run_step / StepGraph -> eagle_step, eagle_step_graph_* (the four stages
                    in one call, or recorded once as a graph and replayed)
 """
@@ -32,6 +39,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libeagle.so")
 F32, BF16 = 0, 1
 GREEDY, SAMPLE = 0, 1
 TREE_CONFIDENCE_ONLY, TREE_NO_RERANK = 1, 2
+ROPE_KINDS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
 
 EXPORTED = (
     "eagle_status_string", "eagle_version", "eagle_selftest_wait",
@@ -40,6 +48,8 @@ EXPORTED = (
     "eagle_tree_attn_workspace_size", "eagle_tree_attn_kernel_count", "eagle_tree_attn",
     "eagle_tree_attn_paged_workspace_size", "eagle_tree_attn_paged", "eagle_kv_commit",
     "eagle_verify_workspace_size", "eagle_verify", "eagle_verify_noalloc", "eagle_verify_draft",
+    "eagle_page_map", "eagle_page_release", "eagle_rope", "eagle_rope_freqs",
+    "eagle_kv8_append", "eagle_kv8_commit", "eagle_tree_attn_kv8_workspace_size", "eagle_tree_attn_kv8",
     "eagle_step_workspace_size", "eagle_step", "eagle_step_graph_create", "eagle_step_graph_launch",
     "eagle_step_graph_destroy",
 )
@@ -103,6 +113,14 @@ def load_library(path=LIB_PATH):
         "eagle_verify": (I, [P, I, I64, P, P, I, I, I, I, I, F, P, P, P, P, P, P, SZ, P]),
         "eagle_verify_noalloc": (I, [P, I, I64, P, P, I, I, I, I, I, F, P, P, P, P, P, P]),
         "eagle_verify_draft": (I, [P, P, I, I64, I64, P, P, P, I, I, I, I, I, F, P, P, P, P, P, P]),
+        "eagle_page_map": (I, [P, P, I, I, I, I, P, P, P, P, P, I, P, P, P]),
+        "eagle_page_release": (I, [P, I, I, I, I, P, P, P, P, P, P]),
+        "eagle_rope": (I, [P, P, P, I, I, I, I, I, I, I64, I64, I64, P, I, I, F, P, P, I, P, P, P, P]),
+        "eagle_rope_freqs": (I, [I, ctypes.c_double, I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double, P, P]),
+        "eagle_kv8_append": (I, [P, P, I, I, I, I, I64, I64, P, P, P, P, P, I, I, P, P]),
+        "eagle_kv8_commit": (I, [P, P, I, I, I, I, I, P, P, I, P, P, P, P, P, I, I, I, P, P, P, P]),
+        "eagle_tree_attn_kv8_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
+        "eagle_tree_attn_kv8": (I, [P, P, P, P, P, P, I, I, I, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, SZ, P]),
         "eagle_step_workspace_size": (SZ, [ctypes.POINTER(StepArgs)]),
         "eagle_step": (I, [ctypes.POINTER(StepArgs), P, SZ, P]),
         "eagle_step_graph_create": (I, [ctypes.POINTER(StepArgs), P, SZ, ctypes.POINTER(P)]),
@@ -390,6 +408,239 @@ def kv_commit(k_tree, v_tree, accept_len, path_nodes, k_cache, v_cache, kv_len, 
                                max_pages, page_size, num_pages, _ptr(kv_len), _ptr(slot_mapping), _ptr(status),
                                _stream(stream)), "eagle_kv_commit")
     return slot_mapping
+
+
+# ---- the serving loop around the step: pages, positions, the 8-bit cache ------
+
+def _need(t, name, dtype=None, shape=None, device=None):
+    """t, if it is a contiguous CUDA tensor of that type, shape and device."""
+    if not t.is_cuda:
+        raise EagleError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise EagleError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise EagleError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise EagleError(f"{name} must be on {device}, not {t.device}")
+    if not t.is_contiguous():
+        raise EagleError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _maybe(t, name, dtype, shape, device):
+    return None if t is None else _need(t, name, dtype, shape, device)
+
+
+def _call(what, fn, device, stream, *args):
+    """fn(*args, stream) with `device` current and on its current stream."""
+    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, s)
+    if rc:
+        _check(rc, what)
+
+
+def page_map(kv_len, new_len, block_table, page_count, free_pages, free_count, page_size, slot_map=None,
+             new_start=None, status=None, stream=None):
+    """Maps the pages that new_len [B] more tokens need and lists the tokens'
+    slots (eagle_page_map).  kv_len, new_len, page_count int32 [B], block_table
+    int32 [B, max_pages], free_pages int32 [num_pages], free_count int32 [1];
+    block_table, page_count and free_count are updated in place.  slot_map
+    int32 [T] (optional) receives the slots of the new tokens, request by
+    request, then -1; new_start int32 [B+1] (optional) their first indices.
+    Returns slot_map.  Too few free pages leave everything as it was and set
+    `status` to -6."""
+    lib = load_library()
+    dev, i32 = kv_len.device, torch.int32
+    B, max_pages = block_table.shape
+    num_pages = free_pages.shape[0]
+    _call("eagle_page_map", lib.eagle_page_map, dev, stream, _need(kv_len, "kv_len", i32, (B,)),
+          _need(new_len, "new_len", i32, (B,), dev), B, page_size, max_pages, num_pages,
+          _need(block_table, "block_table", i32, None, dev), _need(page_count, "page_count", i32, (B,), dev),
+          _need(free_pages, "free_pages", i32, (num_pages,), dev), _need(free_count, "free_count", i32, (1,), dev),
+          _maybe(slot_map, "slot_map", i32, None, dev), 0 if slot_map is None else slot_map.numel(),
+          _maybe(new_start, "new_start", i32, (B + 1,), dev), _maybe(status, "status", i32, None, dev))
+    return slot_map
+
+
+def page_release(keep_len, block_table, page_count, free_pages, free_count, page_size, status=None, stream=None):
+    """Gives back the pages past keep_len [B] tokens of each request
+    (eagle_page_release): 0 ends a request, its kv_len trims it to what it
+    uses, a negative length leaves it alone.  The other arrays are those of
+    page_map, updated in place."""
+    lib = load_library()
+    dev, i32 = keep_len.device, torch.int32
+    B, max_pages = block_table.shape
+    num_pages = free_pages.shape[0]
+    _call("eagle_page_release", lib.eagle_page_release, dev, stream, _need(keep_len, "keep_len", i32, (B,)), B,
+          page_size, max_pages, num_pages, _need(block_table, "block_table", i32, None, dev),
+          _need(page_count, "page_count", i32, (B,), dev), _need(free_pages, "free_pages", i32, (num_pages,), dev),
+          _need(free_count, "free_count", i32, (1,), dev), _maybe(status, "status", i32, None, dev))
+
+
+def rope_freqs(rot_dim, theta=10000.0, kind="plain", stretch=1.0, orig_len=4096, low=1.0, high=32.0, device=None):
+    """Frequencies of rope() (eagle_rope_freqs): (inv_freq float64 [rot_dim/2]
+    on `device`, factor).  kind: "plain", "linear", "bands" (stretched below
+    `low` turns over orig_len tokens, kept above `high`) or "yarn"."""
+    if kind not in ROPE_KINDS:
+        raise EagleError(f"unknown kind {kind!r}: one of {sorted(ROPE_KINDS)}")
+    out = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    factor = ctypes.c_float()
+    _check(load_library().eagle_rope_freqs(int(rot_dim), float(theta), ROPE_KINDS[kind], float(stretch),
+                                           int(orig_len), float(low), float(high), out.data_ptr(),
+                                           ctypes.addressof(factor)), "eagle_rope_freqs")
+    return out.to(device or "cuda"), factor.value
+
+
+def _heads(t, name, B, n, dh, dtype, device):
+    """Node stride of [B, n, heads, dh] whose heads are dense and whose nodes
+    are evenly spaced."""
+    if not t.is_cuda or t.dtype != dtype or t.device != device:
+        raise EagleError(f"{name} must be {dtype} on {device}")
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != dh:
+        raise EagleError(f"{name} must be [B, n, heads, dh]")
+    sb, sn, sh, sd = t.stride()
+    if n == 1 and B > 1:
+        sn = sb                # the one node's stride says nothing
+    elif n == 1:
+        sn = max(sn, t.shape[2] * dh)
+    if sd != 1 or (t.shape[2] > 1 and sh != dh) or (B > 1 and sb != n * sn):
+        raise EagleError(f"{name} must have dense heads and evenly spaced nodes")
+    return sn
+
+
+def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, interleaved=False, q_out=None,
+         k_tree=None, v_tree=None, stream=None):
+    """Rotary positions (eagle_rope).  q [B, n, Hq, dh], k and v [B, n, Hkv, dh]
+    (v may be None), nodes evenly spaced, so slices of one fused projection do
+    -> q_out [B, n, Hq, dh], k_tree and v_tree [B, Hkv, n, dh], as tree_attn
+    takes them.  Node i of sequence b is at position pos_base[b] + pos_off[b,
+    i] + shift (0 and i where they are None).  inv_freq float64 [rot_dim/2]
+    and factor as rope_freqs gives them."""
+    lib = load_library()
+    dev, dt = q.device, q.dtype
+    if q.dim() != 4:
+        raise EagleError("q must be [B, n, Hq, dh]")
+    B, n, Hq, dh = q.shape
+    Hkv = k.shape[2]
+    ld_q, ld_k = _heads(q, "q", B, n, dh, dt, dev), _heads(k, "k", B, n, dh, dt, dev)
+    ld_v = 0
+    if v is not None:
+        ld_v = _heads(v, "v", B, n, dh, dt, dev)
+        if v.shape[2] != Hkv:
+            raise EagleError("k and v must have the same heads")
+    if q_out is None:
+        q_out = torch.empty((B, n, Hq, dh), dtype=dt, device=dev)
+    if k_tree is None:
+        k_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=dev)
+    if v_tree is None and v is not None:
+        v_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=dev)
+    i32 = torch.int32
+    _call("eagle_rope", lib.eagle_rope, dev, stream, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(),
+          _dtype_code(q), B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v,
+          _need(inv_freq, "inv_freq", torch.float64, None, dev), 2 * inv_freq.numel(), int(interleaved), factor,
+          _maybe(pos_base, "pos_base", i32, (B,), dev), _maybe(pos_off, "pos_off", i32, (B, n), dev), shift,
+          _need(q_out, "q_out", dt, (B, n, Hq, dh), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),
+          _maybe(v_tree, "v_tree", dt, (B, Hkv, n, dh), dev))
+    return q_out, k_tree, v_tree
+
+
+_POOL_TYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _pools(k_pages, v_pages, k_scale, v_scale, device):
+    """The 8-bit cache's four pointers, checked against each other."""
+    if k_pages.dtype not in _POOL_TYPES or k_pages.dim() != 4:
+        raise EagleError("k_pages must be float8_e4m3fn (or uint8) [num_pages, Hkv, page_size, dh]")
+    shape = tuple(k_pages.shape)
+    return (_need(k_pages, "k_pages", None, None, device), _need(v_pages, "v_pages", k_pages.dtype, shape, device),
+            _need(k_scale, "k_scale", torch.float32, shape[:2], device),
+            _need(v_scale, "v_scale", torch.float32, shape[:2], device))
+
+
+def kv8_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, status=None, stream=None):
+    """Writes tokens' keys and values (k, v [T, Hkv, dh], any token and head
+    strides, the same for both) to the slots slot_map int32 [T] of the 8-bit
+    cache (eagle_kv8_append): k_pages, v_pages float8_e4m3fn [num_pages, Hkv,
+    page_size, dh], k_scale, v_scale float32 [num_pages, Hkv]."""
+    lib = load_library()
+    dev = k.device
+    if not k.is_cuda or k.dim() != 3:
+        raise EagleError("k must be a CUDA tensor [T, Hkv, dh]")
+    T, Hkv, dh = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != dev or v.stride() != k.stride():
+        raise EagleError("v must have k's shape, strides, type and device")
+    if T and k.stride(2) != 1:
+        raise EagleError("k must have unit stride in dh")
+    num_pages, H, page_size, d = k_pages.shape
+    if H != Hkv or d != dh:
+        raise EagleError("k must have the pages' heads and head dimension")
+    if min(k.stride()) < 0 or (T > 1 and Hkv > 1 and 0 in k.stride()):
+        raise EagleError("k must not be a broadcast view")
+    _call("eagle_kv8_append", lib.eagle_kv8_append, dev, stream, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, Hkv,
+          dh, k.stride(0), k.stride(1), _need(slot_map, "slot_map", torch.int32, (T,), dev),
+          *_pools(k_pages, v_pages, k_scale, v_scale, dev), page_size, num_pages,
+          _maybe(status, "status", torch.int32, None, dev))
+
+
+def kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale, v_scale, kv_len, block_table,
+               slot_mapping=None, status=None, stream=None):
+    """kv_commit into the 8-bit cache (eagle_kv8_commit): the accepted path's
+    rows of k_tree, v_tree [B, Hkv, n, dh] join the pages, kv_len is updated
+    in place.  Returns slot_mapping [B, n]."""
+    lib = load_library()
+    dev, i32 = k_tree.device, torch.int32
+    B, Hkv, n, dh = k_tree.shape
+    num_pages, H, page_size, d = k_pages.shape
+    if H != Hkv or d != dh:
+        raise EagleError("k_tree must have the pages' heads and head dimension")
+    D = path_nodes.shape[1] - 1
+    max_pages = block_table.shape[1]
+    if slot_mapping is None:
+        slot_mapping = torch.empty((B, n), dtype=i32, device=dev)
+    _call("eagle_kv8_commit", lib.eagle_kv8_commit, dev, stream, _need(k_tree, "k_tree"),
+          _need(v_tree, "v_tree", k_tree.dtype, (B, Hkv, n, dh), dev), _dtype_code(k_tree), B, n, Hkv, dh,
+          _need(accept_len, "accept_len", i32, (B,), dev), _need(path_nodes, "path_nodes", i32, (B, D + 1), dev), D,
+          *_pools(k_pages, v_pages, k_scale, v_scale, dev),
+          _need(block_table, "block_table", i32, (B, max_pages), dev), max_pages, page_size, num_pages,
+          _need(kv_len, "kv_len", i32, (B,), dev), _need(slot_mapping, "slot_mapping", i32, (B, n), dev),
+          _maybe(status, "status", i32, None, dev))
+    return slot_mapping
+
+
+def tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_tree, v_tree, mask, scale=None,
+                  out=None, lse=None, workspace=None, status=None, stream=None):
+    """Tree attention over the 8-bit paged cache (eagle_tree_attn_kv8): q
+    [B, n, Hq, dh] and k_tree, v_tree [B, Hkv, n, dh] bf16, pages and scales as
+    kv8_append writes them, block_table int32 [B, max_pages]; else as
+    tree_attn.  n = 1 with mask 1 decodes single tokens."""
+    lib = load_library()
+    dev, dt = q.device, q.dtype
+    B, n, Hq, dh = q.shape
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    max_pages = block_table.shape[1]
+    scale = dh ** -0.5 if scale is None else scale
+    if out is None:
+        out = torch.empty((B, n, Hq, dh), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev)
+    code = _dtype_code(q)
+    if k_pages.shape[3] != dh:
+        raise EagleError("q must have the pages' head dimension")
+    need = lib.eagle_tree_attn_kv8_workspace_size(code, B, n, Hq, Hkv, dh, max_pages, page_size)
+    buf, nbytes = (workspace or Workspace(dev)).get(need)
+    _call("eagle_tree_attn_kv8", lib.eagle_tree_attn_kv8, dev, stream, _need(q, "q"),
+          *_pools(k_pages, v_pages, k_scale, v_scale, dev),
+          _need(block_table, "block_table", torch.int32, (B, max_pages), dev), max_pages, page_size, num_pages,
+          _need(kv_len, "kv_len", torch.int32, (B,), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),
+          _need(v_tree, "v_tree", dt, (B, Hkv, n, dh), dev),
+          _need(mask, "mask", torch.int64, (B, n, (n + 63) // 64), dev), code, B, n, Hq, Hkv, dh, scale,
+          _need(out, "out", dt, (B, n, Hq, dh), dev), _need(lse, "lse", torch.float32, (B, n, Hq), dev),
+          _maybe(status, "status", torch.int32, None, dev), None if buf is None else buf.data_ptr(), nbytes)
+    return out, lse
 
 
 def selftest_wait(limit_ns=1_000_000, which=0, stream=None):

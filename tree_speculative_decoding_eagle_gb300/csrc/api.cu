@@ -63,6 +63,39 @@ cudaError_t launch_verify(const void *target, int dtype, int64_t ld, const int32
                           int32_t *path_nodes, int32_t *out_tokens, int32_t *status, void *ws,
                           int num_sms, cudaStream_t st);
 
+// page_map.cu
+cudaError_t launch_page_map(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages,
+                            int num_pages, int32_t *block_table, int32_t *page_count, const int32_t *free_pages,
+                            int32_t *free_count, int32_t *slot_map, int T, int32_t *new_start, int32_t *status,
+                            cudaStream_t st);
+cudaError_t launch_page_release(const int32_t *keep_len, int B, int page_size, int max_pages, int num_pages,
+                                int32_t *block_table, int32_t *page_count, int32_t *free_pages, int32_t *free_count,
+                                int32_t *status, cudaStream_t st);
+// rope.cu
+cudaError_t launch_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv, int dh,
+                        int64_t ld_q, int64_t ld_k, int64_t ld_v, const double *inv_freq, int rot_dim,
+                        int interleaved, float factor, const int32_t *pos_base, const int32_t *pos_off, int shift,
+                        void *q_out, void *k_tree, void *v_tree, cudaStream_t st);
+void rope_freqs(int rot_dim, double theta, int kind, double stretch, int orig_len, double low, double high,
+                double *inv_freq, float *factor);
+// kv8_write.cu
+cudaError_t launch_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv, int dh, int64_t token_stride,
+                              int64_t head_stride, const int32_t *slot_map, uint8_t *k_pages, uint8_t *v_pages,
+                              float *k_scale, float *v_scale, int page_size, int num_pages, int32_t *status,
+                              int num_sms, cudaStream_t st);
+cudaError_t launch_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+                              const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages,
+                              uint8_t *v_pages, float *k_scale, float *v_scale, const int32_t *block_table,
+                              int max_pages, int page_size, int num_pages, int32_t *kv_len, int32_t *slot_mapping,
+                              int32_t *status, cudaStream_t st);
+// tree_attn_kv8.cu
+size_t attn_kv8_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num_sms);
+cudaError_t launch_tree_attn_kv8(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
+                                 const float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                                 int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
+                                 const uint64_t *mask, int B, int n, int Hq, int Hkv, int dh, float scale, void *out,
+                                 float *lse, void *ws, int32_t *status, int num_sms, cudaStream_t st);
+
 // SM count of the current device (queried once per device).
 int current_num_sms() {
   static int cached[64] = {0};
@@ -96,6 +129,7 @@ const char *eagle_status_string(int code) {
     case EAGLE_ERR_CUDA: return "CUDA error";
     case EAGLE_ERR_WORKSPACE: return "workspace too small";
     case EAGLE_ERR_TIMEOUT: return "device wait timed out";
+    case EAGLE_ERR_PAGES: return "too few free pages";
     default: return "unknown status";
   }
 }
@@ -299,6 +333,134 @@ int eagle_verify_draft(const void *target, const void *draft, int dtype, int64_t
   return from_cuda(launch_verify_draft(target, draft, dtype, ld_t, ld_d, node_tok, node_parent, node_row, B, m,
                                        D, k, V, temperature, uniforms, accept_len, path_nodes, out_tokens, status,
                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Page pools addressed by 32-bit slots.
+static bool valid_slots(int max_pages, int page_size, int num_pages) {
+  return valid_pages(max_pages, page_size, num_pages) && static_cast<int64_t>(num_pages) * page_size <= INT32_MAX;
+}
+
+int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages, int num_pages,
+                   int32_t *block_table, int32_t *page_count, const int32_t *free_pages, int32_t *free_count,
+                   int32_t *slot_map, int T, int32_t *new_start, int32_t *status, eagle_stream_t stream) {
+  if (!kv_len || !new_len || !block_table || !page_count || !free_pages || !free_count) return EAGLE_ERR_INVALID;
+  if (B < 1 || T < 0 || (!slot_map && T) || !valid_slots(max_pages, page_size, num_pages)) return EAGLE_ERR_INVALID;
+  if (B > 4096) return EAGLE_ERR_UNSUPPORTED;  // one CTA's shared memory holds every request's sums
+  return from_cuda(launch_page_map(kv_len, new_len, B, page_size, max_pages, num_pages, block_table, page_count,
+                                   free_pages, free_count, slot_map, T, new_start, status,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_page_release(const int32_t *keep_len, int B, int page_size, int max_pages, int num_pages,
+                       int32_t *block_table, int32_t *page_count, int32_t *free_pages, int32_t *free_count,
+                       int32_t *status, eagle_stream_t stream) {
+  if (!keep_len || !block_table || !page_count || !free_pages || !free_count) return EAGLE_ERR_INVALID;
+  if (B < 1 || !valid_slots(max_pages, page_size, num_pages)) return EAGLE_ERR_INVALID;
+  if (B > 4096) return EAGLE_ERR_UNSUPPORTED;
+  return from_cuda(launch_page_release(keep_len, B, page_size, max_pages, num_pages, block_table, page_count,
+                                       free_pages, free_count, status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv, int dh,
+               int64_t ld_q, int64_t ld_k, int64_t ld_v, const double *inv_freq, int rot_dim, int interleaved,
+               float factor, const int32_t *pos_base, const int32_t *pos_off, int shift, void *q_out, void *k_tree,
+               void *v_tree, eagle_stream_t stream) {
+  if (!q || !k || !inv_freq || !q_out || !k_tree || (v && !v_tree) || !valid_dtype(dtype)) return EAGLE_ERR_INVALID;
+  if (B < 1 || n < 1 || Hq < 1 || Hkv < 1 || dh < 1 || rot_dim < 2 || rot_dim % 2 || rot_dim > dh)
+    return EAGLE_ERR_INVALID;
+  if (static_cast<int64_t>(B) * n > (1 << 24) || dh > 512 || static_cast<int64_t>(Hq) + 2ll * Hkv > (1 << 16))
+    return EAGLE_ERR_UNSUPPORTED;
+  const int es = elem_size(dtype);
+  if ((dh * es) % 16 || (ld_q * es) % 16 || (ld_k * es) % 16 || (v && (ld_v * es) % 16)) return EAGLE_ERR_INVALID;
+  if (ld_q < static_cast<int64_t>(Hq) * dh || ld_k < static_cast<int64_t>(Hkv) * dh ||
+      (v && ld_v < static_cast<int64_t>(Hkv) * dh))
+    return EAGLE_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_tree) ||
+      !aligned16(v_tree))
+    return EAGLE_ERR_INVALID;
+  if (q_out == q && ld_q != static_cast<int64_t>(Hq) * dh) return EAGLE_ERR_INVALID;
+  return from_cuda(launch_rope(q, k, v, dtype, B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v, inv_freq, rot_dim, interleaved,
+                               factor, pos_base, pos_off, shift, q_out, k_tree, v_tree,
+                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch, int orig_len, double low, double high,
+                     double *inv_freq, float *factor) {
+  if (!inv_freq || rot_dim < 2 || rot_dim % 2 || !(theta > 1.0) || !(stretch >= 1.0)) return EAGLE_ERR_INVALID;
+  if (kind < EAGLE_ROPE_PLAIN || kind > EAGLE_ROPE_YARN) return EAGLE_ERR_INVALID;
+  if (kind >= EAGLE_ROPE_BANDS && (orig_len < 1 || !(low > 0.0) || !(high > low))) return EAGLE_ERR_INVALID;
+  rope_freqs(rot_dim, theta, kind, stretch, orig_len, low, high, inv_freq, factor);
+  return EAGLE_OK;
+}
+
+int eagle_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv, int dh, int64_t token_stride,
+                     int64_t head_stride, const int32_t *slot_map, uint8_t *k_pages, uint8_t *v_pages,
+                     float *k_scale, float *v_scale, int page_size, int num_pages, int32_t *status,
+                     eagle_stream_t stream) {
+  if (!valid_dtype(dtype) || T < 0 || Hkv < 1 || dh < 16 || dh % 16 || dh > 512 || token_stride < 0 || head_stride < 0)
+    return EAGLE_ERR_INVALID;
+  if (!valid_slots(1, page_size, num_pages)) return EAGLE_ERR_INVALID;
+  if (Hkv > 32767) return EAGLE_ERR_UNSUPPORTED;
+  if (T == 0) return EAGLE_OK;
+  if (!k || !v || !slot_map || !k_pages || !v_pages || !k_scale || !v_scale) return EAGLE_ERR_INVALID;
+  const int es = elem_size(dtype);
+  if ((token_stride * es) % 16 || (head_stride * es) % 16) return EAGLE_ERR_INVALID;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages)) return EAGLE_ERR_INVALID;
+  return from_cuda(launch_kv8_append(k, v, dtype, T, Hkv, dh, token_stride, head_stride, slot_map, k_pages, v_pages,
+                                     k_scale, v_scale, page_size, num_pages, status, current_num_sms(),
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+                     const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages, uint8_t *v_pages,
+                     float *k_scale, float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                     int num_pages, int32_t *kv_len, int32_t *slot_mapping, int32_t *status, eagle_stream_t stream) {
+  if (!k_tree || !v_tree || !accept_len || !path_nodes || !k_pages || !v_pages || !k_scale || !v_scale ||
+      !block_table || !kv_len)
+    return EAGLE_ERR_INVALID;
+  if (!valid_dtype(dtype) || B < 1 || n < 1 || n > 4096 || Hkv < 1 || dh < 16 || dh % 16 || dh > 512 || D < 1 || D > 64)
+    return EAGLE_ERR_INVALID;
+  if (!valid_slots(max_pages, page_size, num_pages)) return EAGLE_ERR_INVALID;
+  if (Hkv > 32767 || B > 65535) return EAGLE_ERR_UNSUPPORTED;
+  if (!aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_pages) || !aligned16(v_pages))
+    return EAGLE_ERR_INVALID;
+  return from_cuda(launch_kv8_commit(k_tree, v_tree, dtype, B, n, Hkv, dh, accept_len, path_nodes, D, k_pages,
+                                     v_pages, k_scale, v_scale, block_table, max_pages, page_size, num_pages, kv_len,
+                                     slot_mapping, status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t eagle_tree_attn_kv8_workspace_size(int dtype, int B, int n, int Hq, int Hkv, int dh, int max_pages,
+                                          int page_size) {
+  if (dtype != EAGLE_BF16 || B < 1 || n < 1 || n > 4096 || Hq < 1 || Hkv < 1 || Hq % Hkv || (dh != 64 && dh != 128) ||
+      !valid_pages(max_pages, page_size, 1))
+    return 0;
+  return attn_kv8_workspace_bytes(B, n, Hq, Hkv, dh, max_pages * page_size, current_num_sms());
+}
+
+int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
+                        const float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                        int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
+                        const uint64_t *mask, int dtype, int B, int n, int Hq, int Hkv, int dh, float scale,
+                        void *out, float *lse, int32_t *status, void *workspace, size_t workspace_bytes,
+                        eagle_stream_t stream) {
+  if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !kv_len || !k_tree || !v_tree || !mask ||
+      !out)
+    return EAGLE_ERR_INVALID;
+  if (!valid_dtype(dtype) || B < 1 || n < 1 || n > 4096 || Hq < 1 || Hkv < 1 || Hq % Hkv || !(scale > 0.f) ||
+      !valid_pages(max_pages, page_size, num_pages))
+    return EAGLE_ERR_INVALID;
+  if (dtype != EAGLE_BF16 || (dh != 64 && dh != 128)) return EAGLE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * Hkv > 65535 || static_cast<int64_t>(num_pages) * Hkv > INT32_MAX)
+    return EAGLE_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_tree) || !aligned16(v_tree) ||
+      !aligned16(out))
+    return EAGLE_ERR_INVALID;
+  const int sms = current_num_sms();
+  const size_t need = attn_kv8_workspace_bytes(B, n, Hq, Hkv, dh, max_pages * page_size, sms);
+  if (workspace_bytes < need || (need && !workspace)) return EAGLE_ERR_WORKSPACE;
+  return from_cuda(launch_tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, max_pages, page_size,
+                                        num_pages, kv_len, k_tree, v_tree, mask, B, n, Hq, Hkv, dh, scale, out, lse,
+                                        workspace, status, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

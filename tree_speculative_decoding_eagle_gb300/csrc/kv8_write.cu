@@ -1,0 +1,298 @@
+// Keys and values into the 8-bit paged cache.
+//
+// A page's rows of one head share the scale 2^e, the least with
+// max |x| <= 448 * 2^e over every row written to the page so far.  Work is cut
+// into runs: neighbouring tokens that land in one page.  A run of a head is
+// one team's work: the largest magnitude of its rows, the exponent (joined
+// with the page's when earlier rows stay), the rows divided by 2^e and rounded
+// once to e4m3; when the exponent grew, the page's earlier rows are re-encoded
+// at the new one.  Two runs never share a page, so nothing is atomic and the
+// result does not depend on an order.
+//
+// What bounds it: HBM for prompts (2 or 4 bytes read, 1 written an element),
+// latency for single tokens.
+#include "kv8.cuh"
+#include "sm100.cuh"
+
+namespace eagle {
+
+using namespace sm100;
+
+constexpr int kWriteWarps = 8;
+
+// A team's barrier: its warps are neighbours in the CTA.
+__device__ __forceinline__ void team_sync(int team, int warps) {
+  if (warps == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
+}
+
+// 16 elements of a row as floats.
+template <typename T> __device__ __forceinline__ void load16(const T *p, float (&x)[16]);
+template <> __device__ __forceinline__ void load16<float>(const float *p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = ld_stream16(p + 4 * i);
+    x[4 * i] = __uint_as_float(v.x); x[4 * i + 1] = __uint_as_float(v.y);
+    x[4 * i + 2] = __uint_as_float(v.z); x[4 * i + 3] = __uint_as_float(v.w);
+  }
+}
+template <> __device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = ld_stream16(p + 8 * i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[8 * i + 2 * j] = bf16_lo(w[j]);
+      x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+    }
+  }
+}
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// One run: rows 0..count-1 (row_of gives their source) into rows
+// first..first+count-1 of a page of one head.  `red` is the team's shared
+// scratch (one float a warp).  Called by every thread of the team.
+template <typename T, typename RowOf>
+__device__ __forceinline__ void write_run(RowOf row_of, int count, uint8_t *page, float *scale, int first, int dh,
+                                          int team, int warps, int tw, float *red, int32_t *status) {
+  const int lane = threadIdx.x & 31, tt = tw * 32 + lane, nt = warps * 32;
+  const int cpr = dh / 16;  // 16-element chunks a row
+  float amax = 0.f;
+  bool odd = false;
+  for (int c = tt; c < count * cpr; c += nt) {
+    float x[16];
+    load16<T>(row_of(c / cpr) + (c % cpr) * 16, x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool fin = is_finite(x[i]);
+      odd |= !fin;
+      amax = fmaxf(amax, fin ? fabsf(x[i]) : 0.f);
+    }
+  }
+  amax = warp_max(amax);
+  if (warps > 1) {
+    if (lane == 0) red[tw] = amax;
+    team_sync(team, warps);
+    for (int w = 0; w < warps; ++w) amax = fmaxf(amax, red[w]);
+  }
+  int e = block_exponent(amax), e_old = e;
+  if (first > 0) {
+    e_old = scale_exponent(*scale);
+    e = max(e, e_old);
+  }
+  team_sync(team, warps);  // every thread has the page's scale (and red) before it changes
+  if (tt == 0) *scale = exponent_scale(e);
+  if (odd || amax > 448.f * exponent_scale(kScaleMax)) report(status, EAGLE_ERR_INVALID);
+  const float inv = exponent_scale(-e);
+  for (int c = tt; c < count * cpr; c += nt) {
+    float x[16];
+    load16<T>(row_of(c / cpr) + (c % cpr) * 16, x);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = is_finite(x[4 * i + j]) ? x[4 * i + j] * inv : __uint_as_float(0x7fffffffu);
+      w[i] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
+    }
+    *reinterpret_cast<uint4 *>(page + static_cast<int64_t>(first + c / cpr) * dh + (c % cpr) * 16) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (e > e_old) {  // the page's earlier rows at the new scale (rare: a new largest magnitude)
+    const float f = exp2f(static_cast<float>(e_old - e));
+    for (int c = tt; c < first * cpr; c += nt) {
+      uint4 *p = reinterpret_cast<uint4 *>(page) + c;
+      uint4 v = *p;
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = e4m3_to_half2(w[i] & 0xffffu), b = e4m3_to_half2(w[i] >> 16);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+        w[i] = e4m3_pair(x.x * f, x.y * f) | (e4m3_pair(y.x * f, y.y * f) << 16);
+      }
+      *p = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+struct AppendArgs {
+  const void *k, *v;
+  int64_t token_stride, head_stride;
+  const int32_t *slot_map;
+  uint8_t *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+  int T, Hkv, dh, log_page, num_pages;
+  int block;  // tokens a CTA looks after (those whose run begins there)
+  int warps;  // warps a team
+  int32_t *status;
+};
+
+// grid (token blocks, Hkv, K or V)
+template <typename T>
+__global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(AppendArgs a) {
+  __shared__ float red[kWriteWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / a.warps, tw = warp % a.warps, teams = kWriteWarps / a.warps;
+  const int g = blockIdx.y, t0 = blockIdx.x * a.block, t1 = min(a.T, t0 + a.block);
+  const bool is_v = blockIdx.z != 0;
+  const T *src = reinterpret_cast<const T *>(is_v ? a.v : a.k) + g * a.head_stride;
+  uint8_t *pages = is_v ? a.v_pages : a.k_pages;
+  float *scales = is_v ? a.v_scale : a.k_scale;
+  const int P = 1 << a.log_page;
+  pdl_wait();
+  pdl_trigger();
+  const auto page_of = [&](int slot) {  // -1 for a token that is skipped
+    if (slot < 0) return -1;
+    const int page = slot >> a.log_page;
+    return page < a.num_pages ? page : -1;
+  };
+  int seen = 0;  // leaders before this 32-token piece
+  for (int p0 = t0; p0 < t1; p0 += 32) {
+    const int t = p0 + lane;
+    const int slot = t < t1 ? a.slot_map[t] : -1;
+    const int page = page_of(slot);
+    if (slot >= 0 && page < 0 && g == 0 && !is_v && warp == 0) report(a.status, EAGLE_ERR_INVALID);
+    const int before = t < t1 && t > 0 ? page_of(a.slot_map[t - 1]) : -1;
+    uint32_t lead = __ballot_sync(0xffffffffu, page >= 0 && page != before);
+    while (lead) {  // the same in every warp
+      const int l = __ffs(lead) - 1;
+      lead &= lead - 1;
+      if (seen++ % teams != team) continue;
+      const int s0 = __shfl_sync(0xffffffffu, slot, l), pg = s0 >> a.log_page, first = s0 & (P - 1);
+      // the run: neighbours with the next slots, within the page
+      int count = 1;
+      for (;;) {
+        const int u = p0 + l + count + lane;
+        const int su = u < a.T ? a.slot_map[u] : -1;
+        const bool next = su == s0 + count + lane && (su >> a.log_page) == pg;
+        const uint32_t stop = __ballot_sync(0xffffffffu, !next);
+        if (stop == 0) { count += 32; continue; }
+        const int o = __ffs(stop) - 1;
+        count += o;
+        if (lane == o && su >= 0 && (su >> a.log_page) == pg) report(a.status, EAGLE_ERR_INVALID);
+        break;
+      }
+      const int64_t at = static_cast<int64_t>(pg) * a.Hkv + g;
+      const T *row0 = src + static_cast<int64_t>(p0 + l) * a.token_stride;
+      write_run<T>([&](int r) { return row0 + r * a.token_stride; }, count, pages + (at << a.log_page) * a.dh,
+                   scales + at, first, a.dh, team, a.warps, tw, red + team * a.warps, a.status);
+    }
+  }
+}
+
+struct Commit8Args {
+  const void *k_tree, *v_tree;
+  int B, n, Hkv, dh, D, log_page, max_pages, num_pages;
+  const int32_t *accept_len, *path_nodes;
+  uint8_t *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+  const int32_t *block_table;
+  int32_t *kv_len, *slot_mapping, *status;
+};
+
+// One cluster of CTAs per sequence, a warp per (head, K or V): kv_len, which is
+// updated in place, is written after the cluster barrier that every CTA
+// reaches with its reads of it done.
+template <typename T>
+__global__ void __launch_bounds__(kWriteWarps * 32) kv8_commit_kernel(Commit8Args a) {
+  __shared__ int s_ok, s_path[65], s_page[8];
+  const int b = blockIdx.y, rank = blockIdx.x, ctas = gridDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = 1 << a.log_page;
+  pdl_wait();
+  const int L = a.kv_len[b], acc = a.accept_len[b];
+  if (warp == 0) {
+    bool ok = acc >= 0 && acc <= a.D && acc <= 64 && L >= 1 &&
+              static_cast<int64_t>(L) + acc <= (static_cast<int64_t>(a.max_pages) << a.log_page);
+    if (ok) {
+      for (int p = 1 + lane; p <= acc; p += 32) {
+        const int node = a.path_nodes[static_cast<int64_t>(b) * (a.D + 1) + p];
+        s_path[p] = node;
+        if (node < 1 || node >= a.n) ok = false;
+      }
+      // at most 64 rows in pages of at least 16: five pages
+      const int lp = (L >> a.log_page) + lane;
+      if (acc > 0 && lp <= (L + acc - 1) >> a.log_page) {
+        const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + lp];
+        s_page[lane] = page;
+        if (page < 0 || page >= a.num_pages) ok = false;
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) {
+      s_ok = ok;
+      if (!ok && rank == 0) report(a.status, EAGLE_ERR_INVALID);
+    }
+  }
+  __syncthreads();
+  if (ctas > 1) {  // every CTA has read kv_len
+    cluster_arrive_release();
+    cluster_wait();
+  }
+  pdl_trigger();
+  if (!s_ok) return;
+  if (rank == 0 && tid == 0) a.kv_len[b] = L + acc;
+  for (int u = rank * kWriteWarps + warp; u < 2 * a.Hkv; u += ctas * kWriteWarps) {
+    const int g = u >> 1;
+    const bool is_v = u & 1;
+    const T *src = reinterpret_cast<const T *>(is_v ? a.v_tree : a.k_tree) +
+                   (static_cast<int64_t>(b) * a.Hkv + g) * a.n * a.dh;
+    for (int p = 1, lp = 0; p <= acc; ++lp) {
+      const int first = (L + p - 1) & (P - 1), count = min(acc - p + 1, P - first);
+      const int64_t at = static_cast<int64_t>(s_page[lp]) * a.Hkv + g;
+      const int p0 = p;
+      write_run<T>([&](int r) { return src + static_cast<int64_t>(s_path[p0 + r]) * a.dh; }, count,
+                   (is_v ? a.v_pages : a.k_pages) + (at << a.log_page) * a.dh, (is_v ? a.v_scale : a.k_scale) + at,
+                   first, a.dh, 0, 1, 0, nullptr, a.status);
+      p += count;
+    }
+  }
+  if (a.slot_mapping) {
+    for (int i = rank * kWriteWarps * 32 + tid; i < a.n; i += ctas * kWriteWarps * 32) {
+      int slot = i == 0 ? L - 1 : -1;
+      for (int p = 1; p <= acc; ++p)
+        if (s_path[p] == i) slot = L + p - 1;
+      a.slot_mapping[static_cast<int64_t>(b) * a.n + i] = slot;
+    }
+  }
+}
+
+static int log2_page(int p) {
+  int l = 0;
+  while ((1 << l) < p) ++l;
+  return l;
+}
+
+cudaError_t launch_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv, int dh, int64_t token_stride,
+                              int64_t head_stride, const int32_t *slot_map, uint8_t *k_pages, uint8_t *v_pages,
+                              float *k_scale, float *v_scale, int page_size, int num_pages, int32_t *status,
+                              int num_sms, cudaStream_t st) {
+  AppendArgs a = {k, v, token_stride, head_stride, slot_map, k_pages, v_pages, k_scale, v_scale,
+                  T, Hkv, dh, log2_page(page_size), num_pages, 0, 0, status};
+  // a team of a warp for every 16 rows of a page
+  a.warps = page_size >= 128 ? 8 : page_size / 16;
+  a.block = page_size < 256 ? page_size : 256;
+  while (a.block > 4 && static_cast<int64_t>((T + a.block - 1) / a.block) * Hkv * 2 < 4ll * num_sms) a.block /= 2;
+  const dim3 grid((T + a.block - 1) / a.block, Hkv, 2);
+  return dtype == EAGLE_BF16 ? launch_chained(kv8_append_kernel<__nv_bfloat16>, grid, dim3(kWriteWarps * 32), 0, st, a)
+                             : launch_chained(kv8_append_kernel<float>, grid, dim3(kWriteWarps * 32), 0, st, a);
+}
+
+cudaError_t launch_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+                              const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages,
+                              uint8_t *v_pages, float *k_scale, float *v_scale, const int32_t *block_table,
+                              int max_pages, int page_size, int num_pages, int32_t *kv_len, int32_t *slot_mapping,
+                              int32_t *status, cudaStream_t st) {
+  Commit8Args a = {k_tree, v_tree, B, n, Hkv, dh, D, log2_page(page_size), max_pages, num_pages, accept_len,
+                   path_nodes, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, slot_mapping, status};
+  int ctas = 1;  // a warp for each (head, K or V), eight CTAs at most
+  while (ctas < 8 && ctas * kWriteWarps < 2 * Hkv) ctas *= 2;
+  const dim3 grid(ctas, B);
+  return dtype == EAGLE_BF16
+             ? launch_chained_cluster(kv8_commit_kernel<__nv_bfloat16>, grid, dim3(kWriteWarps * 32), 0, st, ctas, a)
+             : launch_chained_cluster(kv8_commit_kernel<float>, grid, dim3(kWriteWarps * 32), 0, st, ctas, a);
+}
+
+}  // namespace eagle
