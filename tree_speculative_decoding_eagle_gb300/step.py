@@ -55,6 +55,13 @@ class TreeStep:
         tree_attn(q, k_cache, v_cache, kv_len, k_tree, v_tree, self.tree["mask"], scale,
                   self.attn_out, self.lse, self.ws_attn, self.status)
 
+    def attend_kv8(self, cache, layer, q, k_tree, v_tree, scale=None):
+        """attend() over one layer of a KV8Cache (cache.py): the prefix in
+        e4m3 pages.  Returns (out, lse)."""
+        if self.attn_out is None or self.attn_out.shape != q.shape or self.attn_out.dtype != q.dtype:
+            self.attn_out = torch.empty_like(q)
+        return cache.attend(layer, q, k_tree, v_tree, self.tree["mask"], scale, self.attn_out, self.lse)
+
     def verify(self, target, uniforms=None):
         verify(target, self.tree["tok"], self.tree["parent"], self.D, self.mode, self.temperature,
                uniforms, self.accept_len, self.path_nodes, self.out_tokens, self.status,
