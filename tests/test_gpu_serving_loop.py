@@ -108,8 +108,8 @@ def one_step(cache, mirror, step, g, freqs):
                 p = np.exp(s - s.max(1, keepdims=True))
                 ref = p @ W[h // (Hq // Hkv)] / p.sum(1, keepdims=True)
                 A = p @ np.abs(W[h // (Hq // Hkv)]) / p.sum(1, keepdims=True)
-                # bf16's rounding, the weights' 11 bits, scores below 2^5 of 64 products in fp32, twice
-                tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -8) + (2.0 ** -12 + 2 * 64 * 2.0 ** -23 * 2 ** 5) * A
+                # bf16's rounding, the weights' f16 (half a step is 2^-11), scores below 2^5 of 64 products in fp32, twice
+                tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -8) + (2.0 ** -11 + 2 * 64 * 2.0 ** -23 * 2 ** 5) * A
                 assert (np.abs(f64(out[b, :, h]) - ref) <= tol).all()
     # targets that follow the draft, so that some nodes are accepted
     row = step.tree["row"].cpu()

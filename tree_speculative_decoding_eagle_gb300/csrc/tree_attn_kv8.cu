@@ -1,105 +1,843 @@
 // Stage 3 over the 8-bit paged cache: tree-masked attention whose prefix keys
 // and values are e4m3 numbers with a power-of-two scale for each page and head.
 //
-// One warp per (sequence, node, query head): the lanes share the head's
-// columns, keys come one at a time, the softmax is the running one (maximum,
-// sum, rescaled accumulator) in float32.
+// The mathematics.  Everything runs in f16 on the tensor cores, and exactly: an
+// e4m3 number is an f16 number, and a bf16 row (queries, tree keys and values)
+// becomes f16 after division by a power of two of its own.  The powers of two
+// never touch the tiles; they go into the softmax's float32 arithmetic.  With
+// q = 2^a q', k = 2^ke k', v = 2^ve v' (ke, ve of a group of 16 keys, which no
+// page splits):
+//   s  = (scale log2e 2^(a+ke)) <q', k'>           score, base 2
+//   P' = 2^(s + ve - m + 6),  m >= max(s + ve) - 8     in f16
+//   O  = sum P' v',  l = sum_groups 2^-ve sum P',  out = O / l,
+//   lse = ln 2 (m - 6 + log2 l)
+// so P' stays below 2^14 and is rounded to 11 bits (bf16 would leave 8), down
+// to 2^-20 of the row's largest; smaller ones are off by up to 2^-31 of it
+// (f16's subnormals).  Neither K nor V is rounded at all.
+//
+// One CTA per (sequence b, KV head g, group of MT 128-row M-tiles, KV split);
+// query rows are (node, head-in-group) pairs, key tiles hold NK keys, first the
+// prefix, then the tree nodes masked with the ancestor bits.  Roles:
+//   * producer warp: page numbers and scales two batches of 32 groups ahead, K/V
+//     bytes by TMA into a ring of S8 staging buffers;
+//   * four converter warps: staging bytes (tree tiles: bf16 from global memory)
+//     to f16 in a ring of SF stages, in the 128-byte swizzle the MMAs read;
+//     rows past the prefix's end become zeros;
+//   * MMA thread and one softmax warpgroup per M-tile as in tree_attn_tc.cu:
+//     S = Q K^T from shared memory, P from tensor memory.
+// KV split over up to 8 CTAs and the merge of their results as there too.
+// Every wait is bounded; a timeout raises EAGLE_ERR_TIMEOUT in the status
+// word and the CTA drains its copies and MMAs, frees tensor memory and exits.
 #include "kv8.cuh"
+#include "sm100.cuh"
+#include "tmap.cuh"
 
 namespace eagle {
 
+using namespace sm100;
+
+constexpr int kMaxSplits8 = 8;
+constexpr float kBias = 6.f;      // P' = 2^(kBias + ...)
+constexpr int kExpSlots = 8;      // tiles whose exponents are held: more than S8 + SF
+
 struct Kv8Args {
   const __nv_bfloat16 *q, *k_tree, *v_tree;
-  const uint8_t *k_pages, *v_pages;
   const float *k_scale, *v_scale;
   const int32_t *block_table, *kv_len;
   const uint64_t *mask;
-  int B, n, Hq, Hkv, G, W, log_page, max_pages, num_pages;
-  float scale_log2;
+  int B, n, Hq, Hkv, G, W, S;
+  int page_size, log_page, page_box, max_pages, num_pages;
+  float scale_log2;  // softmax scale times log2(e)
   __nv_bfloat16 *out;
   float *lse;
   int32_t *status;
+  // KV split (S > 1): one workspace slot per CTA, [slot_rows][DH] fp32 O rows
+  // then [slot_rows] (m, l) pairs, the slots of a (b, g, M-group) consecutive
+  float *part;
+  int slot_rows;
 };
 
-template <int DH>
-__global__ void __launch_bounds__(128) tree_attn_kv8_row_kernel(Kv8Args a) {
-  constexpr int C = DH / 32;  // columns a lane
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  pdl_wait();
-  if (row >= static_cast<int64_t>(a.B) * a.n * a.Hq) return;
-  const int h = static_cast<int>(row % a.Hq), i = static_cast<int>(row / a.Hq % a.n);
-  const int b = static_cast<int>(row / a.Hq / a.n), g = h / a.G;
-  const int P = 1 << a.log_page;
-  const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
-  float q[C], o[C];
-  for (int c = 0; c < C; ++c) {
-    q[c] = __bfloat162float(a.q[row * DH + lane * C + c]) * a.scale_log2;
-    o[c] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const auto take = [&](const float (&k)[C], const float (&v)[C]) {
-    float s = 0.f;
-    for (int c = 0; c < C; ++c) s = fmaf(q[c], k[c], s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), alpha = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * alpha + p;
-    for (int c = 0; c < C; ++c) o[c] = fmaf(p, v[c], o[c] * alpha);
-    m = mn;
-  };
-  for (int p0 = 0; p0 < L; p0 += P) {
-    int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + (p0 >> a.log_page)];
-    if (page < 0 || page >= a.num_pages) {
-      report(a.status, EAGLE_ERR_INVALID);
-      page = 0;
-    }
-    const int64_t at = static_cast<int64_t>(page) * a.Hkv + g;
-    const float ks = exponent_scale(scale_exponent(a.k_scale[at])), vs = exponent_scale(scale_exponent(a.v_scale[at]));
-    const int64_t base = (at << a.log_page) * DH + lane * C;
-    for (int r = 0; r < min(P, L - p0); ++r) {
-      float k[C], v[C];
-      for (int c = 0; c < C; ++c) {
-        const uint32_t kc = e4m3_to_half2(a.k_pages[base + static_cast<int64_t>(r) * DH + c]);
-        const uint32_t vc = e4m3_to_half2(a.v_pages[base + static_cast<int64_t>(r) * DH + c]);
-        k[c] = __low2float(*reinterpret_cast<const __half2 *>(&kc)) * ks;
-        v[c] = __low2float(*reinterpret_cast<const __half2 *>(&vc)) * vs;
-      }
-      take(k, v);
-    }
-  }
-  const uint64_t *mrow = a.mask + (static_cast<int64_t>(b) * a.n + i) * a.W;
-  for (int j = 0; j < a.n; ++j) {
-    if (!((mrow[j >> 6] >> (j & 63)) & 1ull)) continue;
-    const int64_t at = ((static_cast<int64_t>(b) * a.Hkv + g) * a.n + j) * DH + lane * C;
-    float k[C], v[C];
-    for (int c = 0; c < C; ++c) {
-      k[c] = __bfloat162float(a.k_tree[at + c]);
-      v[c] = __bfloat162float(a.v_tree[at + c]);
-    }
-    take(k, v);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int c = 0; c < C; ++c) a.out[row * DH + lane * C + c] = __float2bfloat16(o[c] * inv);
-  if (a.lse && lane == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+// QR: query rows held per M-tile region (64 when there are at most 64: the
+// 128-row MMAs then read rows 64-127 from what follows, and those rows' results
+// are never used).  OCC: CTAs per SM.
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC>
+struct Kv8Shape {
+  static constexpr int kRegions = DH / 64;
+  static constexpr int kQRegionBytes = QR * 128;
+  static constexpr int kQBytes = MT * kRegions * kQRegionBytes;
+  static constexpr int kTileBytes = kRegions * NK * 128;  // one f16 K (or V) tile
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kByteTile = NK * DH;               // one e4m3 K (or V) tile
+  static constexpr int kStagingOff = kQBytes + SF * kStageBytes;
+  static constexpr int kBarOff = kStagingOff + S8 * 2 * kByteTile;
+  static constexpr int kGroups = NK / 16;
+  static constexpr int kNumBars = 2 * S8 + 2 * SF + 4 * MT + 1;
+  // barriers, tensor-memory slot and abort flag, exponents of tiles, of query rows
+  static constexpr int kExpOff = kNumBars * 8 + 8;
+  static constexpr int kBarBytes = kExpOff + kExpSlots * 2 * kGroups + MT * QR;
+  // The barriers sit in the gap before the 1 KB-aligned buffers when it holds
+  // them, else after the buffers.
+  static constexpr int kSmem = kBarOff + (1008 > 2 * kBarBytes - 16 ? 1008 : 2 * kBarBytes - 16);
+  static constexpr int kThreads = (MT + 2) * 128;
+  static constexpr int kColS = 0;                         // S_t at t*NK
+  static constexpr int kColP = MT * NK;                   // P_t at kColP + t*NK/2
+  static constexpr int kColO = MT * NK + MT * NK / 2;     // O_t at kColO + t*DH
+  static constexpr int kCols = kColO + MT * DH;
+  static constexpr int kTmemCols = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
+  // Registers: what a thread is launched with, and the warpgroups' shares of
+  // it (softmax, converters, producer and MMA); they add up to the launch's.
+  static constexpr int kLaunchRegs = 65536 / (kThreads * OCC) / 8 * 8;
+  static constexpr bool kShareRegs = kLaunchRegs < 160;
+  static constexpr int kRegsOther = MT == 1 ? 32 : 40;
+  static constexpr int kRegsConvert = MT == 1 ? 56 : 72;
+  static constexpr int kRegsSoftmax = ((MT + 2) * kLaunchRegs - kRegsOther - kRegsConvert) / MT / 8 * 8;
+  static_assert(QR == 128 || (QR == 64 && MT == 1), "64-row regions with one M-tile only");
+  static_assert(S8 + SF < kExpSlots, "exponents outlive their tile");
+  static_assert(kCols <= 512 && kTmemCols * OCC <= 512, "tensor memory budget");
+  static_assert(kSmem <= 232448 && OCC * (kSmem + 1024) <= 233472, "shared memory budget");
+  static_assert(MT * kRegsSoftmax + kRegsConvert + kRegsOther <= (MT + 2) * kLaunchRegs, "register budget");
+  // split: fp32 O rows in the f16 stages, (m, l) in Q's buffer
+  static_assert(MT * 128 * DH * 4 <= SF * kStageBytes, "partial O fits the stage buffers");
+  static_assert(MT * 128 * 8 <= kQBytes, "(m, l) fit the Q buffer");
+};
+
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// kind::f16 instruction descriptor with f16 A and B, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-size_t attn_kv8_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+// 2^e in float32 for any int e that a sum of exponents can give, kept away
+// from 0 and infinity (0 * inf must not arise from finite inputs).
+__device__ __forceinline__ float pow2_clamped(int e) { return exponent_scale(min(max(e, -120), 120)); }
+
+// The exponent e with amax / 2^e in [2^8, 2^9), where an e4m3 block's numbers
+// end too: a bf16 number keeps its 8 bits in f16 down to 2^-25 of amax.
+__device__ __forceinline__ int half_exponent(float amax) {
+  if (amax == 0.f) return 0;
+  return max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8, -100);
+}
+__device__ __forceinline__ uint32_t bf16x2_to_half2(uint32_t w, float f) {
+  const __half2 h = __floats2half2_rn(bf16_lo(w) * f, bf16_hi(w) * f);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Largest magnitude of eight packed bf16 numbers.
+__device__ __forceinline__ float amax8(const uint4 &v) {
+  const uint4 a = make_uint4(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+  return vec_max<__nv_bfloat16>(a);
+}
+
+// out and lse of row rr, columns 4c..4c+3, of a (b, g, M-group) from its S
+// slots: out = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m).
+template <int DH>
+__device__ __forceinline__ void kv8_merge_item(const Kv8Args &a, int bg, int mg, int MT, int rr, int c) {
+  constexpr int NV = DH / 4;
+  const int64_t slot_floats = static_cast<int64_t>(a.slot_rows) * (DH + 2);
+  const float *slots = a.part + (static_cast<int64_t>(bg) * gridDim.y + mg) * a.S * slot_floats;
+  float2 ml[kMaxSplits8];
+  float4 po[kMaxSplits8];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits8; ++s) {
+    if (s < a.S) {
+      ml[s] = __ldcg(reinterpret_cast<const float2 *>(slots + s * slot_floats + static_cast<int64_t>(a.slot_rows) * DH) + rr);
+      po[s] = __ldcg(reinterpret_cast<const float4 *>(slots + s * slot_floats) + rr * NV + c);
+    } else {
+      ml[s] = make_float2(-INFINITY, 0.f);
+      po[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  float M = -INFINITY;
+#pragma unroll
+  for (int s = 0; s < kMaxSplits8; ++s) M = fmaxf(M, ml[s].x);
+  float Ls = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int s = 0; s < kMaxSplits8; ++s) {
+    const float w = ml[s].x > -INFINITY ? ex2_approx(ml[s].x - M) : 0.f;
+    Ls = fmaf(w, ml[s].y, Ls);
+    // a split without any key holds no O (tensor memory it never wrote)
+    if (w > 0.f) {
+      o.x = fmaf(w, po[s].x, o.x); o.y = fmaf(w, po[s].y, o.y);
+      o.z = fmaf(w, po[s].z, o.z); o.w = fmaf(w, po[s].w, o.w);
+    }
+  }
+  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  const int rho = mg * MT * 128 + rr, i = rho / a.G, h = (bg % a.Hkv) * a.G + rho % a.G;
+  const int64_t orow = (static_cast<int64_t>(bg / a.Hkv) * a.n + i) * a.Hq + h;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  uint2 packed;
+  packed.x = *reinterpret_cast<const uint32_t *>(&lo);
+  packed.y = *reinterpret_cast<const uint32_t *>(&hi);
+  reinterpret_cast<uint2 *>(a.out + orow * DH)[c] = packed;
+  if (c == 0 && a.lse) a.lse[orow] = Ls > 0.f ? (M - kBias + log2f(Ls)) * kLn2 : -INFINITY;
+}
+
+// MERGE: 0 the grid does not split the KV range; 1 the S splits of an item are
+// one cluster and merge in this kernel; 2 tree_attn_kv8_merge_kernel merges.
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, int MERGE>
+__global__ void __launch_bounds__((MT + 2) * 128, OCC)
+    tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, Kv8Args a) {
+  using Sh = Kv8Shape<DH, MT, NK, SF, S8, QR, OCC>;
+  constexpr bool SPLIT = MERGE != 0;
+  constexpr int NH = NK / 64, GR = Sh::kGroups;
+  extern __shared__ unsigned char raw_smem[];
+  const uintptr_t raw = reinterpret_cast<uintptr_t>(raw_smem);
+  unsigned char *sm = reinterpret_cast<unsigned char *>((raw + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char *sQ = sm;
+  unsigned char *sKV = sm + Sh::kQBytes;
+  unsigned char *s8 = sm + Sh::kStagingOff;
+  unsigned char *ctl = reinterpret_cast<uintptr_t>(sm) - raw >= static_cast<uintptr_t>(Sh::kBarBytes) ? raw_smem : sm + Sh::kBarOff;
+  uint64_t *f8_full = reinterpret_cast<uint64_t *>(ctl);
+  uint64_t *f8_empty = f8_full + S8;
+  uint64_t *kv_full = f8_empty + S8;
+  uint64_t *kv_empty = kv_full + SF;
+  uint64_t *s_full = kv_empty + SF;
+  uint64_t *s_free = s_full + MT;
+  uint64_t *p_full = s_free + MT;
+  uint64_t *o_done = p_full + MT;
+  uint64_t *teardown = o_done + MT;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(teardown + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  signed char *exps = reinterpret_cast<signed char *>(ctl + Sh::kExpOff);  // [kExpSlots][K, V][GR]
+  signed char *q_exp = exps + kExpSlots * 2 * GR;                          // [MT * QR]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x, mg = blockIdx.y;
+  const int bg = blockIdx.z, b = bg / a.Hkv, g = bg % a.Hkv;
+  const int n = a.n;
+  constexpr int kConvertWarp = MT * 4, kProducerWarp = MT * 4 + 4, kMmaWarp = MT * 4 + 5;
+
+  if (tid == 0) prefetch_l2(a.kv_len + b);
+  pdl_wait();  // inputs of this step come from earlier kernels
+  const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
+  const int n_ptiles = (L + NK - 1) / NK;
+  const int tps = (n_ptiles + a.S - 1) / a.S;
+  const int p0 = min(n_ptiles, split * tps), p1 = min(n_ptiles, p0 + tps);
+  const int np = p1 - p0;
+  const int ntt = (split == a.S - 1) ? (n + NK - 1) / NK : 0;
+  const int T = np + ntt;  // key tiles of this CTA
+
+  // ---- Q to shared memory as f16, each row over a power of two of its own ----
+  const int rows_total = n * a.G;
+  constexpr int CPR = DH / 8;  // 16-byte pieces a row: 8 or 16 neighbouring lanes hold one
+  for (int idx = tid; idx < MT * QR * CPR; idx += Sh::kThreads) {
+    const int rr = idx / CPR, c = idx % CPR, t = rr / QR, r = rr % QR;
+    const int rho = (mg * MT + t) * 128 + r;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (rho < rows_total) {
+      const int i = rho / a.G, hh = rho % a.G;
+      v = *reinterpret_cast<const uint4 *>(a.q + ((static_cast<int64_t>(b) * n + i) * a.Hq + g * a.G + hh) * DH + c * 8);
+    }
+    float amax = amax8(v);
+#pragma unroll
+    for (int o = 1; o < CPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int e = half_exponent(amax);
+    const float f = pow2_clamped(-e);
+    v = make_uint4(bf16x2_to_half2(v.x, f), bf16x2_to_half2(v.y, f), bf16x2_to_half2(v.z, f), bf16x2_to_half2(v.w, f));
+    *reinterpret_cast<uint4 *>(sQ + (t * Sh::kRegions + c / 8) * Sh::kQRegionBytes + sw128_offset(r, c % 8)) = v;
+    if (c == 0) q_exp[rr] = static_cast<signed char>(e);
+  }
+  fence_async_smem();
+  if (tid == 0) {
+    for (int i = 0; i < S8; ++i) {
+      mbar_init(&f8_full[i], 1);
+      mbar_init(&f8_empty[i], 4);
+    }
+    for (int i = 0; i < SF; ++i) {
+      mbar_init(&kv_full[i], 4);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int t = 0; t < MT; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&s_free[t], 4);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_done[t], 1);
+    }
+    mbar_init(teardown, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, Sh::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  int issued = 0;  // producer: tiles requested
+  bool part_have = false;
+  float part_m = -INFINITY, part_l = 0.f;
+
+  if (warp >= kProducerWarp) {
+    if constexpr (Sh::kShareRegs) regs_dec<Sh::kRegsOther>();
+    if (warp == kProducerWarp) {
+      // -------------------------------------------------------------- producer
+      // Lane i of batch k looks after group 32k + i of this CTA's prefix keys.
+      if (lane == 0) {
+        prefetch_tmap(&k_map);
+        prefetch_tmap(&v_map);
+      }
+      constexpr int TPB = 32 / GR;  // tiles a batch
+      const int key_end = min(L, p1 * NK);
+      const auto page_at = [&](int batch) {
+        const int key = p0 * NK + (batch * 32 + lane) * 16;
+        if (key >= key_end) return 0;
+        const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + (key >> a.log_page)];
+        if (page >= 0 && page < a.num_pages) return page;
+        report(a.status, EAGLE_ERR_INVALID);  // outside the pool: read page 0
+        return 0;
+      };
+      int page = page_at(0), page_next = page_at(1);
+      float ks = a.k_scale[static_cast<int64_t>(page) * a.Hkv + g], vs = a.v_scale[static_cast<int64_t>(page) * a.Hkv + g];
+      float ks_next = 1.f, vs_next = 1.f;
+      for (int j = 0; j < np; ++j) {
+        if (j % TPB == 0) {
+          if (j) {
+            page = page_next; ks = ks_next; vs = vs_next;
+            page_next = page_at(j / TPB + 1);
+          }
+          // requested now, looked at a batch later
+          ks_next = a.k_scale[static_cast<int64_t>(page_next) * a.Hkv + g];
+          vs_next = a.v_scale[static_cast<int64_t>(page_next) * a.Hkv + g];
+        }
+        const int st = j % S8;
+        if (j >= S8 && !warp_wait(&f8_empty[st], (j / S8 - 1) & 1, abort_flag)) break;
+        const int q = lane - (j % TPB) * GR;  // this lane's group of the tile
+        const bool mine = q >= 0 && q < GR;
+        const int key0 = (p0 + j) * NK, valid = min(NK, L - key0);
+        if (mine) {
+          signed char *ex = exps + (j % kExpSlots) * 2 * GR;
+          ex[q] = static_cast<signed char>(scale_exponent(ks));
+          ex[GR + q] = static_cast<signed char>(scale_exponent(vs));
+        }
+        __syncwarp();
+        if (lane == 0)
+          mbar_arrive_expect_tx(&f8_full[st], (valid + a.page_box - 1) / a.page_box * a.page_box * DH * 2);
+        __syncwarp();
+        if (mine && q * 16 < valid && ((q * 16) & (a.page_box - 1)) == 0) {
+          unsigned char *dst = s8 + st * 2 * Sh::kByteTile + q * 16 * DH;
+          const int row = (key0 + q * 16) & (a.page_size - 1);
+          tma_load_3d(dst, &k_map, 0, row, page * a.Hkv + g, &f8_full[st]);
+          tma_load_3d(dst + Sh::kByteTile, &v_map, 0, row, page * a.Hkv + g, &f8_full[st]);
+        }
+        __syncwarp();
+        issued = j + 1;
+      }
+    } else if (warp == kMmaWarp && lane == 0) {
+      // ------------------------------------------------------------------- MMA
+      constexpr uint32_t id_s = idesc_f16(128, NK, false);
+      constexpr uint32_t id_o = idesc_f16(128, DH, true);
+      const uint64_t q_desc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
+      const uint64_t v_desc0 = sdesc_sw128(smem_u32(sKV) + Sh::kTileBytes, NK * 128, 1024);
+      auto issue_s = [&](int j, int t) {
+        const uint64_t kd = k_desc0 + static_cast<uint64_t>((j % SF) * (Sh::kStageBytes >> 4));
+        const uint64_t qd = q_desc0 + static_cast<uint64_t>(t * Sh::kRegions * (Sh::kQRegionBytes >> 4));
+#pragma unroll
+        for (int s = 0; s < DH / 16; ++s) {
+          const uint64_t qoff = static_cast<uint64_t>(((s / 4) * Sh::kQRegionBytes + (s % 4) * 32) >> 4);
+          const uint64_t koff = static_cast<uint64_t>(((s / 4) * (NK * 128) + (s % 4) * 32) >> 4);
+          mma_bf16_ss(tmem + Sh::kColS + t * NK, qd + qoff, kd + koff, id_s, s > 0);
+        }
+        mma_commit(&s_full[t]);
+      };
+      bool ok = T == 0 || mbar_wait(&kv_full[0], 0, abort_flag);
+      if (ok && T > 0) {
+        tc_fence_after();
+        for (int t = 0; t < MT; ++t) issue_s(0, t);
+      }
+      for (int j = 0; j < T && ok; ++j) {
+        const int st = j % SF;
+        const bool next = j + 1 < T;
+        if (next && !mbar_wait(&kv_full[(j + 1) % SF], ((j + 1) / SF) & 1, abort_flag)) break;
+        const uint64_t vd = v_desc0 + static_cast<uint64_t>(st * (Sh::kStageBytes >> 4));
+        for (int t = 0; t < MT && ok && next; ++t) {
+          if (!mbar_wait(&s_free[t], j & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          issue_s(j + 1, t);
+        }
+        for (int t = 0; t < MT && ok; ++t) {
+          if (!mbar_wait(&p_full[t], j & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t pcol = tmem + Sh::kColP + t * (NK / 2);
+#pragma unroll
+          for (int s = 0; s < NK / 16; ++s)
+            mma_bf16_ts(tmem + Sh::kColO + t * DH, pcol + s * 8, vd + static_cast<uint64_t>(s * (2048 >> 4)), id_o,
+                        (j > 0 || s > 0));
+          mma_commit(&o_done[t]);
+        }
+        if (ok) mma_commit(&kv_empty[st]);
+      }
+    }
+  } else if (warp >= kConvertWarp) {
+    // ------------------------------------------------------------- converters
+    // Each warp takes whole groups of 16 keys.  In a step the eight lanes of a
+    // quarter warp hold two rows' 16-byte pieces so chosen that both their loads
+    // (rows of DH bytes) and their two stores (swizzled rows of 128 bytes) touch
+    // every bank once: with DH = 128, columns 0-63 of one row and 64-127 of the
+    // other, the next quarter the complement.
+    if constexpr (Sh::kShareRegs) regs_dec<Sh::kRegsConvert>();
+    const int cw = warp - kConvertWarp, quarter = lane >> 3, l8 = lane & 7;
+    constexpr int STEPS = DH / 32;          // steps of 16 rows: 32 pieces each
+    const int cc = DH == 128 ? l8 : l8 & 3;  // this lane's piece of the row
+    const auto row_of = [&](int step) {
+      return DH == 128 ? 4 * step + 2 * (quarter >> 1) + ((l8 >> 2) ^ (quarter & 1)) : 8 * step + 2 * quarter + (l8 >> 2);
+    };
+    const auto store = [&](unsigned char *tile, int r, const uint32_t (&h)[8]) {
+      unsigned char *region = tile + (cc >> 2) * (NK * 128);
+      *reinterpret_cast<uint4 *>(region + sw128_offset(r, 2 * (cc & 3))) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4 *>(region + sw128_offset(r, 2 * (cc & 3) + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+    };
+    for (int j = 0; j < T; ++j) {
+      const int st = j % SF;
+      const bool prefix = j < np;
+      if (prefix && !warp_wait(&f8_full[j % S8], (j / S8) & 1, abort_flag)) break;
+      if (j >= SF && !warp_wait(&kv_empty[st], (j / SF - 1) & 1, abort_flag)) break;
+      unsigned char *kst = sKV + st * Sh::kStageBytes;
+      const int key0 = prefix ? (p0 + j) * NK : (j - np) * NK;
+      const int valid = min(NK, (prefix ? L : n) - key0);
+      for (int grp = cw; grp < GR; grp += 4) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          unsigned char *tile = kst + kv * Sh::kTileBytes;
+          if (prefix) {
+            const unsigned char *src = s8 + (j % S8) * 2 * Sh::kByteTile + kv * Sh::kByteTile;
+            uint4 x[STEPS];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+              const int r = grp * 16 + row_of(s);
+              x[s] = *reinterpret_cast<const uint4 *>(src + r * DH + cc * 16);
+              if (r >= valid) x[s] = make_uint4(0, 0, 0, 0);  // past the prefix: whatever the page holds
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+              const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+              uint32_t h[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                h[2 * i] = e4m3_to_half2(w[i] & 0xffffu);
+                h[2 * i + 1] = e4m3_to_half2(w[i] >> 16);
+              }
+              store(tile, grp * 16 + row_of(s), h);
+            }
+          } else {
+            // tree nodes: bf16 over the group's power of two
+            const __nv_bfloat16 *src = (kv ? a.v_tree : a.k_tree) + (static_cast<int64_t>(bg) * n + key0) * DH;
+            float amax = 0.f;
+            for (int s = 0; s < STEPS; ++s) {
+              const int r = grp * 16 + row_of(s);
+              if (r >= valid) continue;
+              const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
+              amax = fmaxf(amax, fmaxf(amax8(p[0]), amax8(p[1])));
+            }
+            const int e = half_exponent(warp_max(amax));
+            const float f = pow2_clamped(-e);
+            for (int s = 0; s < STEPS; ++s) {
+              const int r = grp * 16 + row_of(s);
+              uint4 x = make_uint4(0, 0, 0, 0), y = x;
+              if (r < valid) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
+                x = p[0];
+                y = p[1];
+              }
+              const uint32_t h[8] = {bf16x2_to_half2(x.x, f), bf16x2_to_half2(x.y, f), bf16x2_to_half2(x.z, f),
+                                     bf16x2_to_half2(x.w, f), bf16x2_to_half2(y.x, f), bf16x2_to_half2(y.y, f),
+                                     bf16x2_to_half2(y.z, f), bf16x2_to_half2(y.w, f)};
+              store(tile, r, h);
+            }
+            if (lane == 0) exps[(j % kExpSlots) * 2 * GR + kv * GR + grp] = static_cast<signed char>(e);
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&kv_full[st]);
+        if (prefix) mbar_arrive(&f8_empty[j % S8]);
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------- softmax
+    if constexpr (Sh::kShareRegs) regs_inc<Sh::kRegsSoftmax>();
+    const int t = warp >> 2, qtr = warp & 3;
+    const int r = qtr * 32 + lane;
+    const int rho = (mg * MT + t) * 128 + r;
+    const bool row_ok = rho < rows_total;
+    const bool warp_live = (mg * MT + t) * 128 + qtr * 32 < rows_total;  // warp-uniform
+    const int i = row_ok ? rho / a.G : 0;
+    const int hh = row_ok ? rho % a.G : 0;
+    const int qe = row_ok ? q_exp[t * QR + r] : 0;
+    const uint32_t lane_base = static_cast<uint32_t>(qtr * 32) << 16;
+    const uint32_t tS = tmem + lane_base + Sh::kColS + t * NK;
+    const uint32_t tP = tmem + lane_base + Sh::kColP + t * (NK / 2);
+    const uint32_t tO = tmem + lane_base + Sh::kColO + t * DH;
+    const uint64_t *mrow = a.mask + (static_cast<int64_t>(b) * n + i) * a.W;
+    // m is the exponent base of this row's P' and O; it is raised only when the
+    // row maximum exceeds it by more than 8, so O is rescaled rarely.
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < T; ++j) {
+      if (!warp_wait(&s_full[t], j & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      const bool prefix = j < np;
+      uint64_t keep[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        if (prefix) {
+          const int valid = min(NK, L - (p0 + j) * NK) - 64 * h;
+          keep[h] = valid >= 64 ? ~0ull : (valid <= 0 ? 0ull : ((1ull << valid) - 1ull));
+        } else {
+          const int w = (j - np) * NH + h;
+          keep[h] = (row_ok && w < a.W) ? mrow[w] : 0ull;
+        }
+      }
+      bool dense = true;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) dense = dense && keep[h] == ~0ull;
+      dense = __all_sync(0xffffffffu, dense);
+      float sv[NH][64];
+      if (warp_live) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          tmem_ld32(tS + 64 * h, *reinterpret_cast<float(*)[32]>(&sv[h][0]));
+          tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<float(*)[32]>(&sv[h][32]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
+      const signed char *ex = exps + (j % kExpSlots) * 2 * GR;
+      float tmax = -INFINITY;
+      if (warp_live) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (!dense) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) sv[h][c] = ((keep[h] >> c) & 1ull) ? sv[h][c] : -INFINITY;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float x = sv[h][16 * q];
+#pragma unroll
+            for (int c = 1; c < 15; c += 2) x = fmax3(x, sv[h][16 * q + c], sv[h][16 * q + c + 1]);
+            x = fmaxf(x, sv[h][16 * q + 15]);
+            const float f = fmaxf(a.scale_log2 * pow2_clamped(qe + ex[4 * h + q]), 1.2e-38f);
+            tmax = fmaxf(tmax, fmaf(x, f, static_cast<float>(ex[GR + 4 * h + q])));
+          }
+        }
+      }
+      const bool raise = tmax > m + 8.f;
+      const float base = raise ? tmax : m;
+      const float alpha = raise ? ex2_approx(m - tmax) : 1.f;  // m = -inf gives 0
+      m = base;
+      if (j > 0) {  // P.V of the previous tile is done: P is free, O is final for it
+        if (!warp_wait(&o_done[t], (j - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+      }
+      const float nb = kBias - (base > -INFINITY ? base : 0.f);
+      float sum = 0.f;
+      if (warp_live) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float pk[16];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int grp = 4 * h + 2 * half + q;
+              const int ve = ex[GR + grp];
+              const float f = fmaxf(a.scale_log2 * pow2_clamped(qe + ex[grp]), 1.2e-38f);
+              const float off = nb + static_cast<float>(ve);
+              const uint64_t f2 = f2_pack(f, f), o2 = f2_pack(off, off);
+              uint64_t acc = f2_pack(0.f, 0.f);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const int col = 32 * half + 16 * q + 2 * c;
+                float t0, t1;
+                f2_unpack(f2_fma(f2_pack(sv[h][col], sv[h][col + 1]), f2, o2), t0, t1);
+                const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+                acc = f2_add(acc, f2_pack(e0, e1));
+                const __half2 h2 = __floats2half2_rn(e0, e1);
+                pk[8 * q + c] = *reinterpret_cast<const float *>(&h2);
+              }
+              float a0, a1;
+              f2_unpack(acc, a0, a1);
+              sum = fmaf(a0 + a1, pow2_clamped(-ve), sum);
+            }
+            tmem_st16_async(tP + 32 * h + 16 * half, pk);
+          }
+        }
+        tmem_wait_st();
+      }
+      l = fmaf(l, alpha, sum);
+      if (warp_live && j > 0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int c0 = 0; c0 < DH; c0 += 32) {
+          float o[32];
+          tmem_ld32(tO + c0, o);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] *= alpha;
+          tmem_st32(tO + c0, o);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+    if (ok && T > 0 && !warp_wait(&o_done[t], (T - 1) & 1, abort_flag)) ok = false;
+    tc_fence_after();
+    // tcgen05.ld is warp-collective: every lane executes it, rows past the last
+    // node only skip the global writes
+    const int h = g * a.G + hh;
+    const int64_t orow = (static_cast<int64_t>(b) * n + i) * a.Hq + h;
+    const bool have = ok && T > 0;
+    if constexpr (SPLIT) {
+      part_have = have;
+      part_m = m;
+      part_l = l;
+    } else {
+      const float inv = (have && l > 0.f) ? 1.f / l : 0.f;
+#pragma unroll
+      for (int c0 = 0; c0 < DH; c0 += 32) {
+        float o[32];
+        if (have) {
+          tmem_ld32(tO + c0, o);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = 0.f;
+        }
+        if (!row_ok) continue;
+        __nv_bfloat162 hv[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hv[e] = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * DH + c0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = reinterpret_cast<const uint4 *>(hv)[e];
+      }
+      if (row_ok && a.lse) a.lse[orow] = (have && l > 0.f) ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+    }
+  }
+
+  pdl_trigger();
+  // ---- teardown --------------------------------------------------------------
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Equal shares again, only now that every warp has left its role: a warp that
+  // took its registers back earlier would take them from the softmax warps'
+  // share, which would then wait for ever.
+  if constexpr (Sh::kShareRegs) {
+    if (warp < kConvertWarp) regs_dec<Sh::kLaunchRegs>();
+    else regs_inc<Sh::kLaunchRegs>();
+  }
+  if (*abort_flag) {
+    if (tid == 0) report(a.status, EAGLE_ERR_TIMEOUT);
+    volatile int never = 0;
+    if (warp == kMmaWarp && lane == 0) {
+      mma_commit(teardown);  // every MMA issued so far completes before tensor memory is released
+      mbar_wait(teardown, 0, &never, 100000000ull);
+    }
+    if (warp == kProducerWarp && lane == 0) {
+      // copies still in flight complete before shared memory is released
+      for (int j = max(0, issued - S8); j < issued; ++j) mbar_wait(&f8_full[j % S8], (j / S8) & 1, &never, 100000000ull);
+    }
+    __syncthreads();
+  }
+  const int r0 = mg * MT * 128, nr = max(0, min(rows_total, r0 + MT * 128) - r0);
+  if constexpr (SPLIT) {
+    if (warp < MT * 4) {
+      // this CTA's O rows (fp32) into the f16 stages and its (m, l) pairs into
+      // the Q buffer: every MMA and copy has completed.  Row r's 16-byte chunk c
+      // sits at chunk c ^ (r & 7), so a warp's rows store to distinct banks.
+      const int t = warp >> 2, qtr = warp & 3, rl = t * 128 + qtr * 32 + lane;
+      const uint32_t tO = tmem + (static_cast<uint32_t>(qtr * 32) << 16) + Sh::kColO + t * DH;
+      const bool have = part_have && !*abort_flag;
+      float4 *prow = reinterpret_cast<float4 *>(sKV) + rl * (DH / 4);
+#pragma unroll
+      for (int c0 = 0; c0 < DH; c0 += 32) {
+        float o[32];
+        if (__all_sync(0xffffffffu, have)) {
+          tmem_ld32(tO + c0, o);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          prow[(c0 / 4 + e) ^ (rl & 7)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      }
+      reinterpret_cast<float2 *>(sQ)[rl] = have ? make_float2(part_m, part_l) : make_float2(-INFINITY, 0.f);
+    }
+    tc_fence_before();
+    __syncthreads();
+    constexpr int NV = DH / 4;
+    const int64_t cl = static_cast<int64_t>(bg) * gridDim.y + mg;
+    float *slot = a.part + (cl * a.S + split) * static_cast<int64_t>(a.slot_rows) * (DH + 2);
+    for (int idx = tid; idx < nr * NV; idx += Sh::kThreads) {
+      const int r = idx / NV, c = idx % NV;
+      reinterpret_cast<float4 *>(slot)[idx] = reinterpret_cast<const float4 *>(sKV)[r * NV + (c ^ (r & 7))];
+    }
+    for (int r = tid; r < nr; r += Sh::kThreads)
+      reinterpret_cast<float2 *>(slot + static_cast<int64_t>(a.slot_rows) * DH)[r] = reinterpret_cast<const float2 *>(sQ)[r];
+  }
+  if (warp == kMmaWarp) tmem_dealloc(tmem, Sh::kTmemCols);
+
+  // ---- split merge across the cluster: CTA `rank` merges its share of the rows
+  // from all S slots, read from L2
+  if constexpr (MERGE == 1) {
+    cluster_arrive_release();
+    cluster_wait();
+    if (*abort_flag) return;
+    const int per = (nr + a.S - 1) / a.S;
+    const int q0 = min(nr, static_cast<int>(cluster_ctarank()) * per), q1 = min(nr, q0 + per);
+    for (int item = tid; item < (q1 - q0) * (DH / 4); item += Sh::kThreads)
+      kv8_merge_item<DH>(a, bg, mg, MT, q0 + item / (DH / 4), item % (DH / 4));
+  }
+}
+
+// The merge of a split launch of several waves: one thread per (row, 4 columns).
+template <int DH>
+__global__ void __launch_bounds__(256) tree_attn_kv8_merge_kernel(Kv8Args a, int MT) {
+  constexpr int NV = DH / 4;
+  const int mg = blockIdx.y, bg = blockIdx.z;
+  const int nr = max(0, min(a.n * a.G - mg * MT * 128, MT * 128));
+  const int item = blockIdx.x * blockDim.x + threadIdx.x;
+  pdl_wait();  // the partial results come from the attention kernel
+  if (item < nr * NV) kv8_merge_item<DH>(a, bg, mg, MT, item / NV, item % NV);
+}
+
+// ---- host side ---------------------------------------------------------------
+
+// A pool [num_pages * Hkv, page_size, dh] of bytes in boxes of page_box rows.
+// Three dimensions, so no coordinate passes 32 bits however long the pool.
+static bool make_pool_map(CUtensorMap *map, const void *base, int64_t blocks, int page_size, int dh, int page_box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(dh), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(blocks)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(dh), static_cast<cuuint64_t>(dh) * page_size};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(dh), static_cast<cuuint32_t>(page_box), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Kv8Plan {
+  int MT, NK, QR, mgroups, S, ctas_per_sm;
+  bool one_wave;
+};
+
+// M-tiles per CTA, key-tile width, and the KV split S that minimises (waves of
+// CTAs) x (key tiles per CTA + the cost of merging partial results).
+static Kv8Plan kv8_plan(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num_sms) {
+  Kv8Plan p;
+  const int G = Hq / Hkv, rows = n * G, tiles = (rows + 127) / 128;
+  p.MT = tiles <= 1 ? 1 : 2;
+  p.QR = rows <= 64 ? 64 : 128;
+  p.NK = dh == 64 && p.MT == 2 ? 128 : 64;
+  p.mgroups = (tiles + p.MT - 1) / p.MT;
+  p.ctas_per_sm = p.MT == 1 && (dh == 64 || p.QR == 64) ? 2 : 1;
+  const int64_t base = static_cast<int64_t>(B) * Hkv * p.mgroups;
+  const int64_t slots = static_cast<int64_t>(num_sms) * p.ctas_per_sm;
+  const int64_t ptiles = (static_cast<int64_t>(Lmax) + p.NK - 1) / p.NK;
+  const double split_cost = static_cast<double>(rows) * 64.0 / p.NK / 32.0 / p.mgroups;
+  p.S = 1;
+  double best = 1e30;
+  for (int S = 1; S <= kMaxSplits8 && S <= ptiles; ++S) {
+    const int64_t waves = (base * S + slots - 1) / slots;
+    const double cost = waves * (static_cast<double>((ptiles + S - 1) / S) + (S > 1 ? split_cost : 0.0));
+    if (cost < best * 0.97) {  // prefer fewer splits unless clearly better
+      best = cost;
+      p.S = S;
+    }
+  }
+  p.one_wave = base * p.S <= slots;
+  return p;
+}
+
+// Rows of a split's workspace slot, rounded up to 8.
+static int kv8_slot_rows(const Kv8Plan &p, int rows) { return min((rows + 7) / 8 * 8, p.MT * 128); }
+
+size_t attn_kv8_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num_sms) {
+  const Kv8Plan p = kv8_plan(B, n, Hq, Hkv, dh, Lmax, num_sms);
+  if (p.S <= 1) return 0;
+  return static_cast<size_t>(B) * Hkv * p.mgroups * p.S * kv8_slot_rows(p, n * (Hq / Hkv)) * (dh + 2) * sizeof(float);
+}
+
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, int MERGE>
+static cudaError_t launch_kv8_v(const CUtensorMap *maps, const Kv8Args &a, const Kv8Plan &p, cudaStream_t st) {
+  using Sh = Kv8Shape<DH, MT, NK, SF, S8, QR, OCC>;
+  const auto kernel = tree_attn_kv8_kernel<DH, MT, NK, SF, S8, QR, OCC, MERGE>;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = set_smem_limit_once(kernel, Sh::kSmem, configured);
+  if (e != cudaSuccess) return e;
+  if constexpr (Sh::kShareRegs) {
+    // the warpgroups' shares add up only if a thread is launched with these
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kernel);
+      if (e != cudaSuccess) return e;
+      regs.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) != Sh::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
+  const dim3 grid(p.S, p.mgroups, a.B * a.Hkv);
+  if constexpr (MERGE == 2) {
+    e = launch_chained(kernel, grid, dim3(Sh::kThreads), Sh::kSmem, st, maps[0], maps[1], a);
+    if (e != cudaSuccess) return e;
+    const dim3 mgrid((a.slot_rows * (DH / 4) + 255) / 256, p.mgroups, a.B * a.Hkv);
+    return launch_chained(tree_attn_kv8_merge_kernel<DH>, mgrid, dim3(256), 0, st, a, MT);
+  }
+  return launch_chained_cluster(kernel, grid, dim3(Sh::kThreads), Sh::kSmem, st, p.S, maps[0], maps[1], a);
+}
+
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC>
+static cudaError_t launch_kv8_t(const CUtensorMap *maps, const Kv8Args &a, const Kv8Plan &p, cudaStream_t st) {
+  if (p.S <= 1) return launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, 0>(maps, a, p, st);
+  return p.one_wave ? launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, 1>(maps, a, p, st)
+                    : launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, 2>(maps, a, p, st);
+}
 
 cudaError_t launch_tree_attn_kv8(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
                                  const float *v_scale, const int32_t *block_table, int max_pages, int page_size,
                                  int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
                                  const uint64_t *mask, int B, int n, int Hq, int Hkv, int dh, float scale, void *out,
-                                 float *lse, void *, int32_t *status, int, cudaStream_t st) {
-  int lp = 0;
-  while ((1 << lp) < page_size) ++lp;
-  Kv8Args a = {reinterpret_cast<const __nv_bfloat16 *>(q), reinterpret_cast<const __nv_bfloat16 *>(k_tree),
-               reinterpret_cast<const __nv_bfloat16 *>(v_tree), k_pages, v_pages, k_scale, v_scale, block_table,
-               kv_len, mask, B, n, Hq, Hkv, Hq / Hkv, (n + 63) / 64, lp, max_pages, num_pages, scale * kLog2e,
-               reinterpret_cast<__nv_bfloat16 *>(out), lse, status};
-  const int64_t rows = static_cast<int64_t>(B) * n * Hq;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
-  return dh == 64 ? launch_chained(tree_attn_kv8_row_kernel<64>, grid, dim3(128), 0, st, a)
-                  : launch_chained(tree_attn_kv8_row_kernel<128>, grid, dim3(128), 0, st, a);
+                                 float *lse, void *ws, int32_t *status, int num_sms, cudaStream_t st) {
+  const Kv8Plan p = kv8_plan(B, n, Hq, Hkv, dh, max_pages * page_size, num_sms);
+  if (p.S > 1 && !ws) return cudaErrorInvalidValue;
+  const int page_box = min(page_size, p.NK);
+  CUtensorMap maps[2];
+  const int64_t blocks = static_cast<int64_t>(num_pages) * Hkv;
+  if (!make_pool_map(&maps[0], k_pages, blocks, page_size, dh, page_box) ||
+      !make_pool_map(&maps[1], v_pages, blocks, page_size, dh, page_box))
+    return cudaErrorInvalidValue;
+  Kv8Args a;
+  a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+  a.k_tree = reinterpret_cast<const __nv_bfloat16 *>(k_tree);
+  a.v_tree = reinterpret_cast<const __nv_bfloat16 *>(v_tree);
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.block_table = block_table; a.kv_len = kv_len; a.mask = mask;
+  a.B = B; a.n = n; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.W = (n + 63) / 64; a.S = p.S;
+  a.page_size = page_size; a.page_box = page_box; a.max_pages = max_pages; a.num_pages = num_pages;
+  a.log_page = 0;
+  while ((1 << a.log_page) < page_size) ++a.log_page;
+  a.scale_log2 = scale * kLog2e;
+  a.out = reinterpret_cast<__nv_bfloat16 *>(out);
+  a.lse = lse; a.status = status;
+  a.part = p.S > 1 ? reinterpret_cast<float *>(ws) : nullptr;
+  a.slot_rows = kv8_slot_rows(p, n * a.G);
+  if (dh == 64) {
+    if (p.MT == 2) return launch_kv8_t<64, 2, 128, 3, 4, 128, 1>(maps, a, p, st);
+    return launch_kv8_t<64, 1, 64, 3, 4, 128, 2>(maps, a, p, st);
+  }
+  if (p.MT == 2) return launch_kv8_t<128, 2, 64, 4, 1, 128, 1>(maps, a, p, st);
+  return p.QR == 64 ? launch_kv8_t<128, 1, 64, 2, 2, 64, 2>(maps, a, p, st) : launch_kv8_t<128, 1, 64, 3, 4, 128, 1>(maps, a, p, st);
 }
 
 }  // namespace eagle

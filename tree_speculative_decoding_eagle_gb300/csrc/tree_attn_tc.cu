@@ -35,10 +35,9 @@
 // and tree_attn_merge_kernel merges.  The slots are read back from L2.
 // Every wait is bounded; a timeout raises EAGLE_ERR_TIMEOUT in the status
 // word and the CTA drains its copies and MMAs, frees tensor memory and exits.
-#include <mutex>
-
 #include "common.cuh"
 #include "sm100.cuh"
+#include "tmap.cuh"
 
 namespace eagle {
 
@@ -709,24 +708,6 @@ __global__ void __launch_bounds__(256) tree_attn_merge_kernel(TcArgs a, int MT) 
 }
 
 // ---- host side ---------------------------------------------------------------
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 // 2D bf16 tensor [rows, dh] viewed in boxes of 64 columns x `box_rows` rows
 // with 128-byte swizzle.
