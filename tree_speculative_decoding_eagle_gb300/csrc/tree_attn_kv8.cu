@@ -88,7 +88,7 @@ struct Kv8Shape {
   // it (softmax, converters, producer and MMA); they add up to the launch's.
   static constexpr int kLaunchRegs = 65536 / (kThreads * OCC) / 8 * 8;
   static constexpr bool kShareRegs = kLaunchRegs < 160;
-  static constexpr int kRegsOther = MT == 1 ? 32 : 40;
+  static constexpr int kRegsOther = MT == 1 ? 40 : 40;
   static constexpr int kRegsConvert = MT == 1 ? 56 : 72;
   static constexpr int kRegsSoftmax = ((MT + 2) * kLaunchRegs - kRegsOther - kRegsConvert) / MT / 8 * 8;
   static_assert(QR == 128 || (QR == 64 && MT == 1), "64-row regions with one M-tile only");
@@ -96,8 +96,8 @@ struct Kv8Shape {
   static_assert(kCols <= 512 && kTmemCols * OCC <= 512, "tensor memory budget");
   static_assert(kSmem <= 232448 && OCC * (kSmem + 1024) <= 233472, "shared memory budget");
   static_assert(MT * kRegsSoftmax + kRegsConvert + kRegsOther <= (MT + 2) * kLaunchRegs, "register budget");
-  // split: fp32 O rows in the f16 stages, (m, l) in Q's buffer
-  static_assert(MT * 128 * DH * 4 <= SF * kStageBytes, "partial O fits the stage buffers");
+  // split: fp32 O rows in the stages and the staging after them, (m, l) in Q's buffer
+  static_assert(MT * 128 * DH * 4 <= kBarOff - kQBytes, "partial O fits the stage and staging buffers");
   static_assert(MT * 128 * 8 <= kQBytes, "(m, l) fit the Q buffer");
 };
 
@@ -108,6 +108,51 @@ template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setm
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// A value the compiler knows nothing about.
+__device__ __forceinline__ uint32_t anew(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
+// D[tmem] (+)= A B^T in f16 with fp32 accumulation; operands by the low words of
+// their 128-byte-swizzle descriptors (stride between groups of eight rows 1024).
+constexpr uint32_t kDescHigh = static_cast<uint32_t>(sdesc_sw128(0, 0, 1024) >> 32);
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+// The same with A (packed f16 pairs) in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+
+// warp_wait for warps that work on afterwards: brings lane 0, which polled, back
+// together with the others (they would run what follows apart).
+__device__ __forceinline__ bool warp_wait_together(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  const bool ok = warp_wait(bar, parity, abort);
+  __syncwarp();
+  return ok;
 }
 
 // 2^e in float32 for any int e that a sum of exponents can give, kept away
@@ -306,7 +351,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
           vs_next = a.v_scale[static_cast<int64_t>(page_next) * a.Hkv + g];
         }
         const int st = j % S8;
-        if (j >= S8 && !warp_wait(&f8_empty[st], (j / S8 - 1) & 1, abort_flag)) break;
+        if (j >= S8 && !warp_wait_together(&f8_empty[st], (j / S8 - 1) & 1, abort_flag)) break;
         const int q = lane - (j % TPB) * GR;  // this lane's group of the tile
         const bool mine = q >= 0 && q < GR;
         const int key0 = (p0 + j) * NK, valid = min(NK, L - key0);
@@ -328,26 +373,29 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
         __syncwarp();
         issued = j + 1;
       }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp && elect_one()) {
       // ------------------------------------------------------------------- MMA
       constexpr uint32_t id_s = idesc_f16(128, NK, false);
       constexpr uint32_t id_o = idesc_f16(128, DH, true);
-      const uint64_t q_desc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t k_desc0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
-      const uint64_t v_desc0 = sdesc_sw128(smem_u32(sKV) + Sh::kTileBytes, NK * 128, 1024);
+      // Low words of the descriptors (address / 16 below 2^14, leading offset
+      // above); the high words are one constant.  Each tile starts from a base
+      // that the compiler takes as new: it would otherwise keep the two dozen
+      // descriptors of a tile, and with this warp's share of registers spill them.
+      const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sQ), 16, 1024));
+      const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sKV), 16, 1024));
+      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sKV) + Sh::kTileBytes, NK * 128, 1024));
       auto issue_s = [&](int j, int t) {
-        const uint64_t kd = k_desc0 + static_cast<uint64_t>((j % SF) * (Sh::kStageBytes >> 4));
-        const uint64_t qd = q_desc0 + static_cast<uint64_t>(t * Sh::kRegions * (Sh::kQRegionBytes >> 4));
+        const uint32_t kd = anew(k_lo + (j % SF) * (Sh::kStageBytes >> 4));
+        const uint32_t qd = anew(q_lo + t * Sh::kRegions * (Sh::kQRegionBytes >> 4));
 #pragma unroll
-        for (int s = 0; s < DH / 16; ++s) {
-          const uint64_t qoff = static_cast<uint64_t>(((s / 4) * Sh::kQRegionBytes + (s % 4) * 32) >> 4);
-          const uint64_t koff = static_cast<uint64_t>(((s / 4) * (NK * 128) + (s % 4) * 32) >> 4);
-          mma_bf16_ss(tmem + Sh::kColS + t * NK, qd + qoff, kd + koff, id_s, s > 0);
-        }
+        for (int s = 0; s < DH / 16; ++s)
+          mma_f16_ss(tmem + Sh::kColS + t * NK, qd + (((s / 4) * Sh::kQRegionBytes + (s % 4) * 32) >> 4),
+                     kd + (((s / 4) * (NK * 128) + (s % 4) * 32) >> 4), id_s, s > 0);
         mma_commit(&s_full[t]);
       };
       bool ok = T == 0 || mbar_wait(&kv_full[0], 0, abort_flag);
       if (ok && T > 0) {
+        fence_async_smem();
         tc_fence_after();
         for (int t = 0; t < MT; ++t) issue_s(0, t);
       }
@@ -355,7 +403,8 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
         const int st = j % SF;
         const bool next = j + 1 < T;
         if (next && !mbar_wait(&kv_full[(j + 1) % SF], ((j + 1) / SF) & 1, abort_flag)) break;
-        const uint64_t vd = v_desc0 + static_cast<uint64_t>(st * (Sh::kStageBytes >> 4));
+        fence_async_smem();
+        const uint32_t vd = v_lo + st * (Sh::kStageBytes >> 4);
         for (int t = 0; t < MT && ok && next; ++t) {
           if (!mbar_wait(&s_free[t], j & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
@@ -364,11 +413,10 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
         for (int t = 0; t < MT && ok; ++t) {
           if (!mbar_wait(&p_full[t], j & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t pcol = tmem + Sh::kColP + t * (NK / 2);
+          const uint32_t pcol = anew(tmem + Sh::kColP + t * (NK / 2)), vt = anew(vd);
 #pragma unroll
           for (int s = 0; s < NK / 16; ++s)
-            mma_bf16_ts(tmem + Sh::kColO + t * DH, pcol + s * 8, vd + static_cast<uint64_t>(s * (2048 >> 4)), id_o,
-                        (j > 0 || s > 0));
+            mma_f16_ts(tmem + Sh::kColO + t * DH, pcol + s * 8, vt + s * (2048 >> 4), id_o, (j > 0 || s > 0));
           mma_commit(&o_done[t]);
         }
         if (ok) mma_commit(&kv_empty[st]);
@@ -396,8 +444,8 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
     for (int j = 0; j < T; ++j) {
       const int st = j % SF;
       const bool prefix = j < np;
-      if (prefix && !warp_wait(&f8_full[j % S8], (j / S8) & 1, abort_flag)) break;
-      if (j >= SF && !warp_wait(&kv_empty[st], (j / SF - 1) & 1, abort_flag)) break;
+      if (prefix && !warp_wait_together(&f8_full[j % S8], (j / S8) & 1, abort_flag)) break;
+      if (j >= SF && !warp_wait_together(&kv_empty[st], (j / SF - 1) & 1, abort_flag)) break;
       unsigned char *kst = sKV + st * Sh::kStageBytes;
       const int key0 = prefix ? (p0 + j) * NK : (j - np) * NK;
       const int valid = min(NK, (prefix ? L : n) - key0);
@@ -454,7 +502,6 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
           }
         }
       }
-      fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&kv_full[st]);
@@ -482,7 +529,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < T; ++j) {
-      if (!warp_wait(&s_full[t], j & 1, abort_flag)) { ok = false; break; }
+      if (!warp_wait_together(&s_full[t], j & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
       const bool prefix = j < np;
       uint64_t keep[NH];
@@ -536,7 +583,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       const float alpha = raise ? ex2_approx(m - tmax) : 1.f;  // m = -inf gives 0
       m = base;
       if (j > 0) {  // P.V of the previous tile is done: P is free, O is final for it
-        if (!warp_wait(&o_done[t], (j - 1) & 1, abort_flag)) { ok = false; break; }
+        if (!warp_wait_together(&o_done[t], (j - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
       }
       const float nb = kBias - (base > -INFINITY ? base : 0.f);
@@ -589,7 +636,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[t]);
     }
-    if (ok && T > 0 && !warp_wait(&o_done[t], (T - 1) & 1, abort_flag)) ok = false;
+    if (ok && T > 0 && !warp_wait_together(&o_done[t], (T - 1) & 1, abort_flag)) ok = false;
     tc_fence_after();
     // tcgen05.ld is warp-collective: every lane executes it, rows past the last
     // node only skip the global writes
@@ -836,7 +883,7 @@ cudaError_t launch_tree_attn_kv8(const void *q, const uint8_t *k_pages, const ui
     if (p.MT == 2) return launch_kv8_t<64, 2, 128, 3, 4, 128, 1>(maps, a, p, st);
     return launch_kv8_t<64, 1, 64, 3, 4, 128, 2>(maps, a, p, st);
   }
-  if (p.MT == 2) return launch_kv8_t<128, 2, 64, 4, 1, 128, 1>(maps, a, p, st);
+  if (p.MT == 2) return launch_kv8_t<128, 2, 64, 3, 3, 128, 1>(maps, a, p, st);
   return p.QR == 64 ? launch_kv8_t<128, 1, 64, 2, 2, 64, 2>(maps, a, p, st) : launch_kv8_t<128, 1, 64, 3, 4, 128, 1>(maps, a, p, st);
 }
 
