@@ -38,7 +38,6 @@ using namespace sm100;
 
 constexpr int kMaxSplits8 = 8;
 constexpr float kBias = 6.f;      // P' = 2^(kBias + ...)
-constexpr int kExpSlots = 8;      // tiles whose exponents are held: more than S8 + SF
 
 struct Kv8Args {
   const __nv_bfloat16 *q, *k_tree, *v_tree;
@@ -72,9 +71,11 @@ struct Kv8Shape {
   static constexpr int kBarOff = kStagingOff + S8 * 2 * kByteTile;
   static constexpr int kGroups = NK / 16;
   static constexpr int kNumBars = 2 * S8 + 2 * SF + 4 * MT + 1;
-  // barriers, tensor-memory slot and abort flag, exponents of tiles, of query rows
-  static constexpr int kExpOff = kNumBars * 8 + 8;
-  static constexpr int kBarBytes = kExpOff + kExpSlots * 2 * kGroups + MT * QR;
+  // barriers, tensor-memory slot and abort flag, scales of the tiles' groups,
+  // exponents of the query rows
+  static constexpr int kExpSlots = S8 + SF + 1;           // tiles between the producer and the softmax
+  static constexpr int kExpOff = (kNumBars * 8 + 8 + 15) / 16 * 16;
+  static constexpr int kBarBytes = kExpOff + kExpSlots * kGroups * 16 + MT * QR;
   // The barriers sit in the gap before the 1 KB-aligned buffers when it holds
   // them, else after the buffers.
   static constexpr int kSmem = kBarOff + (1008 > 2 * kBarBytes - 16 ? 1008 : 2 * kBarBytes - 16);
@@ -88,11 +89,10 @@ struct Kv8Shape {
   // it (softmax, converters, producer and MMA); they add up to the launch's.
   static constexpr int kLaunchRegs = 65536 / (kThreads * OCC) / 8 * 8;
   static constexpr bool kShareRegs = kLaunchRegs < 160;
-  static constexpr int kRegsOther = MT == 1 ? 40 : 40;
-  static constexpr int kRegsConvert = MT == 1 ? 56 : 72;
+  static constexpr int kRegsOther = MT == 1 ? 40 : 48;
+  static constexpr int kRegsConvert = MT == 1 ? 56 : 88;
   static constexpr int kRegsSoftmax = ((MT + 2) * kLaunchRegs - kRegsOther - kRegsConvert) / MT / 8 * 8;
   static_assert(QR == 128 || (QR == 64 && MT == 1), "64-row regions with one M-tile only");
-  static_assert(S8 + SF < kExpSlots, "exponents outlive their tile");
   static_assert(kCols <= 512 && kTmemCols * OCC <= 512, "tensor memory budget");
   static_assert(kSmem <= 232448 && OCC * (kSmem + 1024) <= 233472, "shared memory budget");
   static_assert(MT * kRegsSoftmax + kRegsConvert + kRegsOther <= (MT + 2) * kLaunchRegs, "register budget");
@@ -246,8 +246,9 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
   uint64_t *teardown = o_done + MT;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(teardown + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  signed char *exps = reinterpret_cast<signed char *>(ctl + Sh::kExpOff);  // [kExpSlots][K, V][GR]
-  signed char *q_exp = exps + kExpSlots * 2 * GR;                          // [MT * QR]
+  // of every 16-key group: (2^ke, ve, 2^-ve, 0)
+  float4 *scales = reinterpret_cast<float4 *>(ctl + Sh::kExpOff);          // [kExpSlots][GR]
+  signed char *q_exp = reinterpret_cast<signed char *>(scales + Sh::kExpSlots * GR);  // [MT * QR]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, mg = blockIdx.y;
@@ -356,9 +357,9 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
         const bool mine = q >= 0 && q < GR;
         const int key0 = (p0 + j) * NK, valid = min(NK, L - key0);
         if (mine) {
-          signed char *ex = exps + (j % kExpSlots) * 2 * GR;
-          ex[q] = static_cast<signed char>(scale_exponent(ks));
-          ex[GR + q] = static_cast<signed char>(scale_exponent(vs));
+          const int ve = scale_exponent(vs);
+          scales[(j % Sh::kExpSlots) * GR + q] =
+              make_float4(exponent_scale(scale_exponent(ks)), static_cast<float>(ve), exponent_scale(-ve), 0.f);
         }
         __syncwarp();
         if (lane == 0)
@@ -498,7 +499,15 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
                                      bf16x2_to_half2(y.z, f), bf16x2_to_half2(y.w, f)};
               store(tile, r, h);
             }
-            if (lane == 0) exps[(j % kExpSlots) * 2 * GR + kv * GR + grp] = static_cast<signed char>(e);
+            if (lane == 0) {
+              float4 *sc = scales + (j % Sh::kExpSlots) * GR + grp;
+              if (kv) {
+                sc->y = static_cast<float>(e);
+                sc->z = pow2_clamped(-e);
+              } else {
+                sc->x = pow2_clamped(e);
+              }
+            }
           }
         }
       }
@@ -518,7 +527,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
     const bool warp_live = (mg * MT + t) * 128 + qtr * 32 < rows_total;  // warp-uniform
     const int i = row_ok ? rho / a.G : 0;
     const int hh = row_ok ? rho % a.G : 0;
-    const int qe = row_ok ? q_exp[t * QR + r] : 0;
+    const float row_scale = a.scale_log2 * (row_ok ? pow2_clamped(q_exp[t * QR + r]) : 1.f);
     const uint32_t lane_base = static_cast<uint32_t>(qtr * 32) << 16;
     const uint32_t tS = tmem + lane_base + Sh::kColS + t * NK;
     const uint32_t tP = tmem + lane_base + Sh::kColP + t * (NK / 2);
@@ -547,36 +556,50 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
 #pragma unroll
       for (int h = 0; h < NH; ++h) dense = dense && keep[h] == ~0ull;
       dense = __all_sync(0xffffffffu, dense);
-      float sv[NH][64];
-      if (warp_live) {
+      // S in halves of 64 columns.  With two halves the first is read once for
+      // the maximum and again for its exponentials, after the second's: 64
+      // scores in registers at a time instead of 128.
+      const float4 *sc = scales + (j % Sh::kExpSlots) * GR;
+      const auto factor = [&](float ke) { return fminf(fmaxf(row_scale * ke, 1.2e-38f), 1e38f); };
+      float sv[2][32];
+      const auto mask_half = [&](int h) {
+        if (dense) return;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          tmem_ld32(tS + 64 * h, *reinterpret_cast<float(*)[32]>(&sv[h][0]));
-          tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<float(*)[32]>(&sv[h][32]));
+        for (int c = 0; c < 64; ++c) sv[c / 32][c % 32] = ((keep[h] >> c) & 1ull) ? sv[c / 32][c % 32] : -INFINITY;
+      };
+      const auto half_max = [&](int h) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float *s16 = sv[q / 2] + 16 * (q % 2);
+          float y = s16[0];
+#pragma unroll
+          for (int c = 1; c < 15; c += 2) y = fmax3(y, s16[c], s16[c + 1]);
+          const float4 g4 = sc[4 * h + q];
+          x = fmaxf(x, fmaf(fmaxf(y, s16[15]), factor(g4.x), g4.y));
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
-      const signed char *ex = exps + (j % kExpSlots) * 2 * GR;
+        return x;
+      };
       float tmax = -INFINITY;
+      if (NH == 2 && warp_live) {
+        tmem_ld32(tS, sv[0]);
+        tmem_ld32(tS + 32, sv[1]);
+        mask_half(0);
+        tmax = half_max(0);
+      }
       if (warp_live) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          if (!dense) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) sv[h][c] = ((keep[h] >> c) & 1ull) ? sv[h][c] : -INFINITY;
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float x = sv[h][16 * q];
-#pragma unroll
-            for (int c = 1; c < 15; c += 2) x = fmax3(x, sv[h][16 * q + c], sv[h][16 * q + c + 1]);
-            x = fmaxf(x, sv[h][16 * q + 15]);
-            const float f = fmaxf(a.scale_log2 * pow2_clamped(qe + ex[4 * h + q]), 1.2e-38f);
-            tmax = fmaxf(tmax, fmaf(x, f, static_cast<float>(ex[GR + 4 * h + q])));
-          }
-        }
+        tmem_ld32(tS + 64 * (NH - 1), sv[0]);
+        tmem_ld32(tS + 64 * (NH - 1) + 32, sv[1]);
+      }
+      const auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
+      };
+      if (NH == 1) release();
+      if (warp_live) {
+        mask_half(NH - 1);
+        tmax = fmaxf(tmax, half_max(NH - 1));
       }
       const bool raise = tmax > m + 8.f;
       const float base = raise ? tmax : m;
@@ -588,39 +611,45 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       }
       const float nb = kBias - (base > -INFINITY ? base : 0.f);
       float sum = 0.f;
-      if (warp_live) {
+      const auto exp_half = [&](int h) {
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
+        for (int half = 0; half < 2; ++half) {
+          float pk[16];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float pk[16];
+          for (int q = 0; q < 2; ++q) {
+            const float4 g4 = sc[4 * h + 2 * half + q];
+            const float f = factor(g4.x), off = nb + g4.y;
+            const uint64_t f2 = f2_pack(f, f), o2 = f2_pack(off, off);
+            uint64_t acc = f2_pack(0.f, 0.f);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int grp = 4 * h + 2 * half + q;
-              const int ve = ex[GR + grp];
-              const float f = fmaxf(a.scale_log2 * pow2_clamped(qe + ex[grp]), 1.2e-38f);
-              const float off = nb + static_cast<float>(ve);
-              const uint64_t f2 = f2_pack(f, f), o2 = f2_pack(off, off);
-              uint64_t acc = f2_pack(0.f, 0.f);
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const int col = 32 * half + 16 * q + 2 * c;
-                float t0, t1;
-                f2_unpack(f2_fma(f2_pack(sv[h][col], sv[h][col + 1]), f2, o2), t0, t1);
-                const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
-                acc = f2_add(acc, f2_pack(e0, e1));
-                const __half2 h2 = __floats2half2_rn(e0, e1);
-                pk[8 * q + c] = *reinterpret_cast<const float *>(&h2);
-              }
-              float a0, a1;
-              f2_unpack(acc, a0, a1);
-              sum = fmaf(a0 + a1, pow2_clamped(-ve), sum);
+            for (int c = 0; c < 8; ++c) {
+              float t0, t1;
+              f2_unpack(f2_fma(f2_pack(sv[half][16 * q + 2 * c], sv[half][16 * q + 2 * c + 1]), f2, o2), t0, t1);
+              const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+              acc = f2_add(acc, f2_pack(e0, e1));
+              const __half2 h2 = __floats2half2_rn(e0, e1);
+              pk[8 * q + c] = *reinterpret_cast<const float *>(&h2);
             }
-            tmem_st16_async(tP + 32 * h + 16 * half, pk);
+            float a0, a1;
+            f2_unpack(acc, a0, a1);
+            sum = fmaf(a0 + a1, g4.z, sum);
           }
+          tmem_st16_async(tP + 32 * h + 16 * half, pk);
         }
-        tmem_wait_st();
+      };
+      if (warp_live) exp_half(NH - 1);
+      if constexpr (NH == 2) {
+        if (warp_live) {
+          tmem_ld32(tS, sv[0]);
+          tmem_ld32(tS + 32, sv[1]);
+        }
+        release();
+        if (warp_live) {
+          mask_half(0);
+          exp_half(0);
+        }
       }
+      if (warp_live) tmem_wait_st();
       l = fmaf(l, alpha, sum);
       if (warp_live && j > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll
