@@ -28,33 +28,11 @@
 // KV split over up to 8 CTAs and the merge of their results as there too.
 // Every wait is bounded; a timeout raises EAGLE_ERR_TIMEOUT in the status
 // word and the CTA drains its copies and MMAs, frees tensor memory and exits.
-#include "kv8.cuh"
-#include "sm100.cuh"
-#include "tmap.cuh"
+#include "kv8_attn.cuh"
 
 namespace eagle {
 
 using namespace sm100;
-
-constexpr int kMaxSplits8 = 8;
-constexpr float kBias = 6.f;      // P' = 2^(kBias + ...)
-
-struct Kv8Args {
-  const __nv_bfloat16 *q, *k_tree, *v_tree;
-  const float *k_scale, *v_scale;
-  const int32_t *block_table, *kv_len;
-  const uint64_t *mask;
-  int B, n, Hq, Hkv, G, W, S;
-  int page_size, log_page, page_box, max_pages, num_pages;
-  float scale_log2;  // softmax scale times log2(e)
-  __nv_bfloat16 *out;
-  float *lse;
-  int32_t *status;
-  // KV split (S > 1): one workspace slot per CTA, [slot_rows][DH] fp32 O rows
-  // then [slot_rows] (m, l) pairs, the slots of a (b, g, M-group) consecutive
-  float *part;
-  int slot_rows;
-};
 
 // QR: query rows held per M-tile region (64 when there are at most 64: the
 // 128-row MMAs then read rows 64-127 from what follows, and those rows' results
@@ -153,71 +131,6 @@ __device__ __forceinline__ bool warp_wait_together(uint64_t *bar, uint32_t parit
   const bool ok = warp_wait(bar, parity, abort);
   __syncwarp();
   return ok;
-}
-
-// 2^e in float32 for any int e that a sum of exponents can give, kept away
-// from 0 and infinity (0 * inf must not arise from finite inputs).
-__device__ __forceinline__ float pow2_clamped(int e) { return exponent_scale(min(max(e, -120), 120)); }
-
-// The exponent e with amax / 2^e in [2^8, 2^9), where an e4m3 block's numbers
-// end too: a bf16 number keeps its 8 bits in f16 down to 2^-25 of amax.
-__device__ __forceinline__ int half_exponent(float amax) {
-  if (amax == 0.f) return 0;
-  return max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8, -100);
-}
-__device__ __forceinline__ uint32_t bf16x2_to_half2(uint32_t w, float f) {
-  const __half2 h = __floats2half2_rn(bf16_lo(w) * f, bf16_hi(w) * f);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-// Largest magnitude of eight packed bf16 numbers.
-__device__ __forceinline__ float amax8(const uint4 &v) {
-  const uint4 a = make_uint4(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
-  return vec_max<__nv_bfloat16>(a);
-}
-
-// out and lse of row rr, columns 4c..4c+3, of a (b, g, M-group) from its S
-// slots: out = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m).
-template <int DH>
-__device__ __forceinline__ void kv8_merge_item(const Kv8Args &a, int bg, int mg, int MT, int rr, int c) {
-  constexpr int NV = DH / 4;
-  const int64_t slot_floats = static_cast<int64_t>(a.slot_rows) * (DH + 2);
-  const float *slots = a.part + (static_cast<int64_t>(bg) * gridDim.y + mg) * a.S * slot_floats;
-  float2 ml[kMaxSplits8];
-  float4 po[kMaxSplits8];
-#pragma unroll
-  for (int s = 0; s < kMaxSplits8; ++s) {
-    if (s < a.S) {
-      ml[s] = __ldcg(reinterpret_cast<const float2 *>(slots + s * slot_floats + static_cast<int64_t>(a.slot_rows) * DH) + rr);
-      po[s] = __ldcg(reinterpret_cast<const float4 *>(slots + s * slot_floats) + rr * NV + c);
-    } else {
-      ml[s] = make_float2(-INFINITY, 0.f);
-      po[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  }
-  float M = -INFINITY;
-#pragma unroll
-  for (int s = 0; s < kMaxSplits8; ++s) M = fmaxf(M, ml[s].x);
-  float Ls = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int s = 0; s < kMaxSplits8; ++s) {
-    const float w = ml[s].x > -INFINITY ? ex2_approx(ml[s].x - M) : 0.f;
-    Ls = fmaf(w, ml[s].y, Ls);
-    // a split without any key holds no O (tensor memory it never wrote)
-    if (w > 0.f) {
-      o.x = fmaf(w, po[s].x, o.x); o.y = fmaf(w, po[s].y, o.y);
-      o.z = fmaf(w, po[s].z, o.z); o.w = fmaf(w, po[s].w, o.w);
-    }
-  }
-  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-  const int rho = mg * MT * 128 + rr, i = rho / a.G, h = (bg % a.Hkv) * a.G + rho % a.G;
-  const int64_t orow = (static_cast<int64_t>(bg / a.Hkv) * a.n + i) * a.Hq + h;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  uint2 packed;
-  packed.x = *reinterpret_cast<const uint32_t *>(&lo);
-  packed.y = *reinterpret_cast<const uint32_t *>(&hi);
-  reinterpret_cast<uint2 *>(a.out + orow * DH)[c] = packed;
-  if (c == 0 && a.lse) a.lse[orow] = Ls > 0.f ? (M - kBias + log2f(Ls)) * kLn2 : -INFINITY;
 }
 
 // MERGE: 0 the grid does not split the KV range; 1 the S splits of an item are
@@ -776,32 +689,15 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
   }
 }
 
-// The merge of a split launch of several waves: one thread per (row, 4 columns).
-template <int DH>
-__global__ void __launch_bounds__(256) tree_attn_kv8_merge_kernel(Kv8Args a, int MT) {
-  constexpr int NV = DH / 4;
-  const int mg = blockIdx.y, bg = blockIdx.z;
-  const int nr = max(0, min(a.n * a.G - mg * MT * 128, MT * 128));
-  const int item = blockIdx.x * blockDim.x + threadIdx.x;
-  pdl_wait();  // the partial results come from the attention kernel
-  if (item < nr * NV) kv8_merge_item<DH>(a, bg, mg, MT, item / NV, item % NV);
-}
-
 // ---- host side ---------------------------------------------------------------
 
-// A pool [num_pages * Hkv, page_size, dh] of bytes in boxes of page_box rows.
-// Three dimensions, so no coordinate passes 32 bits however long the pool.
-static bool make_pool_map(CUtensorMap *map, const void *base, int64_t blocks, int page_size, int dh, int page_box) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(dh), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(blocks)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(dh), static_cast<cuuint64_t>(dh) * page_size};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(dh), static_cast<cuuint32_t>(page_box), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+// tree_attn_kv8_few.cu
+size_t attn_kv8_few_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num_sms);
+cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void *v_pages, int dh, void *ws, int num_sms,
+                                     cudaStream_t st);
+
+// Query rows of a KV head up to which the few-row kernel runs.
+constexpr int kFewRows = 64;
 
 struct Kv8Plan {
   int MT, NK, QR, mgroups, S, ctas_per_sm;
@@ -824,7 +720,7 @@ static Kv8Plan kv8_plan(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num
   const double split_cost = static_cast<double>(rows) * 64.0 / p.NK / 32.0 / p.mgroups;
   p.S = 1;
   double best = 1e30;
-  for (int S = 1; S <= kMaxSplits8 && S <= ptiles; ++S) {
+  for (int S = 1; S <= kMaxClusterSplits8 && S <= ptiles; ++S) {
     const int64_t waves = (base * S + slots - 1) / slots;
     const double cost = waves * (static_cast<double>((ptiles + S - 1) / S) + (S > 1 ? split_cost : 0.0));
     if (cost < best * 0.97) {  // prefer fewer splits unless clearly better
@@ -840,6 +736,7 @@ static Kv8Plan kv8_plan(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num
 static int kv8_slot_rows(const Kv8Plan &p, int rows) { return min((rows + 7) / 8 * 8, p.MT * 128); }
 
 size_t attn_kv8_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num_sms) {
+  if (n * (Hq / Hkv) <= kFewRows) return attn_kv8_few_workspace_bytes(B, n, Hq, Hkv, dh, Lmax, num_sms);
   const Kv8Plan p = kv8_plan(B, n, Hq, Hkv, dh, Lmax, num_sms);
   if (p.S <= 1) return 0;
   return static_cast<size_t>(B) * Hkv * p.mgroups * p.S * kv8_slot_rows(p, n * (Hq / Hkv)) * (dh + 2) * sizeof(float);
@@ -885,29 +782,31 @@ cudaError_t launch_tree_attn_kv8(const void *q, const uint8_t *k_pages, const ui
                                  int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
                                  const uint64_t *mask, int B, int n, int Hq, int Hkv, int dh, float scale, void *out,
                                  float *lse, void *ws, int32_t *status, int num_sms, cudaStream_t st) {
-  const Kv8Plan p = kv8_plan(B, n, Hq, Hkv, dh, max_pages * page_size, num_sms);
-  if (p.S > 1 && !ws) return cudaErrorInvalidValue;
-  const int page_box = min(page_size, p.NK);
-  CUtensorMap maps[2];
-  const int64_t blocks = static_cast<int64_t>(num_pages) * Hkv;
-  if (!make_pool_map(&maps[0], k_pages, blocks, page_size, dh, page_box) ||
-      !make_pool_map(&maps[1], v_pages, blocks, page_size, dh, page_box))
-    return cudaErrorInvalidValue;
   Kv8Args a;
   a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
   a.k_tree = reinterpret_cast<const __nv_bfloat16 *>(k_tree);
   a.v_tree = reinterpret_cast<const __nv_bfloat16 *>(v_tree);
   a.k_scale = k_scale; a.v_scale = v_scale;
   a.block_table = block_table; a.kv_len = kv_len; a.mask = mask;
-  a.B = B; a.n = n; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.W = (n + 63) / 64; a.S = p.S;
-  a.page_size = page_size; a.page_box = page_box; a.max_pages = max_pages; a.num_pages = num_pages;
+  a.B = B; a.n = n; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.W = (n + 63) / 64;
+  a.page_size = page_size; a.max_pages = max_pages; a.num_pages = num_pages;
   a.log_page = 0;
   while ((1 << a.log_page) < page_size) ++a.log_page;
   a.scale_log2 = scale * kLog2e;
   a.out = reinterpret_cast<__nv_bfloat16 *>(out);
   a.lse = lse; a.status = status;
+  if (n * a.G <= kFewRows) return launch_tree_attn_kv8_few(a, k_pages, v_pages, dh, ws, num_sms, st);
+  const Kv8Plan p = kv8_plan(B, n, Hq, Hkv, dh, max_pages * page_size, num_sms);
+  if (p.S > 1 && !ws) return cudaErrorInvalidValue;
+  a.S = p.S;
+  a.page_box = min(page_size, p.NK);
   a.part = p.S > 1 ? reinterpret_cast<float *>(ws) : nullptr;
   a.slot_rows = kv8_slot_rows(p, n * a.G);
+  CUtensorMap maps[2];
+  const int64_t blocks = static_cast<int64_t>(num_pages) * Hkv;
+  if (!make_pool_map(&maps[0], k_pages, blocks, page_size, dh, a.page_box, false) ||
+      !make_pool_map(&maps[1], v_pages, blocks, page_size, dh, a.page_box, false))
+    return cudaErrorInvalidValue;
   if (dh == 64) {
     if (p.MT == 2) return launch_kv8_t<64, 2, 128, 3, 4, 128, 1>(maps, a, p, st);
     return launch_kv8_t<64, 1, 64, 3, 4, 128, 2>(maps, a, p, st);
