@@ -8,21 +8,22 @@
 // q = 2^a q', k = 2^ke k', v = 2^ve v' (ke, ve of a group of 16 keys, which no
 // page splits):
 //   s  = (scale log2e 2^(a+ke)) <q', k'>           score, base 2
-//   P' = 2^(s + ve - m + 6),  m >= max(s + ve) - 8     in f16
+//   P' = 2^(s + ve - m + 6),  m >= max(s + ve) - 9     in f16
 //   O  = sum P' v',  l = sum_groups 2^-ve sum P',  out = O / l,
 //   lse = ln 2 (m - 6 + log2 l)
-// so P' stays below 2^14 and is rounded to 11 bits (bf16 would leave 8), down
+// so P' stays below 2^15 and is rounded to 11 bits (bf16 would leave 8), down
 // to 2^-20 of the row's largest; smaller ones are off by up to 2^-31 of it
 // (f16's subnormals).  Neither K nor V is rounded at all.
 //
 // One CTA per (sequence b, KV head g, group of MT 128-row M-tiles, KV split);
 // query rows are (node, head-in-group) pairs, key tiles hold NK keys, first the
 // prefix, then the tree nodes masked with the ancestor bits.  Roles:
-//   * producer warp: page numbers and scales two batches of 32 groups ahead, K/V
-//     bytes by TMA into a ring of S8 staging buffers;
-//   * four converter warps: staging bytes (tree tiles: bf16 from global memory)
-//     to f16 in a ring of SF stages, in the 128-byte swizzle the MMAs read;
-//     rows past the prefix's end become zeros;
+//   * two producer warps, K's and V's: page numbers and scales two batches of 32
+//     groups ahead, bytes by TMA into a ring of S8 staging buffers;
+//   * converter warps: staging bytes (tree tiles: bf16 from global memory) to f16
+//     in rings of SF tiles, K's and V's, in the 128-byte swizzle the MMAs read;
+//     rows past the prefix's end become zeros.  K's ring runs ahead:
+//     its tiles are free once S is taken, V's only after P.V;
 //   * MMA thread and one softmax warpgroup per M-tile as in tree_attn_tc.cu:
 //     S = Q K^T from shared memory, P from tensor memory.
 // KV split over up to 8 CTAs and the merge of their results as there too.
@@ -43,39 +44,44 @@ struct Kv8Shape {
   static constexpr int kQRegionBytes = QR * 128;
   static constexpr int kQBytes = MT * kRegions * kQRegionBytes;
   static constexpr int kTileBytes = kRegions * NK * 128;  // one f16 K (or V) tile
-  static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kByteTile = NK * DH;               // one e4m3 K (or V) tile
-  static constexpr int kStagingOff = kQBytes + SF * kStageBytes;
+  // Q, the rings of f16 K and V tiles, the staging of K's and V's bytes
+  static constexpr int kVOff = kQBytes + SF * kTileBytes;
+  static constexpr int kStagingOff = kVOff + SF * kTileBytes;
   static constexpr int kBarOff = kStagingOff + S8 * 2 * kByteTile;
   static constexpr int kGroups = NK / 16;
-  static constexpr int kNumBars = 2 * S8 + 2 * SF + 4 * MT + 1;
+  static constexpr int kNumBars = 4 * S8 + 4 * SF + 4 * MT + 2;
   // barriers, tensor-memory slot and abort flag, scales of the tiles' groups,
   // exponents of the query rows
-  static constexpr int kExpSlots = S8 + SF + 1;           // tiles between the producer and the softmax
-  static constexpr int kExpOff = (kNumBars * 8 + 8 + 15) / 16 * 16;
-  static constexpr int kBarBytes = kExpOff + kExpSlots * kGroups * 16 + MT * QR;
+  static constexpr int kScaleSlots = S8 + SF + 3;         // tiles between K's producer and the softmax
+  static constexpr int kScaleOff = (kNumBars * 8 + 8 + 15) / 16 * 16;
+  static constexpr int kBarBytes = kScaleOff + kScaleSlots * kGroups * 8 + MT * QR;
   // The barriers sit in the gap before the 1 KB-aligned buffers when it holds
   // them, else after the buffers.
   static constexpr int kSmem = kBarOff + (1008 > 2 * kBarBytes - 16 ? 1008 : 2 * kBarBytes - 16);
-  static constexpr int kThreads = (MT + 2) * 128;
+  // Warpgroups that convert: K's and V's, or with two M-tiles (whose softmax has
+  // the use of the issue slots) one that takes K and V in turn.
+  static constexpr int kConvertGroups = MT == 1 ? 2 : 1;
+  static constexpr int kGroupsAll = MT + kConvertGroups + 1;
+  static constexpr int kThreads = kGroupsAll * 128;
   static constexpr int kColS = 0;                         // S_t at t*NK
   static constexpr int kColP = MT * NK;                   // P_t at kColP + t*NK/2
   static constexpr int kColO = MT * NK + MT * NK / 2;     // O_t at kColO + t*DH
   static constexpr int kCols = kColO + MT * DH;
   static constexpr int kTmemCols = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   // Registers: what a thread is launched with, and the warpgroups' shares of
-  // it (softmax, converters, producer and MMA); they add up to the launch's.
+  // it (softmax, converters, producers and MMA); they add up to the launch's.
   static constexpr int kLaunchRegs = 65536 / (kThreads * OCC) / 8 * 8;
-  static constexpr bool kShareRegs = kLaunchRegs < 160;
-  static constexpr int kRegsOther = MT == 1 ? 40 : 48;
-  static constexpr int kRegsConvert = MT == 1 ? 56 : 88;
-  static constexpr int kRegsSoftmax = ((MT + 2) * kLaunchRegs - kRegsOther - kRegsConvert) / MT / 8 * 8;
+  static constexpr int kRegsOther = kLaunchRegs < 80 ? 32 : 48;
+  static constexpr int kRegsConvert = kLaunchRegs < 80 ? 40 : (kConvertGroups == 1 ? 88 : 56);
+  static constexpr int kRegsLeft = (kGroupsAll * kLaunchRegs - kRegsOther - kConvertGroups * kRegsConvert) / MT / 8 * 8;
+  static constexpr int kRegsSoftmax = kRegsLeft > 208 ? 208 : kRegsLeft;
   static_assert(QR == 128 || (QR == 64 && MT == 1), "64-row regions with one M-tile only");
   static_assert(kCols <= 512 && kTmemCols * OCC <= 512, "tensor memory budget");
   static_assert(kSmem <= 232448 && OCC * (kSmem + 1024) <= 233472, "shared memory budget");
-  static_assert(MT * kRegsSoftmax + kRegsConvert + kRegsOther <= (MT + 2) * kLaunchRegs, "register budget");
-  // split: fp32 O rows in the stages and the staging after them, (m, l) in Q's buffer
-  static_assert(MT * 128 * DH * 4 <= kBarOff - kQBytes, "partial O fits the stage and staging buffers");
+  static_assert(MT * kRegsSoftmax + kConvertGroups * kRegsConvert + kRegsOther <= kGroupsAll * kLaunchRegs, "register budget");
+  // split: fp32 O rows in the rings and the staging after them, (m, l) in Q's buffer
+  static_assert(MT * 128 * DH * 4 <= kBarOff - kQBytes, "partial O fits the rings and the staging");
   static_assert(MT * 128 * 8 <= kQBytes, "(m, l) fit the Q buffer");
 };
 
@@ -125,18 +131,56 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-// warp_wait for warps that work on afterwards: brings lane 0, which polled, back
-// together with the others (they would run what follows apart).
-__device__ __forceinline__ bool warp_wait_together(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  const bool ok = warp_wait(bar, parity, abort);
-  __syncwarp();
-  return ok;
+// The scales of a 16-key group as the softmax takes them: two powers of two in
+// one word (the upper half of the float 2^ke, that of 2^-ve below it), and ve.
+__device__ __forceinline__ uint32_t pack_scales(float k_pow2, float v_inverse) {
+  return (__float_as_uint(k_pow2) & 0xffff0000u) | (__float_as_uint(v_inverse) >> 16);
 }
+
+// 64 fp32 columns of this thread's tensor-memory lane as two runs of 32, one wait.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t taddr, float (&a)[32], float (&b)[32]) {
+  uint32_t r[32], q[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15]), "=r"(q[16]), "=r"(q[17]), "=r"(q[18]), "=r"(q[19]), "=r"(q[20]), "=r"(q[21]), "=r"(q[22]), "=r"(q[23]), "=r"(q[24]), "=r"(q[25]), "=r"(q[26]), "=r"(q[27]), "=r"(q[28]), "=r"(q[29]), "=r"(q[30]), "=r"(q[31])
+      : "r"(taddr), "r"(taddr + 32)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    a[i] = __uint_as_float(r[i]);
+    b[i] = __uint_as_float(q[i]);
+  }
+}
+
+// Bounded wait (two seconds of wall time) of a whole warp, or of one elected
+// thread, in few instructions: this kernel's roles share the instruction cache,
+// and a wait written out in each place costs more in fetches than in waiting.
+// Every lane polls, so the warp stays together.
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort || now - t0 > 2000000000ull) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
 
 // MERGE: 0 the grid does not split the KV range; 1 the S splits of an item are
 // one cluster and merge in this kernel; 2 tree_attn_kv8_merge_kernel merges.
 template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, int MERGE>
-__global__ void __launch_bounds__((MT + 2) * 128, OCC)
+__global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, Kv8Args a) {
   using Sh = Kv8Shape<DH, MT, NK, SF, S8, QR, OCC>;
   constexpr bool SPLIT = MERGE != 0;
@@ -145,69 +189,40 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
   const uintptr_t raw = reinterpret_cast<uintptr_t>(raw_smem);
   unsigned char *sm = reinterpret_cast<unsigned char *>((raw + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char *sQ = sm;
-  unsigned char *sKV = sm + Sh::kQBytes;
+  unsigned char *sK = sm + Sh::kQBytes, *sV = sm + Sh::kVOff;
   unsigned char *s8 = sm + Sh::kStagingOff;
   unsigned char *ctl = reinterpret_cast<uintptr_t>(sm) - raw >= static_cast<uintptr_t>(Sh::kBarBytes) ? raw_smem : sm + Sh::kBarOff;
-  uint64_t *f8_full = reinterpret_cast<uint64_t *>(ctl);
-  uint64_t *f8_empty = f8_full + S8;
-  uint64_t *kv_full = f8_empty + S8;
-  uint64_t *kv_empty = kv_full + SF;
-  uint64_t *s_full = kv_empty + SF;
+  // K's barriers, then V's: bytes landed, staging free, f16 tile written, tile read
+  uint64_t *bytes_full = reinterpret_cast<uint64_t *>(ctl);  // [K, V][S8]
+  uint64_t *bytes_empty = bytes_full + 2 * S8;
+  uint64_t *tile_full = bytes_empty + 2 * S8;                // [K, V][SF]
+  uint64_t *tile_empty = tile_full + 2 * SF;
+  uint64_t *s_full = tile_empty + 2 * SF;
   uint64_t *s_free = s_full + MT;
   uint64_t *p_full = s_free + MT;
   uint64_t *o_done = p_full + MT;
-  uint64_t *teardown = o_done + MT;
+  uint64_t *q_full = o_done + MT;
+  uint64_t *teardown = q_full + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(teardown + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  // of every 16-key group: (2^ke, ve, 2^-ve, 0)
-  float4 *scales = reinterpret_cast<float4 *>(ctl + Sh::kExpOff);          // [kExpSlots][GR]
-  signed char *q_exp = reinterpret_cast<signed char *>(scales + Sh::kExpSlots * GR);  // [MT * QR]
+  uint2 *scales = reinterpret_cast<uint2 *>(ctl + Sh::kScaleOff);                   // [kScaleSlots][GR]
+  signed char *q_exp = reinterpret_cast<signed char *>(scales + Sh::kScaleSlots * GR);  // [MT * QR]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, mg = blockIdx.y;
   const int bg = blockIdx.z, b = bg / a.Hkv, g = bg % a.Hkv;
   const int n = a.n;
-  constexpr int kConvertWarp = MT * 4, kProducerWarp = MT * 4 + 4, kMmaWarp = MT * 4 + 5;
+  constexpr int kConvertWarp = MT * 4, kProducerWarp = kConvertWarp + 4 * Sh::kConvertGroups, kMmaWarp = kProducerWarp + 2;
 
   if (tid == 0) prefetch_l2(a.kv_len + b);
-  pdl_wait();  // inputs of this step come from earlier kernels
-  const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
-  const int n_ptiles = (L + NK - 1) / NK;
-  const int tps = (n_ptiles + a.S - 1) / a.S;
-  const int p0 = min(n_ptiles, split * tps), p1 = min(n_ptiles, p0 + tps);
-  const int np = p1 - p0;
-  const int ntt = (split == a.S - 1) ? (n + NK - 1) / NK : 0;
-  const int T = np + ntt;  // key tiles of this CTA
-
-  // ---- Q to shared memory as f16, each row over a power of two of its own ----
-  const int rows_total = n * a.G;
-  constexpr int CPR = DH / 8;  // 16-byte pieces a row: 8 or 16 neighbouring lanes hold one
-  for (int idx = tid; idx < MT * QR * CPR; idx += Sh::kThreads) {
-    const int rr = idx / CPR, c = idx % CPR, t = rr / QR, r = rr % QR;
-    const int rho = (mg * MT + t) * 128 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (rho < rows_total) {
-      const int i = rho / a.G, hh = rho % a.G;
-      v = *reinterpret_cast<const uint4 *>(a.q + ((static_cast<int64_t>(b) * n + i) * a.Hq + g * a.G + hh) * DH + c * 8);
+  if (tid == 32) {
+    for (int i = 0; i < 2 * S8; ++i) {
+      mbar_init(&bytes_full[i], 2);
+      mbar_init(&bytes_empty[i], 4);
     }
-    float amax = amax8(v);
-#pragma unroll
-    for (int o = 1; o < CPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int e = half_exponent(amax);
-    const float f = pow2_clamped(-e);
-    v = make_uint4(bf16x2_to_half2(v.x, f), bf16x2_to_half2(v.y, f), bf16x2_to_half2(v.z, f), bf16x2_to_half2(v.w, f));
-    *reinterpret_cast<uint4 *>(sQ + (t * Sh::kRegions + c / 8) * Sh::kQRegionBytes + sw128_offset(r, c % 8)) = v;
-    if (c == 0) q_exp[rr] = static_cast<signed char>(e);
-  }
-  fence_async_smem();
-  if (tid == 0) {
-    for (int i = 0; i < S8; ++i) {
-      mbar_init(&f8_full[i], 1);
-      mbar_init(&f8_empty[i], 4);
-    }
-    for (int i = 0; i < SF; ++i) {
-      mbar_init(&kv_full[i], 4);
-      mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < 2 * SF; ++i) {
+      mbar_init(&tile_full[i], 4);
+      mbar_init(&tile_empty[i], 1);
     }
     for (int t = 0; t < MT; ++t) {
       mbar_init(&s_full[t], 1);
@@ -215,32 +230,44 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       mbar_init(&p_full[t], 4);
       mbar_init(&o_done[t], 1);
     }
+    mbar_init(q_full, 4 * MT);
     mbar_init(teardown, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
+  pdl_wait();  // inputs of this step come from earlier kernels
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, Sh::kTmemCols);
     tmem_relinquish();
   }
+  const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
+  const int n_ptiles = (L + NK - 1) / NK;
+  const int tps = (n_ptiles + a.S - 1) / a.S;
+  const int p0 = min(n_ptiles, split * tps), p1 = min(n_ptiles, p0 + tps);
+  // Key tiles of this CTA: prefix tiles from pfx0, tree tiles from tree0.  A single
+  // tree tile comes first (it needs no page numbers); several come last, so
+  // that the producers' scales never wait for them.
+  const int np = p1 - p0, ntt = (split == a.S - 1) ? (n + NK - 1) / NK : 0, T = np + ntt;
+  const int pfx0 = ntt == 1 ? 1 : 0, tree0 = ntt == 1 ? 0 : np;
+  const int rows_total = n * a.G;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  int issued = 0;  // producer: tiles requested
+  int issued = 0;  // producers: tiles requested
   bool part_have = false;
   float part_m = -INFINITY, part_l = 0.f;
 
   if (warp >= kProducerWarp) {
-    if constexpr (Sh::kShareRegs) regs_dec<Sh::kRegsOther>();
-    if (warp == kProducerWarp) {
-      // -------------------------------------------------------------- producer
+    regs_dec<Sh::kRegsOther>();
+    if (warp < kMmaWarp) {
+      // ----------------------------------------------- producers: K's, V's warp
       // Lane i of batch k looks after group 32k + i of this CTA's prefix keys.
-      if (lane == 0) {
-        prefetch_tmap(&k_map);
-        prefetch_tmap(&v_map);
-      }
+      const int kv = warp - kProducerWarp;
+      const CUtensorMap *map = kv ? &v_map : &k_map;
+      uint64_t *full = bytes_full + kv * S8, *empty = bytes_empty + kv * S8;
+      if (lane == 0) prefetch_tmap(map);
       constexpr int TPB = 32 / GR;  // tiles a batch
       const int key_end = min(L, p1 * NK);
       const auto page_at = [&](int batch) {
@@ -252,8 +279,9 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
         return 0;
       };
       int page = page_at(0), page_next = page_at(1);
-      float ks = a.k_scale[static_cast<int64_t>(page) * a.Hkv + g], vs = a.v_scale[static_cast<int64_t>(page) * a.Hkv + g];
-      float ks_next = 1.f, vs_next = 1.f;
+      // K's warp also lists the scales of both: the softmax needs them with S
+      const auto scale_at = [&](const float *of, int pg) { return kv ? 1.f : of[static_cast<int64_t>(pg) * a.Hkv + g]; };
+      float ks = scale_at(a.k_scale, page), vs = scale_at(a.v_scale, page), ks_next = 1.f, vs_next = 1.f;
       for (int j = 0; j < np; ++j) {
         if (j % TPB == 0) {
           if (j) {
@@ -261,34 +289,38 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
             page_next = page_at(j / TPB + 1);
           }
           // requested now, looked at a batch later
-          ks_next = a.k_scale[static_cast<int64_t>(page_next) * a.Hkv + g];
-          vs_next = a.v_scale[static_cast<int64_t>(page_next) * a.Hkv + g];
+          ks_next = scale_at(a.k_scale, page_next);
+          vs_next = scale_at(a.v_scale, page_next);
         }
         const int st = j % S8;
-        if (j >= S8 && !warp_wait_together(&f8_empty[st], (j / S8 - 1) & 1, abort_flag)) break;
+        if (j >= S8 && unlikely(!wait_bounded(&empty[st], (j / S8 - 1) & 1, abort_flag))) break;
         const int q = lane - (j % TPB) * GR;  // this lane's group of the tile
         const bool mine = q >= 0 && q < GR;
         const int key0 = (p0 + j) * NK, valid = min(NK, L - key0);
-        if (mine) {
-          const int ve = scale_exponent(vs);
-          scales[(j % Sh::kExpSlots) * GR + q] =
-              make_float4(exponent_scale(scale_exponent(ks)), static_cast<float>(ve), exponent_scale(-ve), 0.f);
-        }
-        __syncwarp();
+        // bytes first: the scales, which may still be on their way, are written
+        // before the tile's conversion can begin (the barrier's second arrival)
         if (lane == 0)
-          mbar_arrive_expect_tx(&f8_full[st], (valid + a.page_box - 1) / a.page_box * a.page_box * DH * 2);
+          mbar_arrive_expect_tx(&full[st], (valid + a.page_box - 1) / a.page_box * a.page_box * DH);
         __syncwarp();
-        if (mine && q * 16 < valid && ((q * 16) & (a.page_box - 1)) == 0) {
-          unsigned char *dst = s8 + st * 2 * Sh::kByteTile + q * 16 * DH;
-          const int row = (key0 + q * 16) & (a.page_size - 1);
-          tma_load_3d(dst, &k_map, 0, row, page * a.Hkv + g, &f8_full[st]);
-          tma_load_3d(dst + Sh::kByteTile, &v_map, 0, row, page * a.Hkv + g, &f8_full[st]);
-        }
+        if (mine && q * 16 < valid && ((q * 16) & (a.page_box - 1)) == 0)
+          tma_load_3d(s8 + (st * 2 + kv) * Sh::kByteTile + q * 16 * DH, map, 0, (key0 + q * 16) & (a.page_size - 1),
+                      page * a.Hkv + g, &full[st]);
         __syncwarp();
         issued = j + 1;
+        if (mine && kv == 0) {
+          const int ve = scale_exponent(vs);
+          scales[((pfx0 + j) % Sh::kScaleSlots) * GR + q] =
+              make_uint2(pack_scales(exponent_scale(scale_exponent(ks)), exponent_scale(-ve)), __float_as_uint(static_cast<float>(ve)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
       }
     } else if (warp == kMmaWarp && elect_one()) {
       // ------------------------------------------------------------------- MMA
+      // Per tile j: S of tile j+1 for every M-tile as soon as its softmax has
+      // taken S(j), then P(j).V for every M-tile once P(j) is in tensor memory.
+      // The converters wrote the tiles through the generic proxy: the fence
+      // after each wait orders them before the MMAs.
       constexpr uint32_t id_s = idesc_f16(128, NK, false);
       constexpr uint32_t id_o = idesc_f16(128, DH, true);
       // Low words of the descriptors (address / 16 below 2^14, leading offset
@@ -296,10 +328,10 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       // that the compiler takes as new: it would otherwise keep the two dozen
       // descriptors of a tile, and with this warp's share of registers spill them.
       const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sQ), 16, 1024));
-      const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sKV), 16, 1024));
-      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sKV) + Sh::kTileBytes, NK * 128, 1024));
+      const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sK), 16, 1024));
+      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(sV), NK * 128, 1024));
       auto issue_s = [&](int j, int t) {
-        const uint32_t kd = anew(k_lo + (j % SF) * (Sh::kStageBytes >> 4));
+        const uint32_t kd = anew(k_lo + (j % SF) * (Sh::kTileBytes >> 4));
         const uint32_t qd = anew(q_lo + t * Sh::kRegions * (Sh::kQRegionBytes >> 4));
 #pragma unroll
         for (int s = 0; s < DH / 16; ++s)
@@ -307,25 +339,32 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
                      kd + (((s / 4) * (NK * 128) + (s % 4) * 32) >> 4), id_s, s > 0);
         mma_commit(&s_full[t]);
       };
-      bool ok = T == 0 || mbar_wait(&kv_full[0], 0, abort_flag);
+      bool ok = T == 0 || (wait_bounded(q_full, 0, abort_flag) && wait_bounded(&tile_full[0], 0, abort_flag));
       if (ok && T > 0) {
         fence_async_smem();
         tc_fence_after();
         for (int t = 0; t < MT; ++t) issue_s(0, t);
+        mma_commit(&tile_empty[0]);
       }
       for (int j = 0; j < T && ok; ++j) {
         const int st = j % SF;
         const bool next = j + 1 < T;
-        if (next && !mbar_wait(&kv_full[(j + 1) % SF], ((j + 1) / SF) & 1, abort_flag)) break;
-        fence_async_smem();
-        const uint32_t vd = v_lo + st * (Sh::kStageBytes >> 4);
-        for (int t = 0; t < MT && ok && next; ++t) {
-          if (!mbar_wait(&s_free[t], j & 1, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          issue_s(j + 1, t);
+        if (next) {
+          if (!wait_bounded(&tile_full[(j + 1) % SF], ((j + 1) / SF) & 1, abort_flag)) break;
+          fence_async_smem();
+          for (int t = 0; t < MT && ok; ++t) {
+            if (!wait_bounded(&s_free[t], j & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            issue_s(j + 1, t);
+          }
+          if (!ok) break;
+          mma_commit(&tile_empty[(j + 1) % SF]);
         }
+        if (!wait_bounded(&tile_full[SF + st], (j / SF) & 1, abort_flag)) break;
+        fence_async_smem();
+        const uint32_t vd = v_lo + st * (Sh::kTileBytes >> 4);
         for (int t = 0; t < MT && ok; ++t) {
-          if (!mbar_wait(&p_full[t], j & 1, abort_flag)) { ok = false; break; }
+          if (!wait_bounded(&p_full[t], j & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t pcol = anew(tmem + Sh::kColP + t * (NK / 2)), vt = anew(vd);
 #pragma unroll
@@ -333,7 +372,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
             mma_f16_ts(tmem + Sh::kColO + t * DH, pcol + s * 8, vt + s * (2048 >> 4), id_o, (j > 0 || s > 0));
           mma_commit(&o_done[t]);
         }
-        if (ok) mma_commit(&kv_empty[st]);
+        if (ok) mma_commit(&tile_empty[SF + st]);
       }
     }
   } else if (warp >= kConvertWarp) {
@@ -343,8 +382,8 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
     // (rows of DH bytes) and their two stores (swizzled rows of 128 bytes) touch
     // every bank once: with DH = 128, columns 0-63 of one row and 64-127 of the
     // other, the next quarter the complement.
-    if constexpr (Sh::kShareRegs) regs_dec<Sh::kRegsConvert>();
-    const int cw = warp - kConvertWarp, quarter = lane >> 3, l8 = lane & 7;
+    regs_dec<Sh::kRegsConvert>();
+    const int cw = warp & 3, quarter = lane >> 3, l8 = lane & 7;
     constexpr int STEPS = DH / 32;          // steps of 16 rows: 32 pieces each
     const int cc = DH == 128 ? l8 : l8 & 3;  // this lane's piece of the row
     const auto row_of = [&](int step) {
@@ -355,85 +394,106 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       *reinterpret_cast<uint4 *>(region + sw128_offset(r, 2 * (cc & 3))) = make_uint4(h[0], h[1], h[2], h[3]);
       *reinterpret_cast<uint4 *>(region + sw128_offset(r, 2 * (cc & 3) + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
     };
-    for (int j = 0; j < T; ++j) {
-      const int st = j % SF;
-      const bool prefix = j < np;
-      if (prefix && !warp_wait_together(&f8_full[j % S8], (j / S8) & 1, abort_flag)) break;
-      if (j >= SF && !warp_wait_together(&kv_empty[st], (j / SF - 1) & 1, abort_flag)) break;
-      unsigned char *kst = sKV + st * Sh::kStageBytes;
-      const int key0 = prefix ? (p0 + j) * NK : (j - np) * NK;
+    const int kv0 = Sh::kConvertGroups == 2 ? (warp - kConvertWarp) >> 2 : 0;
+    for (int jj = 0; jj < T * (3 - Sh::kConvertGroups); ++jj) {
+      const int j = Sh::kConvertGroups == 2 ? jj : jj >> 1, kv = Sh::kConvertGroups == 2 ? kv0 : jj & 1;
+      unsigned char *tiles = kv ? sV : sK;
+      uint64_t *full = tile_full + kv * SF, *empty = tile_empty + kv * SF;
+      const int st = j % SF, jp = j - pfx0;
+      const bool prefix = jp >= 0 && jp < np;
+      if (prefix && unlikely(!wait_bounded(&bytes_full[kv * S8 + jp % S8], (jp / S8) & 1, abort_flag))) break;
+      if (j >= SF && unlikely(!wait_bounded(&empty[st], (j / SF - 1) & 1, abort_flag))) break;
+      unsigned char *tile = tiles + st * Sh::kTileBytes;
+      const int key0 = (prefix ? p0 + jp : j - tree0) * NK;
       const int valid = min(NK, (prefix ? L : n) - key0);
       for (int grp = cw; grp < GR; grp += 4) {
+        if (__builtin_expect(prefix, 1)) {
+          const unsigned char *src = s8 + ((jp % S8) * 2 + kv) * Sh::kByteTile;
+          uint4 x[STEPS];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          unsigned char *tile = kst + kv * Sh::kTileBytes;
-          if (prefix) {
-            const unsigned char *src = s8 + (j % S8) * 2 * Sh::kByteTile + kv * Sh::kByteTile;
-            uint4 x[STEPS];
+          for (int s = 0; s < STEPS; ++s) {
+            const int r = grp * 16 + row_of(s);
+            x[s] = *reinterpret_cast<const uint4 *>(src + r * DH + cc * 16);
+            if (r >= valid) x[s] = make_uint4(0, 0, 0, 0);  // past the prefix: whatever the page holds
+          }
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-              const int r = grp * 16 + row_of(s);
-              x[s] = *reinterpret_cast<const uint4 *>(src + r * DH + cc * 16);
-              if (r >= valid) x[s] = make_uint4(0, 0, 0, 0);  // past the prefix: whatever the page holds
+          for (int s = 0; s < STEPS; ++s) {
+            const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h[2 * i] = e4m3_to_half2(w[i] & 0xffffu);
+              h[2 * i + 1] = e4m3_to_half2(w[i] >> 16);
             }
+            store(tile, grp * 16 + row_of(s), h);
+          }
+        } else {
+          // tree nodes: bf16 over the group's power of two
+          const __nv_bfloat16 *src = (kv ? a.v_tree : a.k_tree) + (static_cast<int64_t>(bg) * n + key0) * DH;
+          float amax = 0.f;
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-              const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-              uint32_t h[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                h[2 * i] = e4m3_to_half2(w[i] & 0xffffu);
-                h[2 * i + 1] = e4m3_to_half2(w[i] >> 16);
-              }
-              store(tile, grp * 16 + row_of(s), h);
-            }
-          } else {
-            // tree nodes: bf16 over the group's power of two
-            const __nv_bfloat16 *src = (kv ? a.v_tree : a.k_tree) + (static_cast<int64_t>(bg) * n + key0) * DH;
-            float amax = 0.f;
-            for (int s = 0; s < STEPS; ++s) {
-              const int r = grp * 16 + row_of(s);
-              if (r >= valid) continue;
+          for (int s = 0; s < STEPS; ++s) {
+            const int r = grp * 16 + row_of(s);
+            if (r >= valid) continue;
+            const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
+            amax = fmaxf(amax, fmaxf(amax8(p[0]), amax8(p[1])));
+          }
+          const int e = half_exponent(warp_max(amax));
+          const float f = pow2_clamped(-e);
+          for (int s = 0; s < STEPS; ++s) {
+            const int r = grp * 16 + row_of(s);
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (r < valid) {
               const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
-              amax = fmaxf(amax, fmaxf(amax8(p[0]), amax8(p[1])));
+              x = p[0];
+              y = p[1];
             }
-            const int e = half_exponent(warp_max(amax));
-            const float f = pow2_clamped(-e);
-            for (int s = 0; s < STEPS; ++s) {
-              const int r = grp * 16 + row_of(s);
-              uint4 x = make_uint4(0, 0, 0, 0), y = x;
-              if (r < valid) {
-                const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
-                x = p[0];
-                y = p[1];
-              }
-              const uint32_t h[8] = {bf16x2_to_half2(x.x, f), bf16x2_to_half2(x.y, f), bf16x2_to_half2(x.z, f),
-                                     bf16x2_to_half2(x.w, f), bf16x2_to_half2(y.x, f), bf16x2_to_half2(y.y, f),
-                                     bf16x2_to_half2(y.z, f), bf16x2_to_half2(y.w, f)};
-              store(tile, r, h);
-            }
-            if (lane == 0) {
-              float4 *sc = scales + (j % Sh::kExpSlots) * GR + grp;
-              if (kv) {
-                sc->y = static_cast<float>(e);
-                sc->z = pow2_clamped(-e);
-              } else {
-                sc->x = pow2_clamped(e);
-              }
-            }
+            const uint32_t h[8] = {bf16x2_to_half2(x.x, f), bf16x2_to_half2(x.y, f), bf16x2_to_half2(x.z, f),
+                                   bf16x2_to_half2(x.w, f), bf16x2_to_half2(y.x, f), bf16x2_to_half2(y.y, f),
+                                   bf16x2_to_half2(y.z, f), bf16x2_to_half2(y.w, f)};
+            store(tile, r, h);
+          }
+          if (lane == 0) {
+            uint2 *sc = scales + (j % Sh::kScaleSlots) * GR + grp;
+            const uint32_t both = pack_scales(pow2_clamped(e), pow2_clamped(-e));
+            reinterpret_cast<unsigned short *>(&sc->x)[kv ? 0 : 1] = static_cast<unsigned short>(kv ? both : both >> 16);
+            if (kv) sc->y = __float_as_uint(static_cast<float>(e));
           }
         }
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&kv_full[st]);
-        if (prefix) mbar_arrive(&f8_empty[j % S8]);
+        mbar_arrive(&full[st]);
+        if (prefix) mbar_arrive(&bytes_empty[kv * S8 + jp % S8]);
       }
+      __syncwarp();
     }
   } else {
     // ----------------------------------------------------------------- softmax
-    if constexpr (Sh::kShareRegs) regs_inc<Sh::kRegsSoftmax>();
+    regs_inc<Sh::kRegsSoftmax>();
     const int t = warp >> 2, qtr = warp & 3;
+    // this M-tile's query rows to shared memory as f16, each over a power of
+    // two of its own: 8 or 16 neighbouring lanes hold a row
+    constexpr int CPR = DH / 8;
+    for (int idx = tid & 127; idx < QR * CPR; idx += 128) {
+      const int r = idx / CPR, c = idx % CPR;
+      const int rho = (mg * MT + t) * 128 + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (rho < rows_total)
+        v = *reinterpret_cast<const uint4 *>(a.q + ((static_cast<int64_t>(b) * n + rho / a.G) * a.Hq + g * a.G + rho % a.G) * DH + c * 8);
+      float amax = amax8(v);
+#pragma unroll
+      for (int o = 1; o < CPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int e = half_exponent(amax);
+      const float f = pow2_clamped(-e);
+      v = make_uint4(bf16x2_to_half2(v.x, f), bf16x2_to_half2(v.y, f), bf16x2_to_half2(v.z, f), bf16x2_to_half2(v.w, f));
+      *reinterpret_cast<uint4 *>(sQ + (t * Sh::kRegions + c / 8) * Sh::kQRegionBytes + sw128_offset(r, c % 8)) = v;
+      if (c == 0) q_exp[t * QR + r] = static_cast<signed char>(e);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+    asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");  // the M-tile's exponents are written
+
     const int r = qtr * 32 + lane;
     const int rho = (mg * MT + t) * 128 + r;
     const bool row_ok = rho < rows_total;
@@ -446,139 +506,140 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
     const uint32_t tP = tmem + lane_base + Sh::kColP + t * (NK / 2);
     const uint32_t tO = tmem + lane_base + Sh::kColO + t * DH;
     const uint64_t *mrow = a.mask + (static_cast<int64_t>(b) * n + i) * a.W;
-    // m is the exponent base of this row's P' and O; it is raised only when the
-    // row maximum exceeds it by more than 8, so O is rescaled rarely.
+    // m is the exponent base of this row's P' and O, a whole number, so that
+    // raising it scales by powers of two.  No maximum is taken per tile: the
+    // weights are made with the base at hand, and their sum says whether one came
+    // near f16's end (above 2^15: no weight below that sum is).  Only then, and
+    // for the first keys, the maximum is found, the base raised to it, and what was
+    // made with the old one scaled or made again.
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < T; ++j) {
-      if (!warp_wait_together(&s_full[t], j & 1, abort_flag)) { ok = false; break; }
+    for (int j = 0; j < T && ok; ++j) {
+      if (unlikely(!wait_bounded(&s_full[t], j & 1, abort_flag))) { ok = false; break; }
       tc_fence_after();
-      const bool prefix = j < np;
-      uint64_t keep[NH];
-#pragma unroll
+      const int jp = j - pfx0;
+      const bool prefix = jp >= 0 && jp < np;
+      // a tree tile's ve is its V converters' (the prefix's scales came with K)
+      if (!prefix && unlikely(!wait_bounded(&tile_full[SF + j % SF], (j / SF) & 1, abort_flag))) { ok = false; break; }
+      const uint2 *sc = scales + (j % Sh::kScaleSlots) * GR;
+      const bool dense = prefix && (p0 + jp + 1) * NK <= L;  // no key of the tile is masked
+      bool pv_done = j == 0;
+      const auto await_pv = [&] {  // P.V of the previous tile: P is free, O is final for it
+        if (!pv_done) {
+          if (unlikely(!wait_bounded(&o_done[t], (j - 1) & 1, abort_flag))) return false;
+          tc_fence_after();
+          pv_done = true;
+        }
+        return true;
+      };
+      // never 0: it multiplies the -inf of masked keys
+      const auto factor = [&](uint32_t s) { return fmaxf(row_scale * __uint_as_float(s & 0xffff0000u), 1.2e-38f); };
+      // one copy of the code for both halves and both tries: with the other roles'
+      // loops it has to stay in the instruction cache
+#pragma unroll 1
       for (int h = 0; h < NH; ++h) {
-        if (prefix) {
-          const int valid = min(NK, L - (p0 + j) * NK) - 64 * h;
-          keep[h] = valid >= 64 ? ~0ull : (valid <= 0 ? 0ull : ((1ull << valid) - 1ull));
-        } else {
-          const int w = (j - np) * NH + h;
-          keep[h] = (row_ok && w < a.W) ? mrow[w] : 0ull;
+        float sv[2][32], pk[2][16];
+        if (warp_live) tmem_ld32x2(tS + 64 * h, sv[0], sv[1]);
+        if (h == NH - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
+          __syncwarp();  // or lane 0 would make its weights apart from the others
         }
-      }
-      bool dense = true;
+        if (unlikely(warp_live && !dense)) {
+          uint64_t keep;
+          if (prefix) {
+            const int valid = min(NK, L - (p0 + jp) * NK) - 64 * h;
+            keep = valid >= 64 ? ~0ull : (valid <= 0 ? 0ull : ((1ull << valid) - 1ull));
+          } else {
+            const int w = (j - tree0) * NH + h;
+            keep = (row_ok && w < a.W) ? mrow[w] : 0ull;
+          }
 #pragma unroll
-      for (int h = 0; h < NH; ++h) dense = dense && keep[h] == ~0ull;
-      dense = __all_sync(0xffffffffu, dense);
-      // S in halves of 64 columns.  With two halves the first is read once for
-      // the maximum and again for its exponentials, after the second's: 64
-      // scores in registers at a time instead of 128.
-      const float4 *sc = scales + (j % Sh::kExpSlots) * GR;
-      const auto factor = [&](float ke) { return fminf(fmaxf(row_scale * ke, 1.2e-38f), 1e38f); };
-      float sv[2][32];
-      const auto mask_half = [&](int h) {
-        if (dense) return;
-#pragma unroll
-        for (int c = 0; c < 64; ++c) sv[c / 32][c % 32] = ((keep[h] >> c) & 1ull) ? sv[c / 32][c % 32] : -INFINITY;
-      };
-      const auto half_max = [&](int h) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float *s16 = sv[q / 2] + 16 * (q % 2);
-          float y = s16[0];
-#pragma unroll
-          for (int c = 1; c < 15; c += 2) y = fmax3(y, s16[c], s16[c + 1]);
-          const float4 g4 = sc[4 * h + q];
-          x = fmaxf(x, fmaf(fmaxf(y, s16[15]), factor(g4.x), g4.y));
+          for (int c = 0; c < 64; ++c) sv[c / 32][c % 32] = ((keep >> c) & 1ull) ? sv[c / 32][c % 32] : -INFINITY;
         }
-        return x;
-      };
-      float tmax = -INFINITY;
-      if (NH == 2 && warp_live) {
-        tmem_ld32(tS, sv[0]);
-        tmem_ld32(tS + 32, sv[1]);
-        mask_half(0);
-        tmax = half_max(0);
-      }
-      if (warp_live) {
-        tmem_ld32(tS + 64 * (NH - 1), sv[0]);
-        tmem_ld32(tS + 64 * (NH - 1) + 32, sv[1]);
-      }
-      const auto release = [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
-      };
-      if (NH == 1) release();
-      if (warp_live) {
-        mask_half(NH - 1);
-        tmax = fmaxf(tmax, half_max(NH - 1));
-      }
-      const bool raise = tmax > m + 8.f;
-      const float base = raise ? tmax : m;
-      const float alpha = raise ? ex2_approx(m - tmax) : 1.f;  // m = -inf gives 0
-      m = base;
-      if (j > 0) {  // P.V of the previous tile is done: P is free, O is final for it
-        if (!warp_wait_together(&o_done[t], (j - 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-      }
-      const float nb = kBias - (base > -INFINITY ? base : 0.f);
-      float sum = 0.f;
-      const auto exp_half = [&](int h) {
+        float raw = 0.f, sum = 0.f;  // of P', and over the groups' 2^ve
+#pragma unroll 1
+        for (int tries = 0; warp_live; ++tries) {
+          const float nb = kBias - (m > -INFINITY ? m : 0.f);
+          raw = sum = 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float pk[16];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float4 g4 = sc[4 * h + 2 * half + q];
-            const float f = factor(g4.x), off = nb + g4.y;
+          for (int q = 0; q < 4; ++q) {
+            const uint2 gs = sc[4 * h + q];
+            const float f = factor(gs.x), off = nb + __uint_as_float(gs.y);
             const uint64_t f2 = f2_pack(f, f), o2 = f2_pack(off, off);
             uint64_t acc = f2_pack(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               float t0, t1;
-              f2_unpack(f2_fma(f2_pack(sv[half][16 * q + 2 * c], sv[half][16 * q + 2 * c + 1]), f2, o2), t0, t1);
+              f2_unpack(f2_fma(f2_pack(sv[q / 2][16 * (q % 2) + 2 * c], sv[q / 2][16 * (q % 2) + 2 * c + 1]), f2, o2), t0, t1);
               const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
               acc = f2_add(acc, f2_pack(e0, e1));
               const __half2 h2 = __floats2half2_rn(e0, e1);
-              pk[8 * q + c] = *reinterpret_cast<const float *>(&h2);
+              pk[q / 2][8 * (q % 2) + c] = *reinterpret_cast<const float *>(&h2);
             }
             float a0, a1;
             f2_unpack(acc, a0, a1);
-            sum = fmaf(a0 + a1, g4.z, sum);
+            raw += a0 + a1;
+            sum = fmaf(a0 + a1, __uint_as_float(gs.x << 16), sum);
           }
-          tmem_st16_async(tP + 32 * h + 16 * half, pk);
+          const bool high = !(raw <= 32768.f) || m == -INFINITY;
+          if (__builtin_expect(tries || !__any_sync(0xffffffffu, high), 1)) break;  // warp-uniform
+          if (!await_pv()) { ok = false; break; }
+          float tmax = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float *s16 = sv[q / 2] + 16 * (q % 2);
+            float y = s16[0];
+#pragma unroll
+            for (int c = 1; c < 15; c += 2) y = fmax3(y, s16[c], s16[c + 1]);
+            const uint2 gs = sc[4 * h + q];
+            tmax = fmaxf(tmax, fmaf(fmaxf(y, s16[15]), factor(gs.x), __uint_as_float(gs.y)));
+          }
+          const bool up = high && tmax > m;
+          const float base = up ? floorf(tmax) : m;
+          float alpha = 1.f;
+          if (up) alpha = m > -INFINITY ? exponent_scale(static_cast<int>(fmaxf(m - base, -126.f))) : 0.f;
+          m = base;
+          l *= alpha;
+          if (h == 1) {  // the first half's weights lie in tensor memory already
+            float o[32];
+            tmem_wait_st();
+            tmem_ld32(tP, o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&o[c]));
+              const __half2 x = __floats2half2_rn(y.x * alpha, y.y * alpha);  // alpha itself may lie below f16
+              o[c] = *reinterpret_cast<const float *>(&x);
+            }
+            tmem_st32(tP, o);
+          }
+          if (j > 0) {
+#pragma unroll
+            for (int c0 = 0; c0 < DH; c0 += 32) {
+              float o[32];
+              tmem_ld32(tO + c0, o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= alpha;
+              tmem_st32(tO + c0, o);
+            }
+          }
         }
-      };
-      if (warp_live) exp_half(NH - 1);
-      if constexpr (NH == 2) {
+        if (ok) l += sum;
+        if (!ok || !await_pv()) { ok = false; break; }
         if (warp_live) {
-          tmem_ld32(tS, sv[0]);
-          tmem_ld32(tS + 32, sv[1]);
-        }
-        release();
-        if (warp_live) {
-          mask_half(0);
-          exp_half(0);
+          tmem_st16_async(tP + 32 * h, pk[0]);
+          tmem_st16_async(tP + 32 * h + 16, pk[1]);
         }
       }
+      if (!ok) break;
       if (warp_live) tmem_wait_st();
-      l = fmaf(l, alpha, sum);
-      if (warp_live && j > 0 && __any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int c0 = 0; c0 < DH; c0 += 32) {
-          float o[32];
-          tmem_ld32(tO + c0, o);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] *= alpha;
-          tmem_st32(tO + c0, o);
-        }
-      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[t]);
+      __syncwarp();
     }
-    if (ok && T > 0 && !warp_wait_together(&o_done[t], (T - 1) & 1, abort_flag)) ok = false;
+    if (ok && T > 0 && unlikely(!wait_bounded(&o_done[t], (T - 1) & 1, abort_flag))) ok = false;
     tc_fence_after();
     // tcgen05.ld is warp-collective: every lane executes it, rows past the last
     // node only skip the global writes
@@ -620,10 +681,8 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
   // Equal shares again, only now that every warp has left its role: a warp that
   // took its registers back earlier would take them from the softmax warps'
   // share, which would then wait for ever.
-  if constexpr (Sh::kShareRegs) {
-    if (warp < kConvertWarp) regs_dec<Sh::kLaunchRegs>();
-    else regs_inc<Sh::kLaunchRegs>();
-  }
+  if (warp < kConvertWarp) regs_dec<Sh::kLaunchRegs>();
+  else regs_inc<Sh::kLaunchRegs>();
   if (*abort_flag) {
     if (tid == 0) report(a.status, EAGLE_ERR_TIMEOUT);
     volatile int never = 0;
@@ -631,9 +690,11 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       mma_commit(teardown);  // every MMA issued so far completes before tensor memory is released
       mbar_wait(teardown, 0, &never, 100000000ull);
     }
-    if (warp == kProducerWarp && lane == 0) {
+    if (warp >= kProducerWarp && warp < kMmaWarp && lane == 0) {
       // copies still in flight complete before shared memory is released
-      for (int j = max(0, issued - S8); j < issued; ++j) mbar_wait(&f8_full[j % S8], (j / S8) & 1, &never, 100000000ull);
+      const uint64_t *full = bytes_full + (warp - kProducerWarp) * S8;
+      for (int j = max(0, issued - S8); j < issued; ++j)
+        mbar_wait(const_cast<uint64_t *>(&full[j % S8]), (j / S8) & 1, &never, 100000000ull);
     }
     __syncthreads();
   }
@@ -646,7 +707,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
       const int t = warp >> 2, qtr = warp & 3, rl = t * 128 + qtr * 32 + lane;
       const uint32_t tO = tmem + (static_cast<uint32_t>(qtr * 32) << 16) + Sh::kColO + t * DH;
       const bool have = part_have && !*abort_flag;
-      float4 *prow = reinterpret_cast<float4 *>(sKV) + rl * (DH / 4);
+      float4 *prow = reinterpret_cast<float4 *>(sK) + rl * (DH / 4);
 #pragma unroll
       for (int c0 = 0; c0 < DH; c0 += 32) {
         float o[32];
@@ -669,7 +730,7 @@ __global__ void __launch_bounds__((MT + 2) * 128, OCC)
     float *slot = a.part + (cl * a.S + split) * static_cast<int64_t>(a.slot_rows) * (DH + 2);
     for (int idx = tid; idx < nr * NV; idx += Sh::kThreads) {
       const int r = idx / NV, c = idx % NV;
-      reinterpret_cast<float4 *>(slot)[idx] = reinterpret_cast<const float4 *>(sKV)[r * NV + (c ^ (r & 7))];
+      reinterpret_cast<float4 *>(slot)[idx] = reinterpret_cast<const float4 *>(sK)[r * NV + (c ^ (r & 7))];
     }
     for (int r = tid; r < nr; r += Sh::kThreads)
       reinterpret_cast<float2 *>(slot + static_cast<int64_t>(a.slot_rows) * DH)[r] = reinterpret_cast<const float2 *>(sQ)[r];
@@ -749,17 +810,15 @@ static cudaError_t launch_kv8_v(const CUtensorMap *maps, const Kv8Args &a, const
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = set_smem_limit_once(kernel, Sh::kSmem, configured);
   if (e != cudaSuccess) return e;
-  if constexpr (Sh::kShareRegs) {
-    // the warpgroups' shares add up only if a thread is launched with these
-    static std::atomic<int> regs{0};
-    if (regs.load(std::memory_order_relaxed) == 0) {
-      cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, kernel);
-      if (e != cudaSuccess) return e;
-      regs.store(fa.numRegs, std::memory_order_relaxed);
-    }
-    if (regs.load(std::memory_order_relaxed) != Sh::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  // the warpgroups' shares add up only if a thread is launched with these
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
   }
+  if (regs.load(std::memory_order_relaxed) != Sh::kLaunchRegs) return cudaErrorInvalidConfiguration;
   const dim3 grid(p.S, p.mgroups, a.B * a.Hkv);
   if constexpr (MERGE == 2) {
     e = launch_chained(kernel, grid, dim3(Sh::kThreads), Sh::kSmem, st, maps[0], maps[1], a);
