@@ -8,10 +8,10 @@
 // q = 2^a q', k = 2^ke k', v = 2^ve v' (ke, ve of a group of 16 keys, which no
 // page splits):
 //   s  = (scale log2e 2^(a+ke)) <q', k'>           score, base 2
-//   P' = 2^(s + ve - m + 6),  m >= max(s + ve) - 9     in f16
+//   P' = 2^(s + ve - m + 6),  m >= max(s + ve) - 8     in f16
 //   O  = sum P' v',  l = sum_groups 2^-ve sum P',  out = O / l,
 //   lse = ln 2 (m - 6 + log2 l)
-// so P' stays below 2^15 and is rounded to 11 bits (bf16 would leave 8), down
+// so P' stays below 2^14 and is rounded to 11 bits (bf16 would leave 8), down
 // to 2^-20 of the row's largest; smaller ones are off by up to 2^-31 of it
 // (f16's subnormals).  Neither K nor V is rounded at all.
 //
@@ -506,134 +506,125 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     const uint32_t tP = tmem + lane_base + Sh::kColP + t * (NK / 2);
     const uint32_t tO = tmem + lane_base + Sh::kColO + t * DH;
     const uint64_t *mrow = a.mask + (static_cast<int64_t>(b) * n + i) * a.W;
-    // m is the exponent base of this row's P' and O, a whole number, so that
-    // raising it scales by powers of two.  No maximum is taken per tile: the
-    // weights are made with the base at hand, and their sum says whether one came
-    // near f16's end (above 2^15: no weight below that sum is).  Only then, and
-    // for the first keys, the maximum is found, the base raised to it, and what was
-    // made with the old one scaled or made again.
+    // m is the exponent base of this row's P' and O; it is raised only when the
+    // row maximum exceeds it by more than 8, so O is rescaled rarely.
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < T && ok; ++j) {
+    for (int j = 0; j < T; ++j) {
       if (unlikely(!wait_bounded(&s_full[t], j & 1, abort_flag))) { ok = false; break; }
       tc_fence_after();
       const int jp = j - pfx0;
       const bool prefix = jp >= 0 && jp < np;
       // a tree tile's ve is its V converters' (the prefix's scales came with K)
-      if (!prefix && unlikely(!wait_bounded(&tile_full[SF + j % SF], (j / SF) & 1, abort_flag))) { ok = false; break; }
+      if (unlikely(!prefix) && unlikely(!wait_bounded(&tile_full[SF + j % SF], (j / SF) & 1, abort_flag))) { ok = false; break; }
       const uint2 *sc = scales + (j % Sh::kScaleSlots) * GR;
       const bool dense = prefix && (p0 + jp + 1) * NK <= L;  // no key of the tile is masked
-      bool pv_done = j == 0;
-      const auto await_pv = [&] {  // P.V of the previous tile: P is free, O is final for it
-        if (!pv_done) {
-          if (unlikely(!wait_bounded(&o_done[t], (j - 1) & 1, abort_flag))) return false;
-          tc_fence_after();
-          pv_done = true;
-        }
-        return true;
-      };
       // never 0: it multiplies the -inf of masked keys
       const auto factor = [&](uint32_t s) { return fmaxf(row_scale * __uint_as_float(s & 0xffff0000u), 1.2e-38f); };
-      // one copy of the code for both halves and both tries: with the other roles'
-      // loops it has to stay in the instruction cache
-#pragma unroll 1
-      for (int h = 0; h < NH; ++h) {
-        float sv[2][32], pk[2][16];
-        if (warp_live) tmem_ld32x2(tS + 64 * h, sv[0], sv[1]);
-        if (h == NH - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
-          __syncwarp();  // or lane 0 would make its weights apart from the others
+      // S in halves of 64 columns.  With two halves the first is read once for
+      // the maximum and again for its exponentials, after the second's: 64
+      // scores in registers at a time instead of 128.
+      float sv[2][32];
+      const auto mask_half = [&](int h) {
+        uint64_t keep;
+        if (prefix) {
+          const int valid = min(NK, L - (p0 + jp) * NK) - 64 * h;
+          keep = valid >= 64 ? ~0ull : (valid <= 0 ? 0ull : ((1ull << valid) - 1ull));
+        } else {
+          const int w = (j - tree0) * NH + h;
+          keep = (row_ok && w < a.W) ? mrow[w] : 0ull;
         }
-        if (unlikely(warp_live && !dense)) {
-          uint64_t keep;
-          if (prefix) {
-            const int valid = min(NK, L - (p0 + jp) * NK) - 64 * h;
-            keep = valid >= 64 ? ~0ull : (valid <= 0 ? 0ull : ((1ull << valid) - 1ull));
-          } else {
-            const int w = (j - tree0) * NH + h;
-            keep = (row_ok && w < a.W) ? mrow[w] : 0ull;
-          }
 #pragma unroll
-          for (int c = 0; c < 64; ++c) sv[c / 32][c % 32] = ((keep >> c) & 1ull) ? sv[c / 32][c % 32] : -INFINITY;
+        for (int c = 0; c < 64; ++c) sv[c / 32][c % 32] = ((keep >> c) & 1ull) ? sv[c / 32][c % 32] : -INFINITY;
+      };
+      const auto half_max = [&](int h) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float *s16 = sv[q / 2] + 16 * (q % 2);
+          float y = s16[0];
+#pragma unroll
+          for (int c = 1; c < 15; c += 2) y = fmax3(y, s16[c], s16[c + 1]);
+          const uint2 gs = sc[4 * h + q];
+          x = fmaxf(x, fmaf(fmaxf(y, s16[15]), factor(gs.x), __uint_as_float(gs.y)));
         }
-        float raw = 0.f, sum = 0.f;  // of P', and over the groups' 2^ve
-#pragma unroll 1
-        for (int tries = 0; warp_live; ++tries) {
-          const float nb = kBias - (m > -INFINITY ? m : 0.f);
-          raw = sum = 0.f;
+        return x;
+      };
+      const auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
+        __syncwarp();  // or lane 0 would work on apart from the others
+      };
+      float tmax = -INFINITY;
+      if (NH == 2 && warp_live) {
+        tmem_ld32x2(tS, sv[0], sv[1]);
+        if (unlikely(!dense)) mask_half(0);
+        tmax = half_max(0);
+      }
+      if (warp_live) tmem_ld32x2(tS + 64 * (NH - 1), sv[0], sv[1]);
+      if (NH == 1) release();
+      if (warp_live) {
+        if (unlikely(!dense)) mask_half(NH - 1);
+        tmax = fmaxf(tmax, half_max(NH - 1));
+      }
+      const bool raise = tmax > m + 8.f;
+      const float base = raise ? tmax : m;
+      const float alpha = raise ? ex2_approx(m - tmax) : 1.f;  // m = -inf gives 0
+      m = base;
+      if (j > 0) {  // P.V of the previous tile is done: P is free, O is final for it
+        if (unlikely(!wait_bounded(&o_done[t], (j - 1) & 1, abort_flag))) { ok = false; break; }
+        tc_fence_after();
+      }
+      const float nb = kBias - (base > -INFINITY ? base : 0.f);
+      float sum = 0.f;
+      const auto exp_half = [&](int h) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint2 gs = sc[4 * h + q];
+        for (int half = 0; half < 2; ++half) {
+          float pk[16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint2 gs = sc[4 * h + 2 * half + q];
             const float f = factor(gs.x), off = nb + __uint_as_float(gs.y);
             const uint64_t f2 = f2_pack(f, f), o2 = f2_pack(off, off);
             uint64_t acc = f2_pack(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               float t0, t1;
-              f2_unpack(f2_fma(f2_pack(sv[q / 2][16 * (q % 2) + 2 * c], sv[q / 2][16 * (q % 2) + 2 * c + 1]), f2, o2), t0, t1);
+              f2_unpack(f2_fma(f2_pack(sv[half][16 * q + 2 * c], sv[half][16 * q + 2 * c + 1]), f2, o2), t0, t1);
               const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
               acc = f2_add(acc, f2_pack(e0, e1));
               const __half2 h2 = __floats2half2_rn(e0, e1);
-              pk[q / 2][8 * (q % 2) + c] = *reinterpret_cast<const float *>(&h2);
+              pk[8 * q + c] = *reinterpret_cast<const float *>(&h2);
             }
             float a0, a1;
             f2_unpack(acc, a0, a1);
-            raw += a0 + a1;
             sum = fmaf(a0 + a1, __uint_as_float(gs.x << 16), sum);
           }
-          const bool high = !(raw <= 32768.f) || m == -INFINITY;
-          if (__builtin_expect(tries || !__any_sync(0xffffffffu, high), 1)) break;  // warp-uniform
-          if (!await_pv()) { ok = false; break; }
-          float tmax = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float *s16 = sv[q / 2] + 16 * (q % 2);
-            float y = s16[0];
-#pragma unroll
-            for (int c = 1; c < 15; c += 2) y = fmax3(y, s16[c], s16[c + 1]);
-            const uint2 gs = sc[4 * h + q];
-            tmax = fmaxf(tmax, fmaf(fmaxf(y, s16[15]), factor(gs.x), __uint_as_float(gs.y)));
-          }
-          const bool up = high && tmax > m;
-          const float base = up ? floorf(tmax) : m;
-          float alpha = 1.f;
-          if (up) alpha = m > -INFINITY ? exponent_scale(static_cast<int>(fmaxf(m - base, -126.f))) : 0.f;
-          m = base;
-          l *= alpha;
-          if (h == 1) {  // the first half's weights lie in tensor memory already
-            float o[32];
-            tmem_wait_st();
-            tmem_ld32(tP, o);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&o[c]));
-              const __half2 x = __floats2half2_rn(y.x * alpha, y.y * alpha);  // alpha itself may lie below f16
-              o[c] = *reinterpret_cast<const float *>(&x);
-            }
-            tmem_st32(tP, o);
-          }
-          if (j > 0) {
-#pragma unroll
-            for (int c0 = 0; c0 < DH; c0 += 32) {
-              float o[32];
-              tmem_ld32(tO + c0, o);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] *= alpha;
-              tmem_st32(tO + c0, o);
-            }
-          }
+          tmem_st16_async(tP + 32 * h + 16 * half, pk);
         }
-        if (ok) l += sum;
-        if (!ok || !await_pv()) { ok = false; break; }
+      };
+      if (warp_live) exp_half(NH - 1);
+      if constexpr (NH == 2) {
+        if (warp_live) tmem_ld32x2(tS, sv[0], sv[1]);
+        release();
         if (warp_live) {
-          tmem_st16_async(tP + 32 * h, pk[0]);
-          tmem_st16_async(tP + 32 * h + 16, pk[1]);
+          if (unlikely(!dense)) mask_half(0);
+          exp_half(0);
         }
       }
-      if (!ok) break;
       if (warp_live) tmem_wait_st();
+      l = fmaf(l, alpha, sum);
+      if (unlikely(warp_live && j > 0 && __any_sync(0xffffffffu, raise))) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < DH; c0 += 32) {
+          float o[32];
+          tmem_ld32(tO + c0, o);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] *= alpha;
+          tmem_st32(tO + c0, o);
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[t]);
