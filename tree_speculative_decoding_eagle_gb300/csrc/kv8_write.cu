@@ -26,29 +26,30 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
   else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
 }
 
-// 16 elements of a row as floats.
-template <typename T> __device__ __forceinline__ void load16(const T *p, float (&x)[16]);
-template <> __device__ __forceinline__ void load16<float>(const float *p, float (&x)[16]) {
+// 16 elements of a row, as loaded and as floats.
+template <typename T> struct Chunk {
+  static constexpr int kVecs = 16 / VecTraits<T>::kElems;
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = ld_stream16(p + 4 * i);
-    x[4 * i] = __uint_as_float(v.x); x[4 * i + 1] = __uint_as_float(v.y);
-    x[4 * i + 2] = __uint_as_float(v.z); x[4 * i + 3] = __uint_as_float(v.w);
+    for (int i = 0; i < kVecs; ++i) v[i] = ld_stream16(p + i * VecTraits<T>::kElems);
   }
-}
-template <> __device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[16]) {
+  __device__ __forceinline__ void floats(float (&x)[16]) const {
+    constexpr int E = VecTraits<T>::kElems;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = ld_stream16(p + 8 * i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < kVecs; ++i) {
+      float y[E];
+      VecTraits<T>::unpack(v[i], y);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = bf16_lo(w[j]);
-      x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+      for (int e = 0; e < E; ++e) x[i * E + e] = y[e];
     }
   }
-}
+};
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// Chunks a thread keeps between the two looks at a run (the largest magnitude,
+// then the rounding); a longer run's others are read again, from L2.
+constexpr int kHeld = 4;
 
 // One run: rows 0..count-1 (row_of gives their source) into rows
 // first..first+count-1 of a page of one head.  `red` is the team's shared
@@ -57,18 +58,32 @@ template <typename T, typename RowOf>
 __device__ __forceinline__ void write_run(RowOf row_of, int count, uint8_t *page, float *scale, int first, int dh,
                                           int team, int warps, int tw, float *red, int32_t *status) {
   const int lane = threadIdx.x & 31, tt = tw * 32 + lane, nt = warps * 32;
-  const int cpr = dh / 16;  // 16-element chunks a row
+  const int cpr = dh / 16, chunks = count * cpr;  // 16-element chunks a row, of the run
+  const auto source = [&](int c) { return row_of(c / cpr) + (c % cpr) * 16; };
+  Chunk<T> held[kHeld];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (tt + u * nt < chunks) held[u].load(source(tt + u * nt));
+  const float s_old = first > 0 ? *scale : 1.f;
   float amax = 0.f;
   bool odd = false;
-  for (int c = tt; c < count * cpr; c += nt) {
+  const auto look = [&](const Chunk<T> &k) {
     float x[16];
-    load16<T>(row_of(c / cpr) + (c % cpr) * 16, x);
+    k.floats(x);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const bool fin = is_finite(x[i]);
       odd |= !fin;
       amax = fmaxf(amax, fin ? fabsf(x[i]) : 0.f);
     }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (tt + u * nt < chunks) look(held[u]);
+  for (int c = tt + kHeld * nt; c < chunks; c += nt) {
+    Chunk<T> k;
+    k.load(source(c));
+    look(k);
   }
   amax = warp_max(amax);
   if (warps > 1) {
@@ -78,16 +93,16 @@ __device__ __forceinline__ void write_run(RowOf row_of, int count, uint8_t *page
   }
   int e = block_exponent(amax), e_old = e;
   if (first > 0) {
-    e_old = scale_exponent(*scale);
+    e_old = scale_exponent(s_old);
     e = max(e, e_old);
   }
   team_sync(team, warps);  // every thread has the page's scale (and red) before it changes
   if (tt == 0) *scale = exponent_scale(e);
   if (odd || amax > 448.f * exponent_scale(kScaleMax)) report(status, EAGLE_ERR_INVALID);
   const float inv = exponent_scale(-e);
-  for (int c = tt; c < count * cpr; c += nt) {
+  const auto round_to_page = [&](const Chunk<T> &k, int c) {
     float x[16];
-    load16<T>(row_of(c / cpr) + (c % cpr) * 16, x);
+    k.floats(x);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -96,8 +111,15 @@ __device__ __forceinline__ void write_run(RowOf row_of, int count, uint8_t *page
       for (int j = 0; j < 4; ++j) y[j] = is_finite(x[4 * i + j]) ? x[4 * i + j] * inv : __uint_as_float(0x7fffffffu);
       w[i] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
     }
-    *reinterpret_cast<uint4 *>(page + static_cast<int64_t>(first + c / cpr) * dh + (c % cpr) * 16) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(page + static_cast<int64_t>(first) * dh + static_cast<int64_t>(c) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (tt + u * nt < chunks) round_to_page(held[u], tt + u * nt);
+  for (int c = tt + kHeld * nt; c < chunks; c += nt) {
+    Chunk<T> k;
+    k.load(source(c));
+    round_to_page(k, c);
   }
   if (e > e_old) {  // the page's earlier rows at the new scale (rare: a new largest magnitude)
     const float f = exp2f(static_cast<float>(e_old - e));
@@ -271,10 +293,18 @@ cudaError_t launch_kv8_append(const void *k, const void *v, int dtype, int T, in
                               int num_sms, cudaStream_t st) {
   AppendArgs a = {k, v, token_stride, head_stride, slot_map, k_pages, v_pages, k_scale, v_scale,
                   T, Hkv, dh, log2_page(page_size), num_pages, 0, 0, status};
-  // a team of a warp for every 16 rows of a page
-  a.warps = page_size >= 128 ? 8 : page_size / 16;
-  a.block = page_size < 256 ? page_size : 256;
-  while (a.block > 4 && static_cast<int64_t>((T + a.block - 1) / a.block) * Hkv * 2 < 4ll * num_sms) a.block /= 2;
+  // A team takes a run.  Long inputs: enough warps that a thread holds a whole
+  // page's share (kHeld chunks), and as many pages a CTA as it has teams.  Few
+  // rows (single tokens mostly): a warp a run, and CTAs cut down until the SMs
+  // have four each.
+  const int64_t rows = static_cast<int64_t>(T) * Hkv * 2;
+  const int page_warps = page_size * (dh / 16) / (32 * kHeld);
+  a.warps = 1;
+  if (rows > 32ll * num_sms)
+    while (a.warps < kWriteWarps && a.warps < page_warps) a.warps *= 2;
+  const int teams = kWriteWarps / a.warps;
+  a.block = teams * page_size;
+  while (a.block > teams && static_cast<int64_t>((T + a.block - 1) / a.block) * Hkv * 2 < 4ll * num_sms) a.block /= 2;
   const dim3 grid((T + a.block - 1) / a.block, Hkv, 2);
   return dtype == EAGLE_BF16 ? launch_chained(kv8_append_kernel<__nv_bfloat16>, grid, dim3(kWriteWarps * 32), 0, st, a)
                              : launch_chained(kv8_append_kernel<float>, grid, dim3(kWriteWarps * 32), 0, st, a);

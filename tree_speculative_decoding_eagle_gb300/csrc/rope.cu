@@ -28,15 +28,8 @@ struct RopeArgs {
   float factor;
 };
 
-template <typename T> __device__ __forceinline__ float load_f(const T *p) { return static_cast<float>(*p); }
-
-// One pair (or one copied element pair) per thread step: any rot_dim.
-template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
-  __shared__ float2 cs[256];
-  const int node = blockIdx.x, b = node / a.n, i = node % a.n;
-  pdl_wait();
-  const int pos = (a.pos_base ? a.pos_base[b] : 0) + (a.pos_off ? a.pos_off[node] : i) + a.shift;
+// cos and sin (times the factor) of the node's angles into shared memory.
+__device__ __forceinline__ void node_turns(const RopeArgs &a, int pos, float2 *cs) {
   for (int j = threadIdx.x; j < a.half; j += kRopeThreads) {
     double t = a.inv_freq[j] * 0.15915494309189533577;  // turns per position
     t -= rint(t);
@@ -46,30 +39,134 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
     sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &sn, &c);
     cs[j] = make_float2(c * a.factor, sn * a.factor);
   }
+}
+__device__ __forceinline__ int position_of(const RopeArgs &a, int node, int b, int i) {
+  return (a.pos_base ? a.pos_base[b] : 0) + (a.pos_off ? a.pos_off[node] : i) + a.shift;
+}
+// Head h of a node: where it is read and written, and whether it turns.
+template <typename T>
+__device__ __forceinline__ bool head_of(const RopeArgs &a, int node, int b, int i, int h, const T *&src, T *&dst) {
+  if (h < a.Hq) {
+    src = reinterpret_cast<const T *>(a.q) + node * a.ld_q + static_cast<int64_t>(h) * a.dh;
+    dst = reinterpret_cast<T *>(a.q_out) + (static_cast<int64_t>(node) * a.Hq + h) * a.dh;
+    return true;
+  }
+  const bool is_k = h < a.Hq + a.Hkv;
+  const int g = h - a.Hq - (is_k ? 0 : a.Hkv);
+  src = reinterpret_cast<const T *>(is_k ? a.k : a.v) + node * (is_k ? a.ld_k : a.ld_v) + static_cast<int64_t>(g) * a.dh;
+  dst = reinterpret_cast<T *>(is_k ? a.k_tree : a.v_tree) + ((static_cast<int64_t>(b) * a.Hkv + g) * a.n + i) * a.dh;
+  return is_k;
+}
+
+template <typename T> __device__ __forceinline__ uint4 pack_vec(const float (&x)[VecTraits<T>::kElems]);
+template <> __device__ __forceinline__ uint4 pack_vec<float>(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+template <> __device__ __forceinline__ uint4 pack_vec<__nv_bfloat16>(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16-byte vectors.  An item of a head is what one thread turns: two vectors half
+// of rot_dim apart, or (interleaved) one vector of whole pairs, or one vector
+// that is copied; a head of v is copied up to two vectors an item.  `lanes` (a
+// power of two) threads share a head, kRopeItems heads' items are requested
+// before the turns are computed, so their latencies overlap.
+constexpr int kRopeItems = 2;
+
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(RopeArgs a, int log_lanes, int items) {
+  constexpr int E = VecTraits<T>::kElems;
+  __shared__ float2 cs[256];
+  const int node = blockIdx.x, b = node / a.n, i = node % a.n;
+  const int it = threadIdx.x & ((1 << log_lanes) - 1);
+  const int H = a.Hq + (a.v ? 2 : 1) * a.Hkv;
+  const int h0 = (blockIdx.y * kRopeItems << (8 - log_lanes)) + (threadIdx.x >> log_lanes), dh = 1 << (8 - log_lanes);
+  pdl_wait();
+  const int pos = position_of(a, node, b, i);
+  const int turning = INTER ? 2 * a.half / E : a.half / E;  // items that turn
+  uint4 x[kRopeItems][2];
+  T *dst[kRopeItems];
+  int c0[kRopeItems], c1[kRopeItems];  // the item's columns; c1 < 0: one vector
+  bool turn[kRopeItems];
+#pragma unroll
+  for (int u = 0; u < kRopeItems; ++u) {
+    const int h = h0 + u * dh;
+    dst[u] = nullptr;
+    if (h >= H || it >= items) continue;
+    const T *src;
+    turn[u] = head_of(a, node, b, i, h, src, dst[u]);
+    c1[u] = -1;
+    if (!turn[u]) {
+      c0[u] = it * E;
+      if ((it + items) * E < a.dh) c1[u] = (it + items) * E;
+    } else if (it < turning) {
+      c0[u] = it * E;
+      if (!INTER) c1[u] = a.half + it * E;
+    } else {
+      c0[u] = 2 * a.half + (it - turning) * E;
+      turn[u] = false;
+    }
+    x[u][0] = ld_stream16(src + c0[u]);
+    if (c1[u] >= 0) x[u][1] = ld_stream16(src + c1[u]);
+  }
+  node_turns(a, pos, cs);
   __syncthreads();
   pdl_trigger();
-  const int H = a.Hq + 2 * a.Hkv, pairs = a.dh / 2;
+#pragma unroll
+  for (int u = 0; u < kRopeItems; ++u) {
+    if (!dst[u]) continue;
+    if (turn[u]) {
+      float f0[E], f1[E];
+      VecTraits<T>::unpack(x[u][0], f0);
+      if constexpr (INTER) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 w = cs[c0[u] / 2 + e / 2];
+          f1[e] = f0[e] * w.x - f0[e + 1] * w.y;
+          f1[e + 1] = f0[e + 1] * w.x + f0[e] * w.y;
+        }
+        x[u][0] = pack_vec<T>(f1);
+      } else {
+        VecTraits<T>::unpack(x[u][1], f1);
+        float r0[E], r1[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float2 w = cs[c0[u] + e];
+          r0[e] = f0[e] * w.x - f1[e] * w.y;
+          r1[e] = f1[e] * w.x + f0[e] * w.y;
+        }
+        x[u][0] = pack_vec<T>(r0);
+        x[u][1] = pack_vec<T>(r1);
+      }
+    }
+    *reinterpret_cast<uint4 *>(dst[u] + c0[u]) = x[u][0];
+    if (c1[u] >= 0) *reinterpret_cast<uint4 *>(dst[u] + c1[u]) = x[u][1];
+  }
+}
+
+// Any even rot_dim: one pair (or two copied elements) a thread step.
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) rope_pair_kernel(RopeArgs a) {
+  __shared__ float2 cs[256];
+  const int node = blockIdx.x, b = node / a.n, i = node % a.n;
+  pdl_wait();
+  node_turns(a, position_of(a, node, b, i), cs);
+  __syncthreads();
+  pdl_trigger();
+  const int H = a.Hq + (a.v ? 2 : 1) * a.Hkv, pairs = a.dh / 2;
   for (int idx = blockIdx.y * kRopeThreads + threadIdx.x; idx < H * pairs; idx += gridDim.y * kRopeThreads) {
     const int h = idx / pairs, j = idx % pairs;
     const T *src;
     T *dst;
-    bool turn = true;
-    if (h < a.Hq) {
-      src = reinterpret_cast<const T *>(a.q) + node * a.ld_q + static_cast<int64_t>(h) * a.dh;
-      dst = reinterpret_cast<T *>(a.q_out) + (static_cast<int64_t>(node) * a.Hq + h) * a.dh;
-    } else if (h < a.Hq + a.Hkv) {
-      const int g = h - a.Hq;
-      src = reinterpret_cast<const T *>(a.k) + node * a.ld_k + static_cast<int64_t>(g) * a.dh;
-      dst = reinterpret_cast<T *>(a.k_tree) + ((static_cast<int64_t>(b) * a.Hkv + g) * a.n + i) * a.dh;
-    } else {
-      if (!a.v) continue;
-      const int g = h - a.Hq - a.Hkv;
-      src = reinterpret_cast<const T *>(a.v) + node * a.ld_v + static_cast<int64_t>(g) * a.dh;
-      dst = reinterpret_cast<T *>(a.v_tree) + ((static_cast<int64_t>(b) * a.Hkv + g) * a.n + i) * a.dh;
-      turn = false;
-    }
+    const bool turn = head_of(a, node, b, i, h, src, dst);
     const bool rot = turn && j < a.half;
-    const int c0 = rot ? (a.interleaved ? 2 * j : j) : (turn ? 2 * a.half + 2 * (j - a.half) : 2 * j);
+    const int c0 = rot ? (a.interleaved ? 2 * j : j) : 2 * j;
     const int c1 = rot && !a.interleaved ? j + a.half : c0 + 1;
     const T x0 = src[c0], x1 = src[c1];
     if (rot) {
@@ -84,16 +181,31 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   }
 }
 
+template <typename T>
+static cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
+  constexpr int E = VecTraits<T>::kElems;
+  const int H = a.Hq + (a.v ? 2 : 1) * a.Hkv;
+  // whole vectors turn: in two halves rot_dim/2, interleaved rot_dim divides into vectors
+  if ((a.interleaved ? 2 * a.half : a.half) % E == 0) {
+    const int items = a.interleaved ? a.dh / E : a.half / E + (a.dh - 2 * a.half) / E;
+    int log_lanes = 0;
+    while ((1 << log_lanes) < items) ++log_lanes;
+    const int heads = kRopeItems << (8 - log_lanes);  // a CTA (log2 of its threads: 8)
+    const dim3 grid(a.B * a.n, (H + heads - 1) / heads);
+    return a.interleaved ? launch_chained(rope_vec_kernel<T, true>, grid, dim3(kRopeThreads), 0, st, a, log_lanes, items)
+                         : launch_chained(rope_vec_kernel<T, false>, grid, dim3(kRopeThreads), 0, st, a, log_lanes, items);
+  }
+  const dim3 grid(a.B * a.n, (H * a.dh / 2 + kRopeThreads * 8 - 1) / (kRopeThreads * 8));
+  return launch_chained(rope_pair_kernel<T>, grid, dim3(kRopeThreads), 0, st, a);
+}
+
 cudaError_t launch_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv, int dh,
                         int64_t ld_q, int64_t ld_k, int64_t ld_v, const double *inv_freq, int rot_dim,
                         int interleaved, float factor, const int32_t *pos_base, const int32_t *pos_off, int shift,
                         void *q_out, void *k_tree, void *v_tree, cudaStream_t st) {
   RopeArgs a = {q, k, v, q_out, k_tree, v_tree, B, n, Hq, Hkv, dh, rot_dim / 2, interleaved, shift,
                 ld_q, ld_k, ld_v, inv_freq, pos_base, pos_off, factor};
-  const int items = (Hq + 2 * Hkv) * dh / 2;
-  const dim3 grid(B * n, (items + kRopeThreads * 8 - 1) / (kRopeThreads * 8));
-  return dtype == EAGLE_BF16 ? launch_chained(rope_kernel<__nv_bfloat16>, grid, dim3(kRopeThreads), 0, st, a)
-                             : launch_chained(rope_kernel<float>, grid, dim3(kRopeThreads), 0, st, a);
+  return dtype == EAGLE_BF16 ? launch_rope_t<__nv_bfloat16>(a, st) : launch_rope_t<float>(a, st);
 }
 
 // Host: the frequencies.

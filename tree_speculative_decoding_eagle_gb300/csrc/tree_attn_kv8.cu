@@ -72,8 +72,8 @@ struct Kv8Shape {
   // Registers: what a thread is launched with, and the warpgroups' shares of
   // it (softmax, converters, producers and MMA); they add up to the launch's.
   static constexpr int kLaunchRegs = 65536 / (kThreads * OCC) / 8 * 8;
-  static constexpr int kRegsOther = kLaunchRegs < 80 ? 32 : 48;
-  static constexpr int kRegsConvert = kLaunchRegs < 80 ? 40 : (kConvertGroups == 1 ? 88 : 56);
+  static constexpr int kRegsOther = kLaunchRegs < 80 ? 40 : 64;
+  static constexpr int kRegsConvert = kLaunchRegs < 80 ? 40 : (kConvertGroups == 1 ? 72 : 56);
   static constexpr int kRegsLeft = (kGroupsAll * kLaunchRegs - kRegsOther - kConvertGroups * kRegsConvert) / MT / 8 * 8;
   static constexpr int kRegsSoftmax = kRegsLeft > 208 ? 208 : kRegsLeft;
   static_assert(QR == 128 || (QR == 64 && MT == 1), "64-row regions with one M-tile only");
@@ -748,8 +748,12 @@ size_t attn_kv8_few_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int L
 cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void *v_pages, int dh, void *ws, int num_sms,
                                      cudaStream_t st);
 
-// Query rows of a KV head up to which the few-row kernel runs.
-constexpr int kFewRows = 64;
+// Query rows of a KV head up to which the few-row kernel runs: its warp-level
+// MMAs cost a row tile of 16 what the bytes cost at two tiles.  Measured (us,
+// few-row kernel / this one): 30 rows, dh 128, 320 heads of U[1024, 4096] keys
+// 149 / 170; 20 rows, dh 64, 64 such heads 27 / 34; 51 rows, dh 128, 320 heads
+// 208 / 166; 56 rows, dh 64, 256 heads of 4096 keys 145 / 88.
+constexpr int kFewRows = 32;
 
 struct Kv8Plan {
   int MT, NK, QR, mgroups, S, ctas_per_sm;

@@ -16,7 +16,7 @@
 //   * P stays in the accumulators' layout, which is the A operand's;
 //   * the running maximum is looked at across a quad only when a lane's own
 //     exceeds it by more than 2^8.
-// A CTA of four warps is KG = 4 / RG groups of keys times RG = 1, 2 or 4 tiles of 16
+// A CTA of four warps is KG = 4 / RG groups of keys times RG = 1 or 2 tiles of 16
 // rows; the RG warps of a key group share its ring.  Three CTAs an SM keep up
 // to 192 KB of requests in flight.
 #include "kv8_attn.cuh"
@@ -430,7 +430,7 @@ struct FewPlan {
 // a warp + a CTA's fixed cost in groups).
 static FewPlan few_plan(int B, int rows, int Hkv, int Lmax, int num_sms) {
   FewPlan p;
-  p.RG = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  p.RG = rows <= 16 ? 1 : 2;
   const int KG = 4 / p.RG;
   const int64_t base = static_cast<int64_t>(B) * Hkv, slots = 3ll * num_sms;
   const int64_t groups = (static_cast<int64_t>(Lmax) + 15) / 16;
@@ -492,10 +492,10 @@ cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void 
     return cudaErrorInvalidValue;
   if (dh == 64) {
     if (p.RG == 1) return launch_few_t<64, 1>(maps, a, p, st);
-    return p.RG == 2 ? launch_few_t<64, 2>(maps, a, p, st) : launch_few_t<64, 4>(maps, a, p, st);
+    return launch_few_t<64, 2>(maps, a, p, st);
   }
   if (p.RG == 1) return launch_few_t<128, 1>(maps, a, p, st);
-  return p.RG == 2 ? launch_few_t<128, 2>(maps, a, p, st) : launch_few_t<128, 4>(maps, a, p, st);
+  return launch_few_t<128, 2>(maps, a, p, st);
 }
 
 }  // namespace eagle
