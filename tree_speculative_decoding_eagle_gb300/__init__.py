@@ -412,33 +412,35 @@ def kv_commit(k_tree, v_tree, accept_len, path_nodes, k_cache, v_cache, kv_len, 
 
 # ---- the serving loop around the step: pages, positions, the 8-bit cache ------
 
-def _need(t, name, dtype=None, shape=None, device=None):
-    """t, if it is a contiguous CUDA tensor of that type, shape and device."""
-    if not t.is_cuda:
-        raise EagleError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise EagleError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise EagleError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise EagleError(f"{name} must be on {device}, not {t.device}")
-    if not t.is_contiguous():
-        raise EagleError(f"{name} must be contiguous")
+def _need(t, name, dtype, shape, dev):
+    """Address of t, if it is a contiguous tensor of that type and shape (None:
+    any) on CUDA device number dev."""
+    if t.get_device() != dev or t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous():
+        what = "" if shape is None else f" of shape {tuple(shape)}"
+        raise EagleError(f"{name} must be a contiguous {dtype} CUDA tensor{what} on device {dev}, not {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _maybe(t, name, dtype, shape, device):
-    return None if t is None else _need(t, name, dtype, shape, device)
+def _maybe(t, name, dtype, shape, dev):
+    return None if t is None else _need(t, name, dtype, shape, dev)
 
 
-def _call(what, fn, device, stream, *args):
-    """fn(*args, stream) with `device` current and on its current stream."""
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, s)
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise EagleError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call(what, fn, dev, stream, *args):
+    """fn(*args, stream) with device number `dev` current, on its current stream
+    unless one is given."""
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, s.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, s)
+        with torch.cuda.device(dev):
+            rc = fn(*args, s.cuda_stream)
     if rc:
         _check(rc, what)
 
@@ -454,10 +456,10 @@ def page_map(kv_len, new_len, block_table, page_count, free_pages, free_count, p
     Returns slot_map.  Too few free pages leave everything as it was and set
     `status` to -6."""
     lib = load_library()
-    dev, i32 = kv_len.device, torch.int32
+    dev, i32 = _device_of(kv_len, "kv_len"), torch.int32
     B, max_pages = block_table.shape
     num_pages = free_pages.shape[0]
-    _call("eagle_page_map", lib.eagle_page_map, dev, stream, _need(kv_len, "kv_len", i32, (B,)),
+    _call("eagle_page_map", lib.eagle_page_map, dev, stream, _need(kv_len, "kv_len", i32, (B,), dev),
           _need(new_len, "new_len", i32, (B,), dev), B, page_size, max_pages, num_pages,
           _need(block_table, "block_table", i32, None, dev), _need(page_count, "page_count", i32, (B,), dev),
           _need(free_pages, "free_pages", i32, (num_pages,), dev), _need(free_count, "free_count", i32, (1,), dev),
@@ -472,10 +474,10 @@ def page_release(keep_len, block_table, page_count, free_pages, free_count, page
     uses, a negative length leaves it alone.  The other arrays are those of
     page_map, updated in place."""
     lib = load_library()
-    dev, i32 = keep_len.device, torch.int32
+    dev, i32 = _device_of(keep_len, "keep_len"), torch.int32
     B, max_pages = block_table.shape
     num_pages = free_pages.shape[0]
-    _call("eagle_page_release", lib.eagle_page_release, dev, stream, _need(keep_len, "keep_len", i32, (B,)), B,
+    _call("eagle_page_release", lib.eagle_page_release, dev, stream, _need(keep_len, "keep_len", i32, (B,), dev), B,
           page_size, max_pages, num_pages, _need(block_table, "block_table", i32, None, dev),
           _need(page_count, "page_count", i32, (B,), dev), _need(free_pages, "free_pages", i32, (num_pages,), dev),
           _need(free_count, "free_count", i32, (1,), dev), _maybe(status, "status", i32, None, dev))
@@ -498,8 +500,8 @@ def rope_freqs(rot_dim, theta=10000.0, kind="plain", stretch=1.0, orig_len=4096,
 def _heads(t, name, B, n, dh, dtype, device):
     """Node stride of [B, n, heads, dh] whose heads are dense and whose nodes
     are evenly spaced."""
-    if not t.is_cuda or t.dtype != dtype or t.device != device:
-        raise EagleError(f"{name} must be {dtype} on {device}")
+    if t.get_device() != device or t.dtype != dtype:
+        raise EagleError(f"{name} must be a {dtype} CUDA tensor on device {device}")
     if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != dh:
         raise EagleError(f"{name} must be [B, n, heads, dh]")
     sb, sn, sh, sd = t.stride()
@@ -521,7 +523,7 @@ def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, in
     i] + shift (0 and i where they are None).  inv_freq float64 [rot_dim/2]
     and factor as rope_freqs gives them."""
     lib = load_library()
-    dev, dt = q.device, q.dtype
+    dev, dt = _device_of(q, "q"), q.dtype
     if q.dim() != 4:
         raise EagleError("q must be [B, n, Hq, dh]")
     B, n, Hq, dh = q.shape
@@ -533,11 +535,11 @@ def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, in
         if v.shape[2] != Hkv:
             raise EagleError("k and v must have the same heads")
     if q_out is None:
-        q_out = torch.empty((B, n, Hq, dh), dtype=dt, device=dev)
+        q_out = torch.empty((B, n, Hq, dh), dtype=dt, device=q.device)
     if k_tree is None:
-        k_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=dev)
+        k_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=q.device)
     if v_tree is None and v is not None:
-        v_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=dev)
+        v_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=q.device)
     i32 = torch.int32
     _call("eagle_rope", lib.eagle_rope, dev, stream, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(),
           _dtype_code(q), B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v,
@@ -555,8 +557,8 @@ def _pools(k_pages, v_pages, k_scale, v_scale, device):
     """The 8-bit cache's four pointers, checked against each other."""
     if k_pages.dtype not in _POOL_TYPES or k_pages.dim() != 4:
         raise EagleError("k_pages must be float8_e4m3fn (or uint8) [num_pages, Hkv, page_size, dh]")
-    shape = tuple(k_pages.shape)
-    return (_need(k_pages, "k_pages", None, None, device), _need(v_pages, "v_pages", k_pages.dtype, shape, device),
+    shape = k_pages.shape
+    return (_need(k_pages, "k_pages", k_pages.dtype, None, device), _need(v_pages, "v_pages", k_pages.dtype, shape, device),
             _need(k_scale, "k_scale", torch.float32, shape[:2], device),
             _need(v_scale, "v_scale", torch.float32, shape[:2], device))
 
@@ -567,11 +569,11 @@ def kv8_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, status=None, 
     cache (eagle_kv8_append): k_pages, v_pages float8_e4m3fn [num_pages, Hkv,
     page_size, dh], k_scale, v_scale float32 [num_pages, Hkv]."""
     lib = load_library()
-    dev = k.device
-    if not k.is_cuda or k.dim() != 3:
-        raise EagleError("k must be a CUDA tensor [T, Hkv, dh]")
+    dev = _device_of(k, "k")
+    if k.dim() != 3:
+        raise EagleError("k must be [T, Hkv, dh]")
     T, Hkv, dh = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != dev or v.stride() != k.stride():
+    if v.shape != k.shape or v.dtype != k.dtype or v.get_device() != dev or v.stride() != k.stride():
         raise EagleError("v must have k's shape, strides, type and device")
     if T and k.stride(2) != 1:
         raise EagleError("k must have unit stride in dh")
@@ -592,7 +594,7 @@ def kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale
     rows of k_tree, v_tree [B, Hkv, n, dh] join the pages, kv_len is updated
     in place.  Returns slot_mapping [B, n]."""
     lib = load_library()
-    dev, i32 = k_tree.device, torch.int32
+    dev, i32 = _device_of(k_tree, "k_tree"), torch.int32
     B, Hkv, n, dh = k_tree.shape
     num_pages, H, page_size, d = k_pages.shape
     if H != Hkv or d != dh:
@@ -600,8 +602,8 @@ def kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale
     D = path_nodes.shape[1] - 1
     max_pages = block_table.shape[1]
     if slot_mapping is None:
-        slot_mapping = torch.empty((B, n), dtype=i32, device=dev)
-    _call("eagle_kv8_commit", lib.eagle_kv8_commit, dev, stream, _need(k_tree, "k_tree"),
+        slot_mapping = torch.empty((B, n), dtype=i32, device=k_tree.device)
+    _call("eagle_kv8_commit", lib.eagle_kv8_commit, dev, stream, _need(k_tree, "k_tree", k_tree.dtype, None, dev),
           _need(v_tree, "v_tree", k_tree.dtype, (B, Hkv, n, dh), dev), _dtype_code(k_tree), B, n, Hkv, dh,
           _need(accept_len, "accept_len", i32, (B,), dev), _need(path_nodes, "path_nodes", i32, (B, D + 1), dev), D,
           *_pools(k_pages, v_pages, k_scale, v_scale, dev),
@@ -618,21 +620,21 @@ def tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_
     kv8_append writes them, block_table int32 [B, max_pages]; else as
     tree_attn.  n = 1 with mask 1 decodes single tokens."""
     lib = load_library()
-    dev, dt = q.device, q.dtype
+    dev, dt = _device_of(q, "q"), q.dtype
     B, n, Hq, dh = q.shape
     num_pages, Hkv, page_size, _ = k_pages.shape
     max_pages = block_table.shape[1]
     scale = dh ** -0.5 if scale is None else scale
     if out is None:
-        out = torch.empty((B, n, Hq, dh), dtype=dt, device=dev)
+        out = torch.empty((B, n, Hq, dh), dtype=dt, device=q.device)
     if lse is None:
-        lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((B, n, Hq), dtype=torch.float32, device=q.device)
     code = _dtype_code(q)
     if k_pages.shape[3] != dh:
         raise EagleError("q must have the pages' head dimension")
     need = lib.eagle_tree_attn_kv8_workspace_size(code, B, n, Hq, Hkv, dh, max_pages, page_size)
-    buf, nbytes = (workspace or Workspace(dev)).get(need)
-    _call("eagle_tree_attn_kv8", lib.eagle_tree_attn_kv8, dev, stream, _need(q, "q"),
+    buf, nbytes = (workspace or Workspace(q.device)).get(need)
+    _call("eagle_tree_attn_kv8", lib.eagle_tree_attn_kv8, dev, stream, _need(q, "q", dt, None, dev),
           *_pools(k_pages, v_pages, k_scale, v_scale, dev),
           _need(block_table, "block_table", torch.int32, (B, max_pages), dev), max_pages, page_size, num_pages,
           _need(kv_len, "kv_len", torch.int32, (B,), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),

@@ -34,6 +34,18 @@ template <typename T> struct Chunk {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) v[i] = ld_stream16(p + i * VecTraits<T>::kElems);
   }
+  // Largest magnitude as a float's bits; above every finite one's if an element
+  // is infinite or NaN.
+  __device__ __forceinline__ uint32_t magnitude() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = sizeof(T) == 2 ? __vmaxu2(m, w[j] & 0x7fff7fffu) : max(m, w[j] & 0x7fffffffu);
+    }
+    return sizeof(T) == 2 ? max(m & 0xffff0000u, m << 16) : m;
+  }
   __device__ __forceinline__ void floats(float (&x)[16]) const {
     constexpr int E = VecTraits<T>::kElems;
 #pragma unroll
@@ -65,25 +77,27 @@ __device__ __forceinline__ void write_run(RowOf row_of, int count, uint8_t *page
   for (int u = 0; u < kHeld; ++u)
     if (tt + u * nt < chunks) held[u].load(source(tt + u * nt));
   const float s_old = first > 0 ? *scale : 1.f;
-  float amax = 0.f;
-  bool odd = false;
-  const auto look = [&](const Chunk<T> &k) {
-    float x[16];
-    k.floats(x);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const bool fin = is_finite(x[i]);
-      odd |= !fin;
-      amax = fmaxf(amax, fin ? fabsf(x[i]) : 0.f);
-    }
-  };
+  uint32_t top = 0;
 #pragma unroll
   for (int u = 0; u < kHeld; ++u)
-    if (tt + u * nt < chunks) look(held[u]);
+    if (tt + u * nt < chunks) top = max(top, held[u].magnitude());
   for (int c = tt + kHeld * nt; c < chunks; c += nt) {
     Chunk<T> k;
     k.load(source(c));
-    look(k);
+    top = max(top, k.magnitude());
+  }
+  const bool odd = top >= 0x7f800000u;  // something is not finite: the largest of the others
+  float amax = __uint_as_float(top);
+  if (odd) {
+    amax = 0.f;
+    for (int c = tt; c < chunks; c += nt) {
+      Chunk<T> k;
+      k.load(source(c));
+      float x[16];
+      k.floats(x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, is_finite(x[i]) ? fabsf(x[i]) : 0.f);
+    }
   }
   amax = warp_max(amax);
   if (warps > 1) {
@@ -103,14 +117,15 @@ __device__ __forceinline__ void write_run(RowOf row_of, int count, uint8_t *page
   const auto round_to_page = [&](const Chunk<T> &k, int c) {
     float x[16];
     k.floats(x);
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!is_finite(x[i])) x[i] = __uint_as_float(0x7fffffffu);
+    }
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = is_finite(x[4 * i + j]) ? x[4 * i + j] * inv : __uint_as_float(0x7fffffffu);
-      w[i] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
-    }
+    for (int i = 0; i < 4; ++i)
+      w[i] = e4m3_pair(x[4 * i] * inv, x[4 * i + 1] * inv) | (e4m3_pair(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
     *reinterpret_cast<uint4 *>(page + static_cast<int64_t>(first) * dh + static_cast<int64_t>(c) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   };
 #pragma unroll

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(RopeArgs a, int 
   const int node = blockIdx.x, b = node / a.n, i = node % a.n;
   const int it = threadIdx.x & ((1 << log_lanes) - 1);
   const int H = a.Hq + (a.v ? 2 : 1) * a.Hkv;
-  const int h0 = (blockIdx.y * kRopeItems << (8 - log_lanes)) + (threadIdx.x >> log_lanes), dh = 1 << (8 - log_lanes);
+  const int step = kRopeThreads >> log_lanes, h0 = blockIdx.y * kRopeItems * step + (threadIdx.x >> log_lanes);
   pdl_wait();
   const int pos = position_of(a, node, b, i);
   const int turning = INTER ? 2 * a.half / E : a.half / E;  // items that turn
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(RopeArgs a, int 
   bool turn[kRopeItems];
 #pragma unroll
   for (int u = 0; u < kRopeItems; ++u) {
-    const int h = h0 + u * dh;
+    const int h = h0 + u * step;
     dst[u] = nullptr;
     if (h >= H || it >= items) continue;
     const T *src;
@@ -190,7 +190,7 @@ static cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
     const int items = a.interleaved ? a.dh / E : a.half / E + (a.dh - 2 * a.half) / E;
     int log_lanes = 0;
     while ((1 << log_lanes) < items) ++log_lanes;
-    const int heads = kRopeItems << (8 - log_lanes);  // a CTA (log2 of its threads: 8)
+    const int heads = kRopeItems * (kRopeThreads >> log_lanes);  // a CTA
     const dim3 grid(a.B * a.n, (H + heads - 1) / heads);
     return a.interleaved ? launch_chained(rope_vec_kernel<T, true>, grid, dim3(kRopeThreads), 0, st, a, log_lanes, items)
                          : launch_chained(rope_vec_kernel<T, false>, grid, dim3(kRopeThreads), 0, st, a, log_lanes, items);
