@@ -181,23 +181,24 @@ struct AppendArgs {
   float *k_scale, *v_scale;
   int T, Hkv, dh, log_page, num_pages;
   int block;  // tokens a CTA looks after (those whose run begins there)
+  int units;  // (head, K or V) pairs a CTA looks after
   int warps;  // warps a team
   int32_t *status;
 };
 
-// One CTA per (token block, K or V, head), heads fastest: the CTAs that run together read
-// neighbouring heads of the same tokens, whose rows lie side by side (measured
-// on 65536 tokens of 8 heads of 128: WAS us with token blocks fastest).
+// One CTA per (token block, `units` of the 2 Hkv (head, K or V) pairs), the pairs
+// fastest, so that CTAs that run together read neighbouring heads of the same
+// tokens.  A team finds its runs once for all of its pairs: finding one costs
+// about what rounding a page of one head does (measured on 65536 tokens of 8
+// heads of 128, pages of 64: 101 us with one pair a CTA, 84 with two, 76 with four, 80 with eight).
 template <typename T>
 __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 3 : 2) kv8_append_kernel(AppendArgs a) {
   __shared__ float red[kWriteWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = warp / a.warps, tw = warp % a.warps, teams = kWriteWarps / a.warps;
-  const int g = blockIdx.x % a.Hkv, part = blockIdx.x / a.Hkv, t0 = (part >> 1) * a.block, t1 = min(a.T, t0 + a.block);
-  const bool is_v = part & 1;
-  const T *src = reinterpret_cast<const T *>(is_v ? a.v : a.k) + g * a.head_stride;
-  uint8_t *pages = is_v ? a.v_pages : a.k_pages;
-  float *scales = is_v ? a.v_scale : a.k_scale;
+  const int splits = (2 * a.Hkv + a.units - 1) / a.units, part = blockIdx.x / splits;
+  const int u0 = (blockIdx.x - part * splits) * a.units, u1 = min(2 * a.Hkv, u0 + a.units);
+  const int t0 = part * a.block, t1 = min(a.T, t0 + a.block);
   const int P = 1 << a.log_page;
   pdl_wait();
   pdl_trigger();
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 3 : 2) kv8_
     const int page = page_of(slot);
     const bool same = page >= 0 && page == page_of(prev);
     // what is skipped: a slot past the pool, a row out of sequence
-    if (g == 0 && !is_v && warp == 0 && ((slot >= 0 && page < 0) || (same && slot != prev + 1))) report(a.status, EAGLE_ERR_INVALID);
+    if (u0 == 0 && warp == 0 && ((slot >= 0 && page < 0) || (same && slot != prev + 1))) report(a.status, EAGLE_ERR_INVALID);
     uint32_t lead = __ballot_sync(0xffffffffu, page >= 0 && !same);
     while (lead) {  // the same in every warp
       const int l = __ffs(lead) - 1;
@@ -239,10 +240,14 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 3 : 2) kv8_
           whole = whole && on == 0xffffffffu;
         }
       }
-      const int64_t at = static_cast<int64_t>(pg) * a.Hkv + g;
-      const T *row0 = src + static_cast<int64_t>(p0 + l) * a.token_stride;
-      write_run<T>(LinearRows<T>{row0, a.token_stride}, count, pages + (at << a.log_page) * a.dh, scales + at, first, a.dh, team,
-                   a.warps, tw, red + team * a.warps, a.status);
+      for (int u = u0; u < u1; ++u) {
+        const int g = u >> 1;
+        const bool is_v = u & 1;
+        const int64_t at = static_cast<int64_t>(pg) * a.Hkv + g;
+        const T *row0 = reinterpret_cast<const T *>(is_v ? a.v : a.k) + g * a.head_stride + (p0 + l) * a.token_stride;
+        write_run<T>(LinearRows<T>{row0, a.token_stride}, count, (is_v ? a.v_pages : a.k_pages) + (at << a.log_page) * a.dh,
+                     (is_v ? a.v_scale : a.k_scale) + at, first, a.dh, team, a.warps, tw, red + team * a.warps, a.status);
+      }
     }
   }
 }
@@ -334,7 +339,7 @@ cudaError_t launch_kv8_append(const void *k, const void *v, int dtype, int T, in
                               float *k_scale, float *v_scale, int page_size, int num_pages, int32_t *status,
                               int num_sms, cudaStream_t st) {
   AppendArgs a = {k, v, token_stride, head_stride, slot_map, k_pages, v_pages, k_scale, v_scale,
-                  T, Hkv, dh, log2_page(page_size), num_pages, 0, 0, status};
+                  T, Hkv, dh, log2_page(page_size), num_pages, 0, 1, 0, status};
   // A team takes a run.  Long inputs: enough warps that a thread holds a whole
   // page's share (kHeld chunks), and as many pages a CTA as it has teams.  Few
   // rows (single tokens mostly): a warp a run, and CTAs cut down until the SMs
@@ -347,7 +352,9 @@ cudaError_t launch_kv8_append(const void *k, const void *v, int dtype, int T, in
   const int teams = kWriteWarps / a.warps;
   a.block = teams * page_size;
   while (a.block > teams && static_cast<int64_t>((T + a.block - 1) / a.block) * Hkv * 2 < 4ll * num_sms) a.block /= 2;
-  const int64_t ctas = static_cast<int64_t>((T + a.block - 1) / a.block) * Hkv * 2;
+  const int64_t blocks = (T + a.block - 1) / a.block;
+  while (a.units < 2 * Hkv && blocks * ((2 * Hkv + 2 * a.units - 1) / (2 * a.units)) >= 12ll * num_sms) a.units *= 2;
+  const int64_t ctas = blocks * ((2 * Hkv + a.units - 1) / a.units);
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(ctas));
   return dtype == EAGLE_BF16 ? launch_chained(kv8_append_kernel<__nv_bfloat16>, grid, dim3(kWriteWarps * 32), 0, st, a)
