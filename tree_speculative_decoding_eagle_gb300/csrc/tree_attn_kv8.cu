@@ -430,28 +430,28 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
         } else {
           // tree nodes: bf16 over the group's power of two
           const __nv_bfloat16 *src = (kv ? a.v_tree : a.k_tree) + (static_cast<int64_t>(bg) * n + key0) * DH;
+          uint4 x[STEPS], y[STEPS];
           float amax = 0.f;
 #pragma unroll
           for (int s = 0; s < STEPS; ++s) {
             const int r = grp * 16 + row_of(s);
-            if (r >= valid) continue;
-            const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
-            amax = fmaxf(amax, fmaxf(amax8(p[0]), amax8(p[1])));
-          }
-          const int e = half_exponent(warp_max(amax));
-          const float f = pow2_clamped(-e);
-          for (int s = 0; s < STEPS; ++s) {
-            const int r = grp * 16 + row_of(s);
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            x[s] = y[s] = make_uint4(0, 0, 0, 0);
             if (r < valid) {
               const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
-              x = p[0];
-              y = p[1];
+              x[s] = p[0];
+              y[s] = p[1];
             }
-            const uint32_t h[8] = {bf16x2_to_half2(x.x, f), bf16x2_to_half2(x.y, f), bf16x2_to_half2(x.z, f),
-                                   bf16x2_to_half2(x.w, f), bf16x2_to_half2(y.x, f), bf16x2_to_half2(y.y, f),
-                                   bf16x2_to_half2(y.z, f), bf16x2_to_half2(y.w, f)};
-            store(tile, r, h);
+          }
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s) amax = fmaxf(amax, fmaxf(amax8(x[s]), amax8(y[s])));
+          const int e = half_exponent(warp_max(amax));
+          const float f = pow2_clamped(-e);
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s) {
+            const uint32_t h[8] = {bf16x2_to_half2(x[s].x, f), bf16x2_to_half2(x[s].y, f), bf16x2_to_half2(x[s].z, f),
+                                   bf16x2_to_half2(x[s].w, f), bf16x2_to_half2(y[s].x, f), bf16x2_to_half2(y[s].y, f),
+                                   bf16x2_to_half2(y[s].z, f), bf16x2_to_half2(y[s].w, f)};
+            store(tile, grp * 16 + row_of(s), h);
           }
           if (lane == 0) {
             uint2 *sc = scales + (j % Sh::kScaleSlots) * GR + grp;
@@ -474,21 +474,33 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     const int t = warp >> 2, qtr = warp & 3;
     // this M-tile's query rows to shared memory as f16, each over a power of
     // two of its own: 8 or 16 neighbouring lanes hold a row
-    constexpr int CPR = DH / 8;
-    for (int idx = tid & 127; idx < QR * CPR; idx += 128) {
-      const int r = idx / CPR, c = idx % CPR;
-      const int rho = (mg * MT + t) * 128 + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (rho < rows_total)
-        v = *reinterpret_cast<const uint4 *>(a.q + ((static_cast<int64_t>(b) * n + rho / a.G) * a.Hq + g * a.G + rho % a.G) * DH + c * 8);
-      float amax = amax8(v);
+    constexpr int CPR = DH / 8, kPieces = QR * CPR / 128, kAhead = 8;  // a thread's; requested together
+    static_assert(kPieces % kAhead == 0 || kPieces < kAhead, "whole batches");
+#pragma unroll 1
+    for (int p0q = 0; p0q < kPieces; p0q += kAhead) {
+      uint4 v[kAhead < kPieces ? kAhead : kPieces];
+      constexpr int kBatch = kAhead < kPieces ? kAhead : kPieces;
 #pragma unroll
-      for (int o = 1; o < CPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int e = half_exponent(amax);
-      const float f = pow2_clamped(-e);
-      v = make_uint4(bf16x2_to_half2(v.x, f), bf16x2_to_half2(v.y, f), bf16x2_to_half2(v.z, f), bf16x2_to_half2(v.w, f));
-      *reinterpret_cast<uint4 *>(sQ + (t * Sh::kRegions + c / 8) * Sh::kQRegionBytes + sw128_offset(r, c % 8)) = v;
-      if (c == 0) q_exp[t * QR + r] = static_cast<signed char>(e);
+      for (int u = 0; u < kBatch; ++u) {
+        const int idx = (tid & 127) + (p0q + u) * 128, r = idx / CPR, c = idx % CPR;
+        const int rho = (mg * MT + t) * 128 + r;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (rho < rows_total)
+          v[u] = *reinterpret_cast<const uint4 *>(
+              a.q + ((static_cast<int64_t>(b) * n + rho / a.G) * a.Hq + g * a.G + rho % a.G) * DH + c * 8);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int idx = (tid & 127) + (p0q + u) * 128, r = idx / CPR, c = idx % CPR;
+        float amax = amax8(v[u]);
+#pragma unroll
+        for (int o = 1; o < CPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = half_exponent(amax);
+        const float f = pow2_clamped(-e);
+        *reinterpret_cast<uint4 *>(sQ + (t * Sh::kRegions + c / 8) * Sh::kQRegionBytes + sw128_offset(r, c % 8)) =
+            make_uint4(bf16x2_to_half2(v[u].x, f), bf16x2_to_half2(v[u].y, f), bf16x2_to_half2(v[u].z, f), bf16x2_to_half2(v[u].w, f));
+        if (c == 0) q_exp[t * QR + r] = static_cast<signed char>(e);
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
