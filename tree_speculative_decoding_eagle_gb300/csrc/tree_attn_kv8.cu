@@ -186,12 +186,14 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
   constexpr bool SPLIT = MERGE != 0;
   constexpr int NH = NK / 64, GR = Sh::kGroups;
   extern __shared__ unsigned char raw_smem[];
-  const uintptr_t raw = reinterpret_cast<uintptr_t>(raw_smem);
-  unsigned char *sm = reinterpret_cast<unsigned char *>((raw + 1023) & ~static_cast<uintptr_t>(1023));
+  // offsets from raw_smem, not address arithmetic: the compiler has to see that
+  // every access is to shared memory (a generic one costs registers and time)
+  const uint32_t gap = (1024u - (smem_u32(raw_smem) & 1023u)) & 1023u;
+  unsigned char *sm = raw_smem + gap;
   unsigned char *sQ = sm;
   unsigned char *sK = sm + Sh::kQBytes, *sV = sm + Sh::kVOff;
   unsigned char *s8 = sm + Sh::kStagingOff;
-  unsigned char *ctl = reinterpret_cast<uintptr_t>(sm) - raw >= static_cast<uintptr_t>(Sh::kBarBytes) ? raw_smem : sm + Sh::kBarOff;
+  unsigned char *ctl = raw_smem + (gap >= static_cast<uint32_t>(Sh::kBarBytes) ? 0u : gap + Sh::kBarOff);
   // K's barriers, then V's: bytes landed, staging free, f16 tile written, tile read
   uint64_t *bytes_full = reinterpret_cast<uint64_t *>(ctl);  // [K, V][S8]
   uint64_t *bytes_empty = bytes_full + 2 * S8;
