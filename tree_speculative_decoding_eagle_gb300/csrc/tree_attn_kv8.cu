@@ -165,7 +165,8 @@ __device__ __forceinline__ void tmem_ld32x2(uint32_t taddr, float (&a)[32], floa
 // Every lane polls, so the warp stays together.
 __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort) {
   uint64_t t0 = 0;
-  while (!mbar_try_wait(bar, parity)) {
+  for (uint32_t polls = 1; !mbar_try_wait(bar, parity); ++polls) {
+    if (polls & 15u) continue;  // a poll sleeps in the barrier; the clock is looked at now and then
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
     if (*abort || now - t0 > 2000000000ull) {
