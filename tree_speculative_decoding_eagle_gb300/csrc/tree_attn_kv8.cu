@@ -776,7 +776,9 @@ struct Kv8Plan {
 };
 
 // M-tiles per CTA, key-tile width, and the KV split S that minimises (waves of
-// CTAs) x (key tiles per CTA + the cost of merging partial results).
+// CTAs) x (key tiles per CTA + what a CTA costs before its first and after its
+// last tile, about six tiles, + the merge of partial results).  From three
+// waves on the last one is hardly seen, ragged lengths spread it.
 static Kv8Plan kv8_plan(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num_sms) {
   Kv8Plan p;
   const int G = Hq / Hkv, rows = n * G, tiles = (rows + 127) / 128;
@@ -792,14 +794,18 @@ static Kv8Plan kv8_plan(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num
   p.S = 1;
   double best = 1e30;
   for (int S = 1; S <= kMaxClusterSplits8 && S <= ptiles; ++S) {
-    const int64_t waves = (base * S + slots - 1) / slots;
-    const double cost = waves * (static_cast<double>((ptiles + S - 1) / S) + (S > 1 ? split_cost : 0.0));
+    const double load = static_cast<double>(base * S) / slots;
+    const double waves = load < 3.0 ? static_cast<double>((base * S + slots - 1) / slots) : load + 0.5;
+    const double cost = waves * (static_cast<double>((ptiles + S - 1) / S) + 6.0 + (S > 1 ? split_cost : 0.0));
     if (cost < best * 0.97) {  // prefer fewer splits unless clearly better
       best = cost;
       p.S = S;
     }
   }
-  p.one_wave = base * p.S <= slots;
+  // A cluster merges its splits where two CTAs share an SM; clusters of CTAs that
+  // fill an SM each find too few neighbours free (392 rows, dh 128, 8 heads of
+  // 4096 keys: 59 us with clusters of eight, 35 with the merge kernel).
+  p.one_wave = p.ctas_per_sm == 2 && base * p.S <= slots;
   return p;
 }
 

@@ -81,6 +81,20 @@ __global__ void __launch_bounds__(128, 3)
     mbar_init_fence();
   }
   pdl_wait();
+  // the query rows are requested first: kv_len, page numbers and bytes follow one another
+  const int rows_total = a.n * a.G;
+  uint4 xq[2][DH / 32];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int rho = rg * 16 + gr + 8 * r;
+#pragma unroll
+    for (int c = 0; c < DH / 32; ++c) {
+      xq[r][c] = make_uint4(0, 0, 0, 0);
+      if (rho < rows_total)
+        xq[r][c] = *reinterpret_cast<const uint4 *>(
+            a.q + ((static_cast<int64_t>(b) * a.n + rho / a.G) * a.Hq + g * a.G + rho % a.G) * DH + t * (DH / 4) + c * 8);
+    }
+  }
   const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
   const int groups = (L + 15) >> 4, per = (groups + a.S - 1) / a.S;
   const int g0 = min(groups, split * per) + kg, g1 = min(groups, split * per + per);
@@ -116,7 +130,6 @@ __global__ void __launch_bounds__(128, 3)
   float ks = a.k_scale[static_cast<int64_t>(page) * a.Hkv + g], vs = a.v_scale[static_cast<int64_t>(page) * a.Hkv + g];
 
   // ---- this warp's 16 query rows, f16 over a power of two of the row ---------
-  const int rows_total = a.n * a.G;
   uint32_t qa[STEPS][4];
   float row_scale[2];
   int node[2];
@@ -124,16 +137,10 @@ __global__ void __launch_bounds__(128, 3)
   for (int r = 0; r < 2; ++r) {
     const int rho = rg * 16 + gr + 8 * r;
     node[r] = rho < rows_total ? rho / a.G : -1;
-    uint4 x[DH / 32];
+    const uint4 (&x)[DH / 32] = xq[r];
     float amax = 0.f;
 #pragma unroll
-    for (int c = 0; c < DH / 32; ++c) {
-      x[c] = make_uint4(0, 0, 0, 0);
-      if (rho < rows_total)
-        x[c] = *reinterpret_cast<const uint4 *>(a.q + ((static_cast<int64_t>(b) * a.n + rho / a.G) * a.Hq + g * a.G + rho % a.G) * DH +
-                                                t * (DH / 4) + c * 8);
-      amax = fmaxf(amax, amax8(x[c]));
-    }
+    for (int c = 0; c < DH / 32; ++c) amax = fmaxf(amax, amax8(x[c]));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const int e = half_exponent(amax);
