@@ -506,8 +506,8 @@ int eagle_kv_commit(const void *k_tree, const void *v_tree, int dtype, int B,
  *                Nothing is written then.  A page number outside
  *                [0, num_pages) in either list gives slot -1 and
  *                EAGLE_ERR_INVALID.
- * Limits: 1 <= B <= 4096; page rules as for eagle_tree_attn_paged;
- * num_pages * page_size < 2^31.
+ * Limits: 1 <= B <= 4096; T <= 2^30; page rules as for
+ * eagle_tree_attn_paged; num_pages * page_size < 2^31.
  * ------------------------------------------------------------------------ */
 int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B,
                    int page_size, int max_pages, int num_pages,
@@ -618,8 +618,8 @@ int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch,
  *             EAGLE_ERR_INVALID, as does a slot past the pool.  A page that is
  *             listed in two places of slot_map ends up unspecified.
  *   status    device int32 (out; may be NULL)
- * Limits: T >= 0; dh a multiple of 16, at most 512; strides * elemsize multiples of 16
- * bytes, tensors 16-byte aligned; page_size a power of two in [16, 4096];
+ * Limits: 0 <= T <= 2^30; dh a multiple of 16, at most 512; strides *
+ * elemsize multiples of 16 bytes, tensors 16-byte aligned; page_size a power of two in [16, 4096];
  * num_pages * page_size < 2^31; Hkv <= 32767.
  * ------------------------------------------------------------------------ */
 int eagle_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv,
@@ -655,7 +655,7 @@ int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B,
  *              [0, num_pages) on a page that the prefix uses (page 0 is read
  *              in its place), EAGLE_ERR_TIMEOUT as in eagle_tree_attn
  * A row without any key (kv_len 0, empty mask row) gives zeros and lse =
- * -inf.  Rows of a page at or beyond kv_len may be read but never
+ * -inf; a row that attends to a NaN of the cache gives NaN.  Rows of a page at or beyond kv_len may be read but never
  * count, whatever they hold.  q, k_tree and v_tree must be finite, and so must
  * every mask-excluded row of the tree.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};

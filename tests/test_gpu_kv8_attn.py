@@ -185,8 +185,44 @@ def test_wide_table_and_short_prefixes():
 
 def test_long_chains_of_nodes():
     """A prompt chunk: causal chain, several tiles and mask words of nodes."""
-    for n in (200, 517):
+    for n in (200, 517, 1030):
         Case([0, 75], n, 4, 2, 64, 16, keep=torch.ones((2, n, n)).tril().bool()).run()
+        Case([0, 75], n, 2, 2, 128, 16, keep=torch.ones((2, n, n)).tril().bool()).run()
+
+
+@pytest.mark.parametrize("n,Hq", [(1, 4), (5, 16), (61, 4), (61, 16)])
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_nan_in_the_cache_reaches_the_rows_that_read_it(n, Hq, which):
+    """A NaN key or value of one head and sequence; the others stay as they are."""
+    c = Case([40, 33], n, Hq, 2, 128, 16)
+    want, want_lse = c.run()
+    page = int(c.table[1, 1])
+    c.pools[which][0][page, 1, 3, 7] = 0x7f
+    out, lse = eg.tree_attn_kv8(*c.args())
+    hit = torch.zeros((2, n, Hq), dtype=torch.bool, device="cuda")
+    hit[1, :, Hq // 2:] = True
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    if which == 0:
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    else:                                            # a NaN value: its column, in every row
+        assert torch.isnan(out[hit][:, 7]).all() and torch.equal(lse[hit], want_lse[hit])
+        assert torch.isfinite(out[hit][:, :7]).all() and torch.isfinite(out[hit][:, 8:]).all()
+
+
+def test_captured_without_a_call_before():
+    """Nothing that a first call sets up is forbidden during capture (a fresh
+    process would show it; here at least a shape not met before)."""
+    for n, Hq in ((3, 2), (90, 2)):
+        c = Case([37], n, Hq, 1, 64, 256, seed=99)
+        args, ws = c.args(), eg.Workspace("cuda")
+        ws.get(1 << 20)
+        out, lse = torch.empty((1, n, Hq, 64), dtype=torch.bfloat16, device="cuda"), torch.empty((1, n, Hq), device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            eg.tree_attn_kv8(*args, out=out, lse=lse, workspace=ws)
+        g.replay()
+        torch.cuda.synchronize()
+        c.check(out, lse)
 
 
 def test_rows_without_keys():

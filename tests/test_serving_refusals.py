@@ -45,6 +45,7 @@ def test_page_map(lib):
     refuse(lib.eagle_page_map, good, INVALID, _5=0)
     refuse(lib.eagle_page_map, good, INVALID, _5=1 << 27)                # slots past 31 bits
     refuse(lib.eagle_page_map, good, INVALID, _11=-1)
+    refuse(lib.eagle_page_map, good, INVALID, _11=(1 << 30) + 1)
     good = [FAKE, 4, 16, 8, 64, FAKE, FAKE, FAKE, FAKE, None, None]
     for p in (0, 5, 6, 7, 8):
         refuse(lib.eagle_page_release, good, INVALID, **{f"_{p}": None})
@@ -82,7 +83,7 @@ def test_kv8_append(lib):
         refuse(lib.eagle_kv8_append, good, INVALID, **{f"_{p}": None})
     for p in (0, 1, 9, 10):
         refuse(lib.eagle_kv8_append, good, INVALID, **{f"_{p}": UNAL})
-    for change in (dict(_2=7), dict(_3=-1), dict(_4=0), dict(_5=24), dict(_5=0), dict(_5=528), dict(_6=129), dict(_7=-64),
+    for change in (dict(_2=7), dict(_3=-1), dict(_3=(1 << 30) + 1), dict(_4=0), dict(_5=24), dict(_5=0), dict(_5=528), dict(_6=129), dict(_7=-64),
                    dict(_13=48), dict(_14=0), dict(_14=1 << 28)):
         refuse(lib.eagle_kv8_append, good, INVALID, **change)
     refuse(lib.eagle_kv8_append, good, UNSUPPORTED, _4=40000)

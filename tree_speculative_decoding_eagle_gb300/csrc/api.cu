@@ -335,6 +335,8 @@ int eagle_verify_draft(const void *target, const void *draft, int dtype, int64_t
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
+constexpr int kMaxTokens = 1 << 30;  // of one call: token indexes stay clear of 2^31
+
 // Page pools addressed by 32-bit slots.
 static bool valid_slots(int max_pages, int page_size, int num_pages) {
   return valid_pages(max_pages, page_size, num_pages) && static_cast<int64_t>(num_pages) * page_size <= INT32_MAX;
@@ -344,7 +346,8 @@ int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B, int pag
                    int32_t *block_table, int32_t *page_count, const int32_t *free_pages, int32_t *free_count,
                    int32_t *slot_map, int T, int32_t *new_start, int32_t *status, eagle_stream_t stream) {
   if (!kv_len || !new_len || !block_table || !page_count || !free_pages || !free_count) return EAGLE_ERR_INVALID;
-  if (B < 1 || T < 0 || (!slot_map && T) || !valid_slots(max_pages, page_size, num_pages)) return EAGLE_ERR_INVALID;
+  if (B < 1 || T < 0 || T > kMaxTokens || (!slot_map && T) || !valid_slots(max_pages, page_size, num_pages))
+    return EAGLE_ERR_INVALID;
   if (B > 4096) return EAGLE_ERR_UNSUPPORTED;  // one CTA's shared memory holds every request's sums
   return from_cuda(launch_page_map(kv_len, new_len, B, page_size, max_pages, num_pages, block_table, page_count,
                                    free_pages, free_count, slot_map, T, new_start, status,
@@ -397,7 +400,7 @@ int eagle_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv, in
                      int64_t head_stride, const int32_t *slot_map, uint8_t *k_pages, uint8_t *v_pages,
                      float *k_scale, float *v_scale, int page_size, int num_pages, int32_t *status,
                      eagle_stream_t stream) {
-  if (!valid_dtype(dtype) || T < 0 || Hkv < 1 || dh < 16 || dh % 16 || dh > 512 || token_stride < 0 || head_stride < 0)
+  if (!valid_dtype(dtype) || T < 0 || T > kMaxTokens || Hkv < 1 || dh < 16 || dh % 16 || dh > 512 || token_stride < 0 || head_stride < 0)
     return EAGLE_ERR_INVALID;
   if (!valid_slots(1, page_size, num_pages)) return EAGLE_ERR_INVALID;
   if (Hkv > 32767) return EAGLE_ERR_UNSUPPORTED;

@@ -51,7 +51,7 @@ __device__ __forceinline__ float amax8(const uint4 &v) {
 // Columns 4c..4c+3 of query row rho of (b, g): out = o / l, lse from (m, l).
 template <int DH>
 __device__ __forceinline__ void kv8_write_out(const Kv8Args &a, int bg, int rho, int c, float4 o, float m, float l) {
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
   const int i = rho / a.G, h = (bg % a.Hkv) * a.G + rho % a.G;
   const int64_t orow = (static_cast<int64_t>(bg / a.Hkv) * a.n + i) * a.Hq + h;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
@@ -59,7 +59,7 @@ __device__ __forceinline__ void kv8_write_out(const Kv8Args &a, int bg, int rho,
   packed.x = *reinterpret_cast<const uint32_t *>(&lo);
   packed.y = *reinterpret_cast<const uint32_t *>(&hi);
   reinterpret_cast<uint2 *>(a.out + orow * DH)[c] = packed;
-  if (c == 0 && a.lse) a.lse[orow] = l > 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+  if (c == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m - kBias + log2f(l)) * kLn2;
 }
 
 // out and lse of row rr, columns 4c..4c+3, of a (b, g, M-group) from its S
@@ -97,7 +97,7 @@ __device__ __forceinline__ void kv8_merge_item(const Kv8Args &a, int bg, int mg,
     for (int u = 0; u < 8; ++u) {
       const float w = ml[u].x > -INFINITY ? ex2_approx(ml[u].x - M) : 0.f;
       Ls = fmaf(w, ml[u].y, Ls);
-      if (w > 0.f) {
+      if (w != 0.f) {
         o.x = fmaf(w, po[u].x, o.x); o.y = fmaf(w, po[u].y, o.y);
         o.z = fmaf(w, po[u].z, o.z); o.w = fmaf(w, po[u].w, o.w);
       }

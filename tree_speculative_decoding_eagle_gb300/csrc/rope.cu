@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(RopeArgs a, int 
       c0[u] = 2 * a.half + (it - turning) * E;
       turn[u] = false;
     }
-    x[u][0] = ld_stream16(src + c0[u]);
-    if (c1[u] >= 0) x[u][1] = ld_stream16(src + c1[u]);
+    x[u][0] = __ldcs(reinterpret_cast<const uint4 *>(src + c0[u]));  // coherent: q may be turned in place
+    if (c1[u] >= 0) x[u][1] = __ldcs(reinterpret_cast<const uint4 *>(src + c1[u]));
   }
   node_turns(a, pos, cs);
   __syncthreads();

@@ -657,7 +657,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
       part_m = m;
       part_l = l;
     } else {
-      const float inv = (have && l > 0.f) ? 1.f / l : 0.f;
+      const float inv = (have && l != 0.f) ? 1.f / l : 0.f;  // a NaN stays one
 #pragma unroll
       for (int c0 = 0; c0 < DH; c0 += 32) {
         float o[32];
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
 #pragma unroll
         for (int e = 0; e < 4; ++e) dst[e] = reinterpret_cast<const uint4 *>(hv)[e];
       }
-      if (row_ok && a.lse) a.lse[orow] = (have && l > 0.f) ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+      if (row_ok && a.lse) a.lse[orow] = (have && l != 0.f) ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
     }
   }
 
