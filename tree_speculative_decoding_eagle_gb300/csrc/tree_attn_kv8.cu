@@ -883,10 +883,10 @@ cudaError_t launch_tree_attn_kv8(const void *q, const uint8_t *k_pages, const ui
       !make_pool_map(&maps[1], v_pages, blocks, page_size, dh, a.page_box, false))
     return cudaErrorInvalidValue;
   if (dh == 64) {
-    if (p.MT == 2) return launch_kv8_t<64, 2, 128, 3, 4, 128, 1>(maps, a, p, st);
+    if (p.MT == 2) return launch_kv8_t<64, 2, 128, 2, 4, 128, 1>(maps, a, p, st);
     return launch_kv8_t<64, 1, 64, 3, 4, 128, 2>(maps, a, p, st);
   }
-  if (p.MT == 2) return launch_kv8_t<128, 2, 64, 3, 3, 128, 1>(maps, a, p, st);
+  if (p.MT == 2) return launch_kv8_t<128, 2, 64, 2, 5, 128, 1>(maps, a, p, st);
   return p.QR == 64 ? launch_kv8_t<128, 1, 64, 2, 2, 64, 2>(maps, a, p, st) : launch_kv8_t<128, 1, 64, 3, 4, 128, 1>(maps, a, p, st);
 }
 
