@@ -619,8 +619,8 @@ int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch,
  *             listed in two places of slot_map ends up unspecified.
  *   status    device int32 (out; may be NULL)
  * Limits: 0 <= T <= 2^30; dh a multiple of 16, at most 512; strides *
- * elemsize multiples of 16 bytes, tensors 16-byte aligned; page_size a power of two in [16, 4096];
- * num_pages * page_size < 2^31; Hkv <= 32767.
+ * elemsize multiples of 16 bytes, tensors 16-byte aligned; page_size a power
+ * of two in [16, 4096]; num_pages * page_size < 2^31; Hkv <= 32767.
  * ------------------------------------------------------------------------ */
 int eagle_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv,
                      int dh, int64_t token_stride, int64_t head_stride,
@@ -655,11 +655,12 @@ int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B,
  *              [0, num_pages) on a page that the prefix uses (page 0 is read
  *              in its place), EAGLE_ERR_TIMEOUT as in eagle_tree_attn
  * A row without any key (kv_len 0, empty mask row) gives zeros and lse =
- * -inf; a row that attends to a NaN of the cache gives NaN.  Rows of a page at or beyond kv_len may be read but never
- * count, whatever they hold.  q, k_tree and v_tree must be finite, and so must
- * every mask-excluded row of the tree.
+ * -inf; a row that attends to a NaN of the cache gives NaN.  Rows of a page at
+ * or beyond kv_len may be read but never count, whatever they hold.  q, k_tree
+ * and v_tree must be finite, mask-excluded rows of the tree too.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};
- * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31.
+ * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31;
+ * n * Hq/Hkv <= 2^23.
  * ------------------------------------------------------------------------ */
 size_t eagle_tree_attn_kv8_workspace_size(int dtype, int B, int n, int Hq,
                                           int Hkv, int dh, int max_pages,

@@ -206,6 +206,78 @@ def test_the_cache_part_of_a_step_in_a_graph():
     assert int(caches[0].status) == 0 and caches[0].kv_len.tolist() == [20 + 12, 5, 31 + 18]
 
 
+@pytest.mark.gpu
+def test_a_captured_attend_outlives_a_larger_workspace():
+    """A larger call grows the cache's workspace: the graph captured before it
+    keeps its own, whatever is allocated and written afterwards."""
+    g = torch.Generator().manual_seed(6)
+    cache = KV8Cache(2, 2, 64, 16, 80, 40)
+    new = i32([600, 333])
+    slots = torch.empty(933, dtype=torch.int32, device="cuda")
+    cache.reserve(new, slots)
+    kv = torch.randn((2, 933, 2, 64), generator=g).to(bf).cuda()
+    cache.append(0, kv[0], kv[1], slots)
+    cache.grow(new)
+
+    def inputs(n):
+        return ([torch.randn(s, generator=g).to(bf).cuda() for s in ((2, n, 8, 64), (2, 2, n, 64), (2, 2, n, 64))]
+                + [eg.tree_mask(i32([[-1] + list(range(n - 1))] * 2))])
+
+    small, large = inputs(12), inputs(60)
+    out, lse = torch.empty_like(small[0]), torch.empty((2, 12, 8), device="cuda")
+    want, want_lse = cache.attend(0, *small)
+    held = cache._ws.buf
+    assert held is not None                      # the KV range is split
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(0, *small, out=out, lse=lse)
+    cache.attend(0, *large)
+    cache._ws.get(held.numel() + 1)              # what a call of more split rows asks for
+    assert cache._ws.buf is not held
+    size, address = held.numel(), held.data_ptr()
+    del held
+    others = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(20)]
+    assert all(t.data_ptr() != address for t in others)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert all(bool((t == 7).all()) for t in others)
+
+
+@pytest.mark.gpu
+def test_calls_on_a_given_stream():
+    """`stream`: what a call allocates for itself belongs to that stream, so
+    work of the current stream that follows does not touch it."""
+    g = torch.Generator().manual_seed(7)
+    cache = KV8Cache(2, 2, 64, 16, 80, 40)
+    new = i32([600, 333])
+    slots = torch.empty(933, dtype=torch.int32, device="cuda")
+    cache.reserve(new, slots)
+    kv = torch.randn((2, 933, 2, 64), generator=g).to(bf).cuda()
+    cache.append(0, kv[0], kv[1], slots)
+    cache.grow(new)
+    n = 12
+    x = [torch.randn((2, n, h, 64), generator=g).to(bf).cuda() for h in (8, 2, 2)]
+    mask = eg.tree_mask(i32([[-1] + list(range(n - 1))] * 2))
+    freqs, factor = eg.rope_freqs(64)
+
+    def run(stream=None):
+        q, k, v = eg.rope(*x, freqs, pos_base=cache.kv_len, factor=factor, stream=stream)
+        return (q, k, v) + eg.tree_attn_kv8(q, *cache._pools(0), cache.block_table, cache.kv_len, k, v, mask, stream=stream)
+
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        got = run(side)
+        junk = [torch.full((1 << 20,), 3, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
+    with pytest.raises(eg.EagleError):
+        eg.rope(x[0], x[1][0, 0], None, freqs)
+
+
 def test_a_cache_checks_its_arguments():
     with pytest.raises(eg.EagleError):
         KV8Cache(1, 1, 64, 16, 4, 4, layers=0, device="cpu")

@@ -117,6 +117,25 @@ def test_tree_attn_kv8(lib):
     assert size(1, 2, 3, 7, 2, 64, 8, 16) == 0 and size(1, 2, 3, 8, 2, 80, 8, 16) == 0
 
 
+def test_tree_attn_kv8_query_rows(lib):
+    """Rows of a KV head past 2^23: the kernels count them in 32 bits."""
+    good = [FAKE] * 6 + [8, 16, 64] + [FAKE] * 4 + [1, 2, 4096, 8, 2, 64, ctypes.c_float(0.1), FAKE, None, None, None, 0, None]
+    refuse(lib.eagle_tree_attn_kv8, good, UNSUPPORTED, _16=2 * 2049)
+    refuse(lib.eagle_tree_attn_kv8, good, UNSUPPORTED, _16=2 << 20)        # 2^32 rows
+    assert lib.eagle_tree_attn_kv8_workspace_size(1, 2, 4096, 2 * 2049, 2, 64, 8, 16) == 0
+
+
+def test_a_cache_keeps_the_workspaces_it_outgrows():
+    """A captured graph holds the address of the workspace of its capture."""
+    from tree_speculative_decoding_eagle_gb300.cache import KV8Cache
+    cache = KV8Cache(1, 1, 64, 16, 2, 2, device="cpu")
+    first = cache._ws.get(1000)[0]
+    again = cache._ws.get(500)[0]
+    larger = cache._ws.get(2000)[0]
+    assert again is first and larger is not first and larger.numel() == 2000
+    assert cache._ws._outgrown[0] is first and len(cache._ws._outgrown) == 1
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     i32 = dict(dtype=torch.int32)
     with pytest.raises(eg.EagleError, match="CUDA"):

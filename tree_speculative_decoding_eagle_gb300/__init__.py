@@ -524,10 +524,13 @@ def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, in
     takes them.  Node i of sequence b is at position pos_base[b] + pos_off[b,
     i] + shift (0 and i where they are None).  inv_freq float64 [rot_dim/2]
     and factor as rope_freqs gives them."""
+    if stream is not None:     # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return rope(q, k, v, inv_freq, pos_base, pos_off, shift, factor, interleaved, q_out, k_tree, v_tree)
     lib = load_library()
     dev, dt = _device_of(q, "q"), q.dtype
-    if q.dim() != 4:
-        raise EagleError("q must be [B, n, Hq, dh]")
+    if q.dim() != 4 or k.dim() != 4:
+        raise EagleError("q and k must be [B, n, heads, dh]")
     B, n, Hq, dh = q.shape
     Hkv = k.shape[2]
     ld_q, ld_k = _heads(q, "q", B, n, dh, dt, dev), _heads(k, "k", B, n, dh, dt, dev)
@@ -543,7 +546,7 @@ def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, in
     if v_tree is None and v is not None:
         v_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=q.device)
     i32 = torch.int32
-    _call("eagle_rope", lib.eagle_rope, dev, stream, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(),
+    _call("eagle_rope", lib.eagle_rope, dev, None, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(),
           _dtype_code(q), B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v,
           _need(inv_freq, "inv_freq", torch.float64, None, dev), 2 * inv_freq.numel(), int(interleaved), factor,
           _maybe(pos_base, "pos_base", i32, (B,), dev), _maybe(pos_off, "pos_off", i32, (B, n), dev), shift,
@@ -595,6 +598,10 @@ def kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale
     """kv_commit into the 8-bit cache (eagle_kv8_commit): the accepted path's
     rows of k_tree, v_tree [B, Hkv, n, dh] join the pages, kv_len is updated
     in place.  Returns slot_mapping [B, n]."""
+    if stream is not None:     # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale, v_scale, kv_len,
+                              block_table, slot_mapping, status)
     lib = load_library()
     dev, i32 = _device_of(k_tree, "k_tree"), torch.int32
     B, Hkv, n, dh = k_tree.shape
@@ -605,7 +612,7 @@ def kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale
     max_pages = block_table.shape[1]
     if slot_mapping is None:
         slot_mapping = torch.empty((B, n), dtype=i32, device=k_tree.device)
-    _call("eagle_kv8_commit", lib.eagle_kv8_commit, dev, stream, _need(k_tree, "k_tree", k_tree.dtype, None, dev),
+    _call("eagle_kv8_commit", lib.eagle_kv8_commit, dev, None, _need(k_tree, "k_tree", k_tree.dtype, None, dev),
           _need(v_tree, "v_tree", k_tree.dtype, (B, Hkv, n, dh), dev), _dtype_code(k_tree), B, n, Hkv, dh,
           _need(accept_len, "accept_len", i32, (B,), dev), _need(path_nodes, "path_nodes", i32, (B, D + 1), dev), D,
           *_pools(k_pages, v_pages, k_scale, v_scale, dev),
@@ -621,6 +628,10 @@ def tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_
     [B, n, Hq, dh] and k_tree, v_tree [B, Hkv, n, dh] bf16, pages and scales as
     kv8_append writes them, block_table int32 [B, max_pages]; else as
     tree_attn.  n = 1 with mask 1 decodes single tokens."""
+    if stream is not None:     # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_tree, v_tree, mask,
+                                 scale, out, lse, workspace, status)
     lib = load_library()
     dev, dt = _device_of(q, "q"), q.dtype
     B, n, Hq, dh = q.shape
@@ -636,7 +647,7 @@ def tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_
         raise EagleError("q must have the pages' head dimension")
     need = lib.eagle_tree_attn_kv8_workspace_size(code, B, n, Hq, Hkv, dh, max_pages, page_size)
     buf, nbytes = (workspace or Workspace(q.device)).get(need)
-    _call("eagle_tree_attn_kv8", lib.eagle_tree_attn_kv8, dev, stream, _need(q, "q", dt, None, dev),
+    _call("eagle_tree_attn_kv8", lib.eagle_tree_attn_kv8, dev, None, _need(q, "q", dt, None, dev),
           *_pools(k_pages, v_pages, k_scale, v_scale, dev),
           _need(block_table, "block_table", torch.int32, (B, max_pages), dev), max_pages, page_size, num_pages,
           _need(kv_len, "kv_len", torch.int32, (B,), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),

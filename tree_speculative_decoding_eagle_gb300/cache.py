@@ -10,11 +10,29 @@ all on the device, and calls the library's entry points on the current stream:
     release  -> eagle_page_release  pages back: of requests that ended, or past kv_len
 Nothing is allocated and nothing synchronises after the constructor (but for the
 attention's workspace, which grows to the largest call), so the calls can be
-captured in a CUDA graph.  The layers share block tables and lengths.
+captured in a CUDA graph; a workspace that a larger call replaces stays, for the
+graphs that hold its address.  Calls on one cache, and graphs captured from it,
+follow one another; layers attended at the same time on several streams take a
+Workspace each.  The layers share block tables and lengths.
 """
 import torch
 
 from . import EagleError, Workspace, kv8_append, kv8_commit, page_map, page_release, tree_attn_kv8
+
+
+class _KeptWorkspace(Workspace):
+    """A workspace whose outgrown buffers live as long as it does."""
+
+    def __init__(self, device=None):
+        super().__init__(device)
+        self._outgrown = []
+
+    def get(self, nbytes):
+        before = self.buf
+        got = super().get(nbytes)
+        if before is not None and self.buf is not before:
+            self._outgrown.append(before)
+        return got
 
 
 class KV8Cache:
@@ -35,7 +53,7 @@ class KV8Cache:
         self.kv_len = torch.zeros(B, **i32)
         self.status = torch.zeros(1, **i32)
         self._len = torch.zeros(B, **i32)      # the lengths that all layers but the last commit to
-        self._ws = Workspace(device)
+        self._ws = _KeptWorkspace(device)
 
     def _pools(self, layer):
         return self.k_pages[layer], self.v_pages[layer], self.k_scale[layer], self.v_scale[layer]
@@ -53,9 +71,9 @@ class KV8Cache:
     def grow(self, new_len):
         self.kv_len.add_(new_len)
 
-    def attend(self, layer, q, k_tree, v_tree, mask, scale=None, out=None, lse=None):
+    def attend(self, layer, q, k_tree, v_tree, mask, scale=None, out=None, lse=None, workspace=None):
         return tree_attn_kv8(q, *self._pools(layer), self.block_table, self.kv_len, k_tree, v_tree, mask, scale=scale,
-                             out=out, lse=lse, workspace=self._ws, status=self.status)
+                             out=out, lse=lse, workspace=workspace or self._ws, status=self.status)
 
     def commit(self, k_trees, v_trees, accept_len, path_nodes, slot_mapping=None):
         """The accepted path of every layer (lists of k_tree, v_tree); kv_len

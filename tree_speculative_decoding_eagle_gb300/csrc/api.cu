@@ -432,10 +432,13 @@ int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, i
                                      slot_mapping, status, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Query rows of a KV head: their M-groups are a grid dimension, their number an int.
+static bool valid_query_rows(int n, int Hq, int Hkv) { return static_cast<int64_t>(n) * (Hq / Hkv) <= (1 << 23); }
+
 size_t eagle_tree_attn_kv8_workspace_size(int dtype, int B, int n, int Hq, int Hkv, int dh, int max_pages,
                                           int page_size) {
   if (dtype != EAGLE_BF16 || B < 1 || n < 1 || n > 4096 || Hq < 1 || Hkv < 1 || Hq % Hkv || (dh != 64 && dh != 128) ||
-      !valid_pages(max_pages, page_size, 1))
+      !valid_pages(max_pages, page_size, 1) || !valid_query_rows(n, Hq, Hkv))
     return 0;
   return attn_kv8_workspace_bytes(B, n, Hq, Hkv, dh, max_pages * page_size, current_num_sms());
 }
@@ -453,7 +456,8 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages, const uint8_t *v_
       !valid_pages(max_pages, page_size, num_pages))
     return EAGLE_ERR_INVALID;
   if (dtype != EAGLE_BF16 || (dh != 64 && dh != 128)) return EAGLE_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(B) * Hkv > 65535 || static_cast<int64_t>(num_pages) * Hkv > INT32_MAX)
+  if (static_cast<int64_t>(B) * Hkv > 65535 || static_cast<int64_t>(num_pages) * Hkv > INT32_MAX ||
+      !valid_query_rows(n, Hq, Hkv))
     return EAGLE_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_tree) || !aligned16(v_tree) ||
       !aligned16(out))
