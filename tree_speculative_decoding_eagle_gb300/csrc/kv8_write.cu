@@ -10,7 +10,10 @@
 // result does not depend on an order.
 //
 // What bounds it: HBM for prompts (2 or 4 bytes read, 1 written an element),
-// latency for single tokens.
+// latency for single tokens and commits.  Measured: 65536 tokens of 8 heads of
+// 128, bf16, pages of 64: 76.4 us (5.3 TB/s, 79 % of a copy's rate; 403 MB); one
+// token of each of 64 requests, 8 heads of 64: 4.0 us; the accepted paths of 8
+// trees, 40 heads of 128: 7.7 us with a copy of kv_len before it.
 #include "kv8.cuh"
 #include "sm100.cuh"
 

@@ -12,6 +12,10 @@
 // number of tokens); every CTA reads all lengths and makes the sums itself in
 // shared memory (12 bytes a request, from L2 after the first), which
 // costs less than handing them over, and then writes its share of the outputs.
+// Measured, a map and a release together (two launches in a graph): 6.4 us for
+// one request, 11.1 us for 512 requests with up to 32768 new tokens, whose 0.2
+// MB would stream in 0.03 us: the chain is two launches, the lengths, two sums,
+// a bisection and the free list's entries.
 // Everything that is updated in place (page_count, free_count) is written only
 // after a cluster barrier that every CTA reaches with its reads done.
 #include "common.cuh"

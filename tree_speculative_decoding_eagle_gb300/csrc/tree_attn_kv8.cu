@@ -27,6 +27,20 @@
 //   * MMA thread and one softmax warpgroup per M-tile as in tree_attn_tc.cu:
 //     S = Q K^T from shared memory, P from tensor memory.
 // KV split over up to 8 CTAs and the merge of their results as there too.
+//
+// What bounds it.  With grouped heads, the softmax warps: of 3300 cycles a 128-key
+// tile of two M-tiles takes at dh 64 (a trace of each role's waits) they wait in
+// 360; tensor pipe 32 %, ex2 33 %, issue slots 57 % of active cycles; HBM 12 %.
+// With few rows, each CTA's chain (length - page number - bytes - f16 - S - P - O)
+// through the warps.  Measured (the same call on a 16-bit cache): 16 x 49 nodes,
+// 64 heads on 8 of 128, 4096 keys 152 us (184; 694 TFLOP/s, 36 % of cuBLAS's
+// bf16 rate); 64 x 61 nodes, 64 heads on 8 of 64, 8192 keys 731 us (688; 717
+// TFLOP/s, 38 %); 61 nodes, 32 heads of 128, 2048 keys 21.5 us (17.8); 8 x 51
+// nodes, 40 heads of 128, 1024 to 4096 keys 131 us (142).
+// Two M-tiles a CTA (one converter warpgroup, which then takes K and V in turn)
+// from 129 rows on, since a tile's conversion is shared by its M-tiles; two CTAs an
+// SM up to 64 rows, where latency counts.
+//
 // Every wait is bounded; a timeout raises EAGLE_ERR_TIMEOUT in the status
 // word and the CTA drains its copies and MMAs, frees tensor memory and exits.
 #include "kv8_attn.cuh"
