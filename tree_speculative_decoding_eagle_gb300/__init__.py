@@ -427,18 +427,20 @@ def _maybe(t, name, dtype, shape, dev):
 
 
 def _device_of(t, name):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise EagleError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def _call(what, fn, dev, stream, *args):
     """fn(*args, stream) with device number `dev` current, on its current stream
     unless one is given."""
-    # the stream's handle without a Stream object around it: a microsecond of a
-    # call that takes nine
+    # the stream's handle without a Stream object around it and the device without
+    # a look at the runtime's state (a CUDA tensor is at hand): two microseconds of
+    # a call that takes nine
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -540,11 +542,11 @@ def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, in
         if v.shape[2] != Hkv:
             raise EagleError("k and v must have the same heads")
     if q_out is None:
-        q_out = torch.empty((B, n, Hq, dh), dtype=dt, device=q.device)
+        q_out = q.new_empty((B, n, Hq, dh))
     if k_tree is None:
-        k_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=q.device)
+        k_tree = q.new_empty((B, Hkv, n, dh))
     if v_tree is None and v is not None:
-        v_tree = torch.empty((B, Hkv, n, dh), dtype=dt, device=q.device)
+        v_tree = q.new_empty((B, Hkv, n, dh))
     i32 = torch.int32
     _call("eagle_rope", lib.eagle_rope, dev, None, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(),
           _dtype_code(q), B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v,
@@ -574,21 +576,22 @@ def kv8_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, status=None, 
     cache (eagle_kv8_append): k_pages, v_pages float8_e4m3fn [num_pages, Hkv,
     page_size, dh], k_scale, v_scale float32 [num_pages, Hkv]."""
     lib = load_library()
-    dev = _device_of(k, "k")
-    if k.dim() != 3:
+    dev, shape, stride = _device_of(k, "k"), k.shape, k.stride()
+    if len(shape) != 3:
         raise EagleError("k must be [T, Hkv, dh]")
-    T, Hkv, dh = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype or v.get_device() != dev or v.stride() != k.stride():
+    if v.shape != shape or v.stride() != stride or v.dtype != k.dtype or v.get_device() != dev:
         raise EagleError("v must have k's shape, strides, type and device")
-    if T and k.stride(2) != 1:
+    T, Hkv, dh = shape
+    per_token, per_head, per_element = stride
+    if T and per_element != 1:
         raise EagleError("k must have unit stride in dh")
     num_pages, H, page_size, d = k_pages.shape
     if H != Hkv or d != dh:
         raise EagleError("k must have the pages' heads and head dimension")
-    if min(k.stride()) < 0 or (T > 1 and Hkv > 1 and 0 in k.stride()):
+    if T > 1 and Hkv > 1 and (per_token == 0 or per_head == 0):
         raise EagleError("k must not be a broadcast view")
     _call("eagle_kv8_append", lib.eagle_kv8_append, dev, stream, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, Hkv,
-          dh, k.stride(0), k.stride(1), _need(slot_map, "slot_map", torch.int32, (T,), dev),
+          dh, per_token, per_head, _need(slot_map, "slot_map", torch.int32, (T,), dev),
           *_pools(k_pages, v_pages, k_scale, v_scale, dev), page_size, num_pages,
           _maybe(status, "status", torch.int32, None, dev))
 
