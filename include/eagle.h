@@ -657,7 +657,9 @@ int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B,
  * A row without any key (kv_len 0, empty mask row) gives zeros and lse =
  * -inf; a row that attends to a NaN of the cache gives NaN.  Rows of a page at
  * or beyond kv_len may be read but never count, whatever they hold.  q, k_tree
- * and v_tree must be finite, mask-excluded rows of the tree too.
+ * and v_tree must be finite, mask-excluded rows of the tree too.  k_tree and
+ * v_tree count down to 2^-25 of the largest magnitude among their neighbours
+ * (16 to 128 nodes of a head); what is smaller is rounded there.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};
  * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31;
  * n * Hq/Hkv <= 2^23.

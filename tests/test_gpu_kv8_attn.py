@@ -313,3 +313,26 @@ def test_refused_by_the_binding():
                 dict(block_table=good["block_table"][:1]), dict(scale=0.0), dict(q=q.cpu()), dict(out=q.float())):
         with pytest.raises(eg.EagleError):
             eg.tree_attn_kv8(**{**good, **bad})
+
+
+@pytest.mark.parametrize("P", [16, 64, 128, 4096])
+@pytest.mark.parametrize("n,G,dh", [(61, 8, 64), (49, 8, 128), (200, 2, 64), (333, 1, 128), (150, 1, 64)])
+def test_tree_rows_of_many_sizes(n, G, dh, P):
+    """Neighbouring nodes' keys and values 2^-8 to 2^8 times apart, over pages
+    shorter and longer than a key tile, one tree tile and several.  Within the
+    tolerance: a row becomes f16 over a power of two that leaves the largest in
+    [2^8, 2^9), so a number is exact unless its bits end below 2^-24, and off by
+    at most 2^-25, 2^-33 of the largest (2^-23 where that is 2^10); its weight
+    times that is far below 2^-11 A, the prefix alone giving A some tenths."""
+    c = Case([300, 77], n, 2 * G, 2, dh, P)
+    size = torch.exp2((torch.arange(n) % 17 - 8).float())[:, None]
+    c.kt, c.vt = (c.kt.float() * size).bfloat16(), (c.vt.float() * size.flip(0)).bfloat16()
+    c.run()
+
+
+@pytest.mark.parametrize("L", [0, 1, 63, 64, 65, 127, 128, 129, 1000])
+@pytest.mark.parametrize("dh,P", [(64, 128), (64, 256), (128, 64), (128, 512)])
+def test_grouped_heads_over_long_pages(L, dh, P):
+    """129 query rows a KV head and more, pages no shorter than a key tile."""
+    Case([L, 3 * L // 4 + 1], 43, 6, 2, dh, P).run()
+    Case([L, 3 * L // 4 + 1], 129, 2, 2, dh, P).run()

@@ -28,15 +28,15 @@
 //     S = Q K^T from shared memory, P from tensor memory.
 // KV split over up to 8 CTAs and the merge of their results as there too.
 //
-// What bounds it.  With grouped heads, the softmax warps: of 3300 cycles a 128-key
-// tile of two M-tiles takes at dh 64 (a trace of each role's waits) they wait in
-// 360; tensor pipe 32 %, ex2 33 %, issue slots 57 % of active cycles; HBM 12 %.
-// With few rows, each CTA's chain (length - page number - bytes - f16 - S - P - O)
-// through the warps.  Measured (the same call on a 16-bit cache): 16 x 49 nodes,
-// 64 heads on 8 of 128, 4096 keys 152 us (184; 694 TFLOP/s, 36 % of cuBLAS's
-// bf16 rate); 64 x 61 nodes, 64 heads on 8 of 64, 8192 keys 731 us (688; 717
-// TFLOP/s, 38 %); 61 nodes, 32 heads of 128, 2048 keys 21.5 us (17.8); 8 x 51
-// nodes, 40 heads of 128, 1024 to 4096 keys 131 us (142).
+// What bounds it.  With grouped heads, the softmax warps: of 3300 cycles that a
+// 128-key tile of two M-tiles took at dh 64 (a trace of each role's waits, before
+// the one-scale form) they waited in 360; tensor pipe 32 %, ex2 33 %, issue slots
+// 57 % of active cycles; HBM 12 %.  With few rows, each CTA's chain (length -
+// page number - bytes - f16 - S - P - O) through the warps.  Measured (the same
+// call on a 16-bit cache): 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 148 us
+// (184; 714 TFLOP/s, 37 % of cuBLAS's bf16 rate); 64 x 61 nodes, 64 heads on 8 of
+// 64, 8192 keys 675 us (688; 777 TFLOP/s, 41 %); 61 nodes, 32 heads of 128, 2048
+// keys 21.6 us (17.8); 8 x 51 nodes, 40 heads of 128, 1024 to 4096 keys 131 us (142).
 // Two M-tiles a CTA (one converter warpgroup, which then takes K and V in turn)
 // from 129 rows on, since a tile's conversion is shared by its M-tiles; two CTAs an
 // SM up to 64 rows, where latency counts.
@@ -52,7 +52,12 @@ using namespace sm100;
 // QR: query rows held per M-tile region (64 when there are at most 64: the
 // 128-row MMAs then read rows 64-127 from what follows, and those rows' results
 // are never used).  OCC: CTAs per SM.
-template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC>
+// ONE: every key tile has one scale (pages no shorter than a tile; the tree's
+// nodes then share a tile's power of two), so the softmax does nothing group by
+// group.  Measured with it / without: 64 x 61 nodes, 64 heads on 8 of 64, 8192
+// keys 675 / 731 us; 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 148 / 152 us.  A
+// choice made per tile in one kernel costs more than it gains (registers spill).
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, bool ONE>
 struct Kv8Shape {
   static constexpr int kRegions = DH / 64;
   static constexpr int kQRegionBytes = QR * 128;
@@ -64,12 +69,12 @@ struct Kv8Shape {
   static constexpr int kStagingOff = kVOff + SF * kTileBytes;
   static constexpr int kBarOff = kStagingOff + S8 * 2 * kByteTile;
   static constexpr int kGroups = NK / 16;
-  static constexpr int kNumBars = 4 * S8 + 4 * SF + 4 * MT + 2;
+  static constexpr int kNumBars = 4 * S8 + 4 * SF + 4 * MT + 2 + (ONE ? 2 : 0);
   // barriers, tensor-memory slot and abort flag, scales of the tiles' groups,
   // exponents of the query rows
   static constexpr int kScaleSlots = S8 + SF + 3;         // tiles between K's producer and the softmax
   static constexpr int kScaleOff = (kNumBars * 8 + 8 + 15) / 16 * 16;
-  static constexpr int kBarBytes = kScaleOff + kScaleSlots * kGroups * 8 + MT * QR;
+  static constexpr int kBarBytes = kScaleOff + kScaleSlots * kGroups * 8 + (ONE ? 32 : 0) + MT * QR;
   // The barriers sit in the gap before the 1 KB-aligned buffers when it holds
   // them, else after the buffers.
   static constexpr int kSmem = kBarOff + (1008 > 2 * kBarBytes - 16 ? 1008 : 2 * kBarBytes - 16);
@@ -91,6 +96,7 @@ struct Kv8Shape {
   static constexpr int kRegsLeft = (kGroupsAll * kLaunchRegs - kRegsOther - kConvertGroups * kRegsConvert) / MT / 8 * 8;
   static constexpr int kRegsSoftmax = kRegsLeft > 208 ? 208 : kRegsLeft;
   static_assert(QR == 128 || (QR == 64 && MT == 1), "64-row regions with one M-tile only");
+  static_assert(!ONE || kConvertGroups == 1, "four warps exchange a tree tile's largest magnitude");
   static_assert(kCols <= 512 && kTmemCols * OCC <= 512, "tensor memory budget");
   static_assert(kSmem <= 232448 && OCC * (kSmem + 1024) <= 233472, "shared memory budget");
   static_assert(MT * kRegsSoftmax + kConvertGroups * kRegsConvert + kRegsOther <= kGroupsAll * kLaunchRegs, "register budget");
@@ -194,10 +200,10 @@ __device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0)
 
 // MERGE: 0 the grid does not split the KV range; 1 the S splits of an item are
 // one cluster and merge in this kernel; 2 tree_attn_kv8_merge_kernel merges.
-template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, int MERGE>
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, bool ONE, int MERGE>
 __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, Kv8Args a) {
-  using Sh = Kv8Shape<DH, MT, NK, SF, S8, QR, OCC>;
+  using Sh = Kv8Shape<DH, MT, NK, SF, S8, QR, OCC, ONE>;
   constexpr bool SPLIT = MERGE != 0;
   constexpr int NH = NK / 64, GR = Sh::kGroups;
   extern __shared__ unsigned char raw_smem[];
@@ -220,10 +226,12 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
   uint64_t *o_done = p_full + MT;
   uint64_t *q_full = o_done + MT;
   uint64_t *teardown = q_full + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(teardown + 1);
+  uint64_t *tree_sync = teardown + 1;  // [K, V]: the converter warps' exchange (ONE)
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tree_sync + (ONE ? 2 : 0));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   uint2 *scales = reinterpret_cast<uint2 *>(ctl + Sh::kScaleOff);                   // [kScaleSlots][GR]
-  signed char *q_exp = reinterpret_cast<signed char *>(scales + Sh::kScaleSlots * GR);  // [MT * QR]
+  volatile float *tree_max = reinterpret_cast<volatile float *>(scales + Sh::kScaleSlots * GR);  // [K, V][4 converter warps]
+  signed char *q_exp = reinterpret_cast<signed char *>(scales + Sh::kScaleSlots * GR) + (ONE ? 32 : 0);      // [MT * QR]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, mg = blockIdx.y;
@@ -249,6 +257,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     }
     mbar_init(q_full, 4 * MT);
     mbar_init(teardown, 1);
+    for (int i = 0; i < (ONE ? 2 : 0); ++i) mbar_init(&tree_sync[i], 4);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -423,8 +432,8 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
       unsigned char *tile = tiles + st * Sh::kTileBytes;
       const int key0 = (prefix ? p0 + jp : j - tree0) * NK;
       const int valid = min(NK, (prefix ? L : n) - key0);
-      for (int grp = cw; grp < GR; grp += 4) {
-        if (__builtin_expect(prefix, 1)) {
+      if (__builtin_expect(prefix, 1)) {
+        for (int grp = cw; grp < GR; grp += 4) {
           const unsigned char *src = s8 + ((jp % S8) * 2 + kv) * Sh::kByteTile;
           uint4 x[STEPS];
 #pragma unroll
@@ -444,39 +453,64 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
             }
             store(tile, grp * 16 + row_of(s), h);
           }
-        } else {
-          // tree nodes: bf16 over the group's power of two
-          const __nv_bfloat16 *src = (kv ? a.v_tree : a.k_tree) + (static_cast<int64_t>(bg) * n + key0) * DH;
-          uint4 x[STEPS], y[STEPS];
+        }
+      } else {
+        // tree nodes: bf16 over a power of two, the group's or (ONE) the tile's;
+        // all of a warp's groups are then loaded at once and their largest
+        // magnitude is exchanged with the other warps'
+        constexpr int GW = ONE ? GR / 4 : 1;
+        const __nv_bfloat16 *src = (kv ? a.v_tree : a.k_tree) + (static_cast<int64_t>(bg) * n + key0) * DH;
+        bool gave_up = false;
+        for (int g0 = cw; g0 < GR; g0 += 4 * GW) {
+          uint4 x[GW][STEPS], y[GW][STEPS];
           float amax = 0.f;
 #pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            const int r = grp * 16 + row_of(s);
-            x[s] = y[s] = make_uint4(0, 0, 0, 0);
-            if (r < valid) {
-              const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
-              x[s] = p[0];
-              y[s] = p[1];
-            }
-          }
+          for (int w = 0; w < GW; ++w)
 #pragma unroll
-          for (int s = 0; s < STEPS; ++s) amax = fmaxf(amax, fmaxf(amax8(x[s]), amax8(y[s])));
-          const int e = half_exponent(warp_max(amax));
+            for (int s = 0; s < STEPS; ++s) {
+              const int r = (g0 + 4 * w) * 16 + row_of(s);
+              x[w][s] = y[w][s] = make_uint4(0, 0, 0, 0);
+              if (r < valid) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
+                x[w][s] = p[0];
+                y[w][s] = p[1];
+              }
+            }
+#pragma unroll
+          for (int w = 0; w < GW; ++w)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) amax = fmaxf(amax, fmaxf(amax8(x[w][s]), amax8(y[w][s])));
+          amax = warp_max(amax);
+          if constexpr (ONE) {
+            // a slot is written again only after the other ring's exchange
+            if (lane == 0) {
+              tree_max[4 * kv + cw] = amax;
+              mbar_arrive(&tree_sync[kv]);
+            }
+            __syncwarp();
+            if (unlikely(!wait_bounded(&tree_sync[kv], (j - tree0) & 1, abort_flag))) { gave_up = true; break; }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) amax = fmaxf(amax, tree_max[4 * kv + w]);
+          }
+          const int e = half_exponent(amax);
           const float f = pow2_clamped(-e);
 #pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            const uint32_t h[8] = {bf16x2_to_half2(x[s].x, f), bf16x2_to_half2(x[s].y, f), bf16x2_to_half2(x[s].z, f),
-                                   bf16x2_to_half2(x[s].w, f), bf16x2_to_half2(y[s].x, f), bf16x2_to_half2(y[s].y, f),
-                                   bf16x2_to_half2(y[s].z, f), bf16x2_to_half2(y[s].w, f)};
-            store(tile, grp * 16 + row_of(s), h);
-          }
+          for (int w = 0; w < GW; ++w)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+              const uint32_t h[8] = {bf16x2_to_half2(x[w][s].x, f), bf16x2_to_half2(x[w][s].y, f), bf16x2_to_half2(x[w][s].z, f),
+                                     bf16x2_to_half2(x[w][s].w, f), bf16x2_to_half2(y[w][s].x, f), bf16x2_to_half2(y[w][s].y, f),
+                                     bf16x2_to_half2(y[w][s].z, f), bf16x2_to_half2(y[w][s].w, f)};
+              store(tile, (g0 + 4 * w) * 16 + row_of(s), h);
+            }
           if (lane == 0) {
-            uint2 *sc = scales + (j % Sh::kScaleSlots) * GR + grp;
+            uint2 *sc = scales + (j % Sh::kScaleSlots) * GR + g0;
             const uint32_t both = pack_scales(pow2_clamped(e), pow2_clamped(-e));
             reinterpret_cast<unsigned short *>(&sc->x)[kv ? 0 : 1] = static_cast<unsigned short>(kv ? both : both >> 16);
             if (kv) sc->y = __float_as_uint(static_cast<float>(e));
           }
         }
+        if (unlikely(gave_up)) break;
       }
       __syncwarp();
       if (lane == 0) {
@@ -557,7 +591,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
       // 70B 154 -> 152 us with four kept, GPT-OSS 734 -> 757 with eight).
       float2 held[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) held[q] = NH == 1 ? group(q) : make_float2(0.f, 0.f);
+      for (int q = 0; q < 4; ++q) held[q] = ONE || NH == 1 ? group(ONE ? 0 : q) : make_float2(0.f, 0.f);
       // S in halves of 64 columns.  With two halves the first is read once for
       // the maximum and again for its exponentials, after the second's: 64
       // scores in registers at a time instead of 128.
@@ -582,6 +616,11 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
           float y = s16[0];
 #pragma unroll
           for (int c = 1; c < 15; c += 2) y = fmax3(y, s16[c], s16[c + 1]);
+          if constexpr (ONE) {
+            x = fmax3(x, y, s16[15]);
+            if (q == 3) x = fmaf(x, held[0].x, held[0].y);
+            continue;
+          }
           const float2 fv = NH == 1 ? held[q] : group(4 * h + q);
           x = fmaxf(x, fmaf(fmaxf(y, s16[15]), fv.x, fv.y));
         }
@@ -616,16 +655,17 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
       const float nb = kBias - (base > -INFINITY ? base : 0.f);
       float sum = 0.f;
       const auto exp_half = [&](int h) {
+        uint64_t one_acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float pk[16];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int gi = 4 * h + 2 * half + q;
-            const float2 fv = NH == 1 ? held[2 * half + q] : group(gi);
+            const float2 fv = ONE ? held[0] : (NH == 1 ? held[2 * half + q] : group(gi));
             const float f = fv.x, off = nb + fv.y;
             const uint64_t f2 = f2_pack(f, f), o2 = f2_pack(off, off);
-            uint64_t acc = f2_pack(0.f, 0.f);
+            uint64_t acc = ONE ? one_acc[q] : f2_pack(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               float t0, t1;
@@ -635,11 +675,20 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
               const __half2 h2 = __floats2half2_rn(e0, e1);
               pk[8 * q + c] = *reinterpret_cast<const float *>(&h2);
             }
-            float a0, a1;
-            f2_unpack(acc, a0, a1);
-            sum = fmaf(a0 + a1, __uint_as_float(sc[gi].x << 16), sum);
+            if constexpr (ONE) {
+              one_acc[q] = acc;
+            } else {
+              float a0, a1;
+              f2_unpack(acc, a0, a1);
+              sum = fmaf(a0 + a1, __uint_as_float(sc[gi].x << 16), sum);
+            }
           }
           tmem_st16_async(tP + 32 * h + 16 * half, pk);
+        }
+        if constexpr (ONE) {
+          float a0, a1;
+          f2_unpack(f2_add(one_acc[0], one_acc[1]), a0, a1);
+          sum = fmaf(a0 + a1, __uint_as_float(sc[0].x << 16), sum);
         }
       };
       if (warp_live) exp_half(NH - 1);
@@ -842,10 +891,10 @@ size_t attn_kv8_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int Lmax,
   return static_cast<size_t>(B) * Hkv * p.mgroups * p.S * kv8_slot_rows(p, n * (Hq / Hkv)) * (dh + 2) * sizeof(float);
 }
 
-template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, int MERGE>
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, bool ONE, int MERGE>
 static cudaError_t launch_kv8_v(const CUtensorMap *maps, const Kv8Args &a, const Kv8Plan &p, cudaStream_t st) {
-  using Sh = Kv8Shape<DH, MT, NK, SF, S8, QR, OCC>;
-  const auto kernel = tree_attn_kv8_kernel<DH, MT, NK, SF, S8, QR, OCC, MERGE>;
+  using Sh = Kv8Shape<DH, MT, NK, SF, S8, QR, OCC, ONE>;
+  const auto kernel = tree_attn_kv8_kernel<DH, MT, NK, SF, S8, QR, OCC, ONE, MERGE>;
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = set_smem_limit_once(kernel, Sh::kSmem, configured);
   if (e != cudaSuccess) return e;
@@ -868,11 +917,11 @@ static cudaError_t launch_kv8_v(const CUtensorMap *maps, const Kv8Args &a, const
   return launch_chained_cluster(kernel, grid, dim3(Sh::kThreads), Sh::kSmem, st, p.S, maps[0], maps[1], a);
 }
 
-template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC>
+template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, bool ONE>
 static cudaError_t launch_kv8_t(const CUtensorMap *maps, const Kv8Args &a, const Kv8Plan &p, cudaStream_t st) {
-  if (p.S <= 1) return launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, 0>(maps, a, p, st);
-  return p.one_wave ? launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, 1>(maps, a, p, st)
-                    : launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, 2>(maps, a, p, st);
+  if (p.S <= 1) return launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, ONE, 0>(maps, a, p, st);
+  return p.one_wave ? launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, ONE, 1>(maps, a, p, st)
+                    : launch_kv8_v<DH, MT, NK, SF, S8, QR, OCC, ONE, 2>(maps, a, p, st);
 }
 
 cudaError_t launch_tree_attn_kv8(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
@@ -905,12 +954,15 @@ cudaError_t launch_tree_attn_kv8(const void *q, const uint8_t *k_pages, const ui
   if (!make_pool_map(&maps[0], k_pages, blocks, page_size, dh, a.page_box, false) ||
       !make_pool_map(&maps[1], v_pages, blocks, page_size, dh, a.page_box, false))
     return cudaErrorInvalidValue;
+  const bool one = page_size >= p.NK;
   if (dh == 64) {
-    if (p.MT == 2) return launch_kv8_t<64, 2, 128, 2, 4, 128, 1>(maps, a, p, st);
-    return launch_kv8_t<64, 1, 64, 3, 4, 128, 2>(maps, a, p, st);
+    if (p.MT == 2)
+      return one ? launch_kv8_t<64, 2, 128, 2, 4, 128, 1, true>(maps, a, p, st) : launch_kv8_t<64, 2, 128, 2, 4, 128, 1, false>(maps, a, p, st);
+    return launch_kv8_t<64, 1, 64, 3, 4, 128, 2, false>(maps, a, p, st);
   }
-  if (p.MT == 2) return launch_kv8_t<128, 2, 64, 2, 5, 128, 1>(maps, a, p, st);
-  return p.QR == 64 ? launch_kv8_t<128, 1, 64, 2, 2, 64, 2>(maps, a, p, st) : launch_kv8_t<128, 1, 64, 3, 4, 128, 1>(maps, a, p, st);
+  if (p.MT == 2)
+    return one ? launch_kv8_t<128, 2, 64, 2, 5, 128, 1, true>(maps, a, p, st) : launch_kv8_t<128, 2, 64, 2, 5, 128, 1, false>(maps, a, p, st);
+  return p.QR == 64 ? launch_kv8_t<128, 1, 64, 2, 2, 64, 2, false>(maps, a, p, st) : launch_kv8_t<128, 1, 64, 3, 4, 128, 1, false>(maps, a, p, st);
 }
 
 }  // namespace eagle
