@@ -650,7 +650,8 @@ int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B,
  *   k_pages, v_pages, k_scale, v_scale   as above; scales that are not powers
  *              of two in range are read as the power of two below, clamped
  *   block_table, max_pages, page_size, num_pages, kv_len, k_tree, v_tree,
- *   mask, scale, out, lse, workspace      as in eagle_tree_attn_paged
+ *   mask, scale, out, lse, workspace      as in eagle_tree_attn_paged; bits of
+ *              the mask past the last node count for nothing
  *   status     EAGLE_ERR_INVALID for a block-table entry outside
  *              [0, num_pages) on a page that the prefix uses (page 0 is read
  *              in its place), EAGLE_ERR_TIMEOUT as in eagle_tree_attn

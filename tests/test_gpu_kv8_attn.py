@@ -336,3 +336,14 @@ def test_grouped_heads_over_long_pages(L, dh, P):
     """129 query rows a KV head and more, pages no shorter than a key tile."""
     Case([L, 3 * L // 4 + 1], 43, 6, 2, dh, P).run()
     Case([L, 3 * L // 4 + 1], 129, 2, 2, dh, P).run()
+
+
+@pytest.mark.parametrize("P", [16, 128])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("n,G", [(1, 1), (1, 40), (3, 2), (61, 1), (61, 8), (65, 1), (100, 2), (130, 4)])
+def test_mask_bits_past_the_last_node(n, G, dh, P):
+    """Words of all ones are a mask of all nodes: bits that name no node count for nothing."""
+    c = Case([70, 0], n, 2 * G, 2, dh, P, keep=torch.ones((2, n, n), dtype=torch.bool))
+    args = list(c.args())
+    args[9] = torch.full_like(args[9], -1)
+    c.check(*eg.tree_attn_kv8(*args))

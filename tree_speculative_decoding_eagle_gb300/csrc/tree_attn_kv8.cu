@@ -35,7 +35,7 @@
 // page number - bytes - f16 - S - P - O) through the warps.  Measured (the same
 // call on a 16-bit cache): 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 148 us
 // (184; 714 TFLOP/s, 37 % of cuBLAS's bf16 rate); 64 x 61 nodes, 64 heads on 8 of
-// 64, 8192 keys 675 us (688; 777 TFLOP/s, 41 %); 61 nodes, 32 heads of 128, 2048
+// 64, 8192 keys 684 us (688; 766 TFLOP/s, 40 %); 61 nodes, 32 heads of 128, 2048
 // keys 21.6 us (17.8); 8 x 51 nodes, 40 heads of 128, 1024 to 4096 keys 131 us (142).
 // Two M-tiles a CTA (one converter warpgroup, which then takes K and V in turn)
 // from 129 rows on, since a tile's conversion is shared by its M-tiles; two CTAs an
@@ -55,7 +55,7 @@ using namespace sm100;
 // ONE: every key tile has one scale (pages no shorter than a tile; the tree's
 // nodes then share a tile's power of two), so the softmax does nothing group by
 // group.  Measured with it / without: 64 x 61 nodes, 64 heads on 8 of 64, 8192
-// keys 675 / 731 us; 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 148 / 152 us.  A
+// keys 684 / 731 us; 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 148 / 152 us.  A
 // choice made per tile in one kernel costs more than it gains (registers spill).
 template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, bool ONE>
 struct Kv8Shape {
@@ -601,9 +601,9 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
         if (prefix) {
           const int valid = min(NK, L - (p0 + jp) * NK) - 64 * h;
           keep = valid >= 64 ? ~0ull : (valid <= 0 ? 0ull : ((1ull << valid) - 1ull));
-        } else {
+        } else {  // bits past the last node count for nothing
           const int w = (j - tree0) * NH + h;
-          keep = (row_ok && w < a.W) ? mrow[w] : 0ull;
+          keep = (row_ok && w < a.W) ? mrow[w] & (~0ull >> max(0, 64 * (w + 1) - n)) : 0ull;
         }
 #pragma unroll
         for (int c = 0; c < 64; ++c) sv[c / 32][c % 32] = ((keep >> c) & 1ull) ? sv[c / 32][c % 32] : -INFINITY;
