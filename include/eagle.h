@@ -13,7 +13,7 @@
  * Around them, for a serving loop whose KV cache is paged and held in 8 bits:
  *   eagle_page_map, eagle_page_release   pages of a free list to requests and back
  *   eagle_rope                           rotary positions of q and k
- *   eagle_kv8_append, eagle_kv8_commit   keys and values into the 8-bit cache
+ *   eagle_kv8_append, eagle_kv8_commit, eagle_kv8_commit_root   keys and values into the 8-bit cache
  *   eagle_tree_attn_kv8                  the tree attention over that cache
  *
  * Sources (the pages the method is taken from):
@@ -254,6 +254,8 @@ int eagle_tree_mask(const int32_t *node_parent, int B, int n, uint64_t *mask,
  * ancestors.  For node i (0..n-1, n = m+1), query head h, KV head
  * g = h / (Hq/Hkv):
  *   keys = k_cache[b, g, 0:kv_len[b]]  ++  { k_tree[b, g, j] : mask bit j of row i }
+ * The root is tree node 0 and counts once: this kv_len is the number of
+ * positions before it.
  *   s = scale * <q[b, i, h], key>,  out[b, i, h] = softmax(s) . values,
  *   lse[b, i, h] = ln sum exp(s).
  *   q          [B, n, Hq, dh]        dtype
@@ -445,7 +447,9 @@ int eagle_verify_draft(const void *target, const void *draft, int dtype,
  * After verification — commit the accepted path's keys and values.
  * [EAGLE-1] section "検証方法" / [EAGLE-2]: the accepted draft tokens become
  * part of the sequence; everything after a rejection is discarded.  The
- * root's K/V is already the last prefix position.  For each sequence b with
+ * root's K/V is already the last prefix position: the caller has stored it
+ * after the attention, whose kv_len was one less (the root was its tree node
+ * 0); eagle_kv8_commit_root stores it too.  For each sequence b with
  * a = accept_len[b], nodes path_nodes[b, 1..a] (as eagle_verify writes them)
  * have their rows of k_tree/v_tree [B, Hkv, n, dh] copied, in path order, to
  * positions kv_len[b] .. kv_len[b]+a-1 of the cache, and kv_len[b] becomes
@@ -489,7 +493,8 @@ int eagle_kv_commit(const void *k_tree, const void *v_tree, int dtype, int B,
  * -1 for T > t >= the number of new tokens.
  *   kv_len       device int32 [B]: tokens already in each request's cache
  *   new_len      device int32 [B]: tokens about to be written (0 allowed);
- *                before a tree step, the most the verification can accept
+ *                before a tree step, the root and the most nodes that the
+ *                verification can accept after it
  *   block_table  device int32 [B, max_pages]  (in/out; other entries stay)
  *   page_count   device int32 [B]             (in/out: pages mapped)
  *   free_pages   device int32 [num_pages]     (in; distinct page numbers
@@ -543,8 +548,9 @@ int eagle_page_release(const int32_t *keep_len, int B, int page_size,
  * for j < rot_dim / 2; the pair is (j, j + rot_dim/2) or, with `interleaved`,
  * (2j, 2j + 1).  Columns rot_dim .. dh-1 are copied.  The position of node i
  * of sequence b is pos_base[b] + pos_off[b, i] + shift (pos_base NULL: 0;
- * pos_off NULL: i); for a tree whose root is the last prefix position, as
- * eagle_kv_commit has it, pass kv_len, node_depth and shift = -1.
+ * pos_off NULL: i).  For a tree pass the attention's kv_len (the positions
+ * before the root), node_depth and shift = 0; where kv_len counts the root
+ * already, shift = -1.
  *   q, k, v    dtype, node (b, i) starts at element (b*n + i) * ld_q (ld_k,
  *              ld_v), its heads dh apart: slices of one fused projection do.
  *              v may be NULL (then v_tree is unused)
@@ -632,8 +638,9 @@ int eagle_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv,
 /* eagle_kv_commit into the 8-bit cache: the accepted path's rows of
  * k_tree/v_tree [B, Hkv, n, dh] join the cache at kv_len[b] .., kv_len[b]
  * grows by accept_len[b].  Arguments, slot_mapping and device errors as in
- * eagle_kv_commit with a block table.  Limits: those of eagle_kv_commit and
- * of eagle_kv8_append. */
+ * eagle_kv_commit with a block table: the root is stored already, and kv_len
+ * is one more than the attention's.  Limits: those of eagle_kv_commit and of
+ * eagle_kv8_append. */
 int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B,
                      int n, int Hkv, int dh, const int32_t *accept_len,
                      const int32_t *path_nodes, int D, uint8_t *k_pages,
@@ -641,6 +648,29 @@ int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B,
                      const int32_t *block_table, int max_pages, int page_size,
                      int num_pages, int32_t *kv_len, int32_t *slot_mapping,
                      int32_t *status, eagle_stream_t stream);
+
+/* The commit of a decoding loop: the root's rows too.  The loop has one rule:
+ * kv_len counts the positions before the root, the tree holds the root as
+ * node 0 (position kv_len, depth 0), so
+ *   eagle_page_map with new_len = D + 1 -> eagle_rope with pos_base = kv_len,
+ *   pos_off = node_depth, shift = 0 -> eagle_tree_attn_kv8 with kv_len ->
+ *   eagle_verify -> this call -> eagle_page_release with kv_len
+ * and the bonus token is the next root.  Nodes path_nodes[b, 0..a] (the root
+ * first) go to positions kv_len[b] .. kv_len[b]+a, and kv_len[b] becomes
+ * kv_len[b] + a + 1; slot_mapping gives the root kv_len[b] and node
+ * path_nodes[b, p] kv_len[b] + p, by the kv_len before.  With several layers
+ * every call but the last gets a copy of kv_len.
+ * Device errors as in eagle_kv8_commit, but kv_len 0 is a length like others
+ * and path_nodes[b, 0] has to be 0.  Limits of eagle_kv8_commit. */
+int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
+                          int B, int n, int Hkv, int dh,
+                          const int32_t *accept_len, const int32_t *path_nodes,
+                          int D, uint8_t *k_pages, uint8_t *v_pages,
+                          float *k_scale, float *v_scale,
+                          const int32_t *block_table, int max_pages,
+                          int page_size, int num_pages, int32_t *kv_len,
+                          int32_t *slot_mapping, int32_t *status,
+                          eagle_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Stage 3 over the 8-bit paged cache.

@@ -11,7 +11,8 @@ for tokens that are not kept.
 
 Readings:
   * The root's K/V is already the last prefix position (it was the last
-    accepted token of the previous step).  The accepted path nodes
+    accepted token of the previous step, stored after the tree's attention,
+    which had it as node 0 and a prefix without it).  The accepted path nodes
     path[1..a] are appended, in path order, at positions kv_len .. kv_len+a-1
     of their sequence, and kv_len becomes kv_len + a.  The bonus token has no
     K/V yet (the next step's forward pass makes it).

@@ -22,8 +22,9 @@ library is missing or a call reports an error, an exception is raised.
                    free list to requests and back; slots of new tokens)
     rope        -> eagle_rope         (rotary positions, into the attention's layouts;
                    rope_freqs -> eagle_rope_freqs)
-    kv8_append / kv8_commit -> eagle_kv8_append, eagle_kv8_commit (keys and
-                   values into the paged cache of e4m3 numbers)
+    kv8_append / kv8_commit -> eagle_kv8_append, eagle_kv8_commit,
+                   eagle_kv8_commit_root (keys and values into the paged cache
+                   of e4m3 numbers)
     tree_attn_kv8 -> eagle_tree_attn_kv8 (tree attention over that cache)
     run_step / StepGraph -> eagle_step, eagle_step_graph_* (the four stages
                    in one call, or recorded once as a graph and replayed)
@@ -49,7 +50,7 @@ EXPORTED = (
     "eagle_tree_attn_paged_workspace_size", "eagle_tree_attn_paged", "eagle_kv_commit",
     "eagle_verify_workspace_size", "eagle_verify", "eagle_verify_noalloc", "eagle_verify_draft",
     "eagle_page_map", "eagle_page_release", "eagle_rope", "eagle_rope_freqs",
-    "eagle_kv8_append", "eagle_kv8_commit", "eagle_tree_attn_kv8_workspace_size", "eagle_tree_attn_kv8",
+    "eagle_kv8_append", "eagle_kv8_commit", "eagle_kv8_commit_root", "eagle_tree_attn_kv8_workspace_size", "eagle_tree_attn_kv8",
     "eagle_step_workspace_size", "eagle_step", "eagle_step_graph_create", "eagle_step_graph_launch",
     "eagle_step_graph_destroy",
 )
@@ -119,6 +120,7 @@ def load_library(path=LIB_PATH):
         "eagle_rope_freqs": (I, [I, ctypes.c_double, I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double, P, P]),
         "eagle_kv8_append": (I, [P, P, I, I, I, I, I64, I64, P, P, P, P, P, I, I, P, P]),
         "eagle_kv8_commit": (I, [P, P, I, I, I, I, I, P, P, I, P, P, P, P, P, I, I, I, P, P, P, P]),
+        "eagle_kv8_commit_root": (I, [P, P, I, I, I, I, I, P, P, I, P, P, P, P, P, I, I, I, P, P, P, P]),
         "eagle_tree_attn_kv8_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
         "eagle_tree_attn_kv8": (I, [P, P, P, P, P, P, I, I, I, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, SZ, P]),
         "eagle_step_workspace_size": (SZ, [ctypes.POINTER(StepArgs)]),
@@ -597,14 +599,16 @@ def kv8_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, status=None, 
 
 
 def kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale, v_scale, kv_len, block_table,
-               slot_mapping=None, status=None, stream=None):
+               slot_mapping=None, status=None, stream=None, root=False):
     """kv_commit into the 8-bit cache (eagle_kv8_commit): the accepted path's
     rows of k_tree, v_tree [B, Hkv, n, dh] join the pages, kv_len is updated
-    in place.  Returns slot_mapping [B, n]."""
+    in place.  With `root` (eagle_kv8_commit_root) the root's rows go before
+    them, and kv_len is the attention's; without it the root is stored already.
+    Returns slot_mapping [B, n]."""
     if stream is not None:     # what is allocated here belongs to that stream
         with torch.cuda.stream(stream):
             return kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale, v_scale, kv_len,
-                              block_table, slot_mapping, status)
+                              block_table, slot_mapping, status, root=root)
     lib = load_library()
     dev, i32 = _device_of(k_tree, "k_tree"), torch.int32
     B, Hkv, n, dh = k_tree.shape
@@ -615,7 +619,8 @@ def kv8_commit(k_tree, v_tree, accept_len, path_nodes, k_pages, v_pages, k_scale
     max_pages = block_table.shape[1]
     if slot_mapping is None:
         slot_mapping = torch.empty((B, n), dtype=i32, device=k_tree.device)
-    _call("eagle_kv8_commit", lib.eagle_kv8_commit, dev, None, _need(k_tree, "k_tree", k_tree.dtype, None, dev),
+    name = "eagle_kv8_commit_root" if root else "eagle_kv8_commit"
+    _call(name, getattr(lib, name), dev, None, _need(k_tree, "k_tree", k_tree.dtype, None, dev),
           _need(v_tree, "v_tree", k_tree.dtype, (B, Hkv, n, dh), dev), _dtype_code(k_tree), B, n, Hkv, dh,
           _need(accept_len, "accept_len", i32, (B,), dev), _need(path_nodes, "path_nodes", i32, (B, D + 1), dev), D,
           *_pools(k_pages, v_pages, k_scale, v_scale, dev),

@@ -6,8 +6,14 @@ all on the device, and calls the library's entry points on the current stream:
     reserve  -> eagle_page_map      pages and slots for new tokens
     append   -> eagle_kv8_append    a prompt's (or single tokens') keys and values
     attend   -> eagle_tree_attn_kv8 draft nodes or single tokens over the cache
-    commit   -> eagle_kv8_commit    the accepted path, in every layer
+    commit   -> eagle_kv8_commit_root (root=True), eagle_kv8_commit
+                                    the accepted path, in every layer
     release  -> eagle_page_release  pages back: of requests that ended, or past kv_len
+kv_len counts the positions before the tree's root, which is node 0 of the tree,
+at position kv_len.  So one step over a tree of depth D is
+    reserve(D + 1) -> rope(pos_base=kv_len, pos_off=depth) -> attend -> verify
+    -> commit(root=True) -> trim
+(TreeStep.attend_kv8 and commit_kv8), and the bonus token is the next root.
 Nothing is allocated and nothing synchronises after the constructor (but for the
 attention's workspace, which grows to the largest call), so the calls can be
 captured in a CUDA graph; a workspace that a larger call replaces stays, for the
@@ -75,9 +81,12 @@ class KV8Cache:
         return tree_attn_kv8(q, *self._pools(layer), self.block_table, self.kv_len, k_tree, v_tree, mask, scale=scale,
                              out=out, lse=lse, workspace=workspace or self._ws, status=self.status)
 
-    def commit(self, k_trees, v_trees, accept_len, path_nodes, slot_mapping=None):
-        """The accepted path of every layer (lists of k_tree, v_tree); kv_len
-        grows by accept_len once."""
+    def commit(self, k_trees, v_trees, accept_len, path_nodes, slot_mapping=None, root=False):
+        """The accepted path of every layer (lists of k_tree, v_tree).  With
+        `root` the root's rows and the path's are stored, and kv_len grows by
+        accept_len + 1; without it by accept_len, and the caller has appended
+        the root's rows and grown kv_len by one between the attention and this
+        call."""
         last = len(self.k_pages) - 1
         if len(k_trees) != last + 1 or len(v_trees) != last + 1:
             raise EagleError("commit takes the tree K/V of every layer")
@@ -87,7 +96,7 @@ class KV8Cache:
                 lens = self._len
                 lens.copy_(self.kv_len)
             slot_mapping = kv8_commit(k, v, accept_len, path_nodes, *self._pools(layer), lens, self.block_table,
-                                      slot_mapping=slot_mapping, status=self.status)
+                                      slot_mapping=slot_mapping, status=self.status, root=root)
         return slot_mapping
 
     def trim(self):

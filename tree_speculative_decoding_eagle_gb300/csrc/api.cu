@@ -83,7 +83,7 @@ cudaError_t launch_kv8_append(const void *k, const void *v, int dtype, int T, in
                               int64_t head_stride, const int32_t *slot_map, uint8_t *k_pages, uint8_t *v_pages,
                               float *k_scale, float *v_scale, int page_size, int num_pages, int32_t *status,
                               int num_sms, cudaStream_t st);
-cudaError_t launch_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+cudaError_t launch_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh, bool root,
                               const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages,
                               uint8_t *v_pages, float *k_scale, float *v_scale, const int32_t *block_table,
                               int max_pages, int page_size, int num_pages, int32_t *kv_len, int32_t *slot_mapping,
@@ -414,10 +414,10 @@ int eagle_kv8_append(const void *k, const void *v, int dtype, int T, int Hkv, in
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
-                     const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages, uint8_t *v_pages,
-                     float *k_scale, float *v_scale, const int32_t *block_table, int max_pages, int page_size,
-                     int num_pages, int32_t *kv_len, int32_t *slot_mapping, int32_t *status, eagle_stream_t stream) {
+static int kv8_commit(bool root, const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+                      const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages, uint8_t *v_pages,
+                      float *k_scale, float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                      int num_pages, int32_t *kv_len, int32_t *slot_mapping, int32_t *status, eagle_stream_t stream) {
   if (!k_tree || !v_tree || !accept_len || !path_nodes || !k_pages || !v_pages || !k_scale || !v_scale ||
       !block_table || !kv_len)
     return EAGLE_ERR_INVALID;
@@ -427,9 +427,26 @@ int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, i
   if (Hkv > 32767 || B > 65535) return EAGLE_ERR_UNSUPPORTED;
   if (!aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_pages) || !aligned16(v_pages))
     return EAGLE_ERR_INVALID;
-  return from_cuda(launch_kv8_commit(k_tree, v_tree, dtype, B, n, Hkv, dh, accept_len, path_nodes, D, k_pages,
+  return from_cuda(launch_kv8_commit(k_tree, v_tree, dtype, B, n, Hkv, dh, root, accept_len, path_nodes, D, k_pages,
                                      v_pages, k_scale, v_scale, block_table, max_pages, page_size, num_pages, kv_len,
                                      slot_mapping, status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+                     const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages, uint8_t *v_pages,
+                     float *k_scale, float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                     int num_pages, int32_t *kv_len, int32_t *slot_mapping, int32_t *status, eagle_stream_t stream) {
+  return kv8_commit(false, k_tree, v_tree, dtype, B, n, Hkv, dh, accept_len, path_nodes, D, k_pages, v_pages, k_scale,
+                    v_scale, block_table, max_pages, page_size, num_pages, kv_len, slot_mapping, status, stream);
+}
+
+int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+                          const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages,
+                          uint8_t *v_pages, float *k_scale, float *v_scale, const int32_t *block_table, int max_pages,
+                          int page_size, int num_pages, int32_t *kv_len, int32_t *slot_mapping, int32_t *status,
+                          eagle_stream_t stream) {
+  return kv8_commit(true, k_tree, v_tree, dtype, B, n, Hkv, dh, accept_len, path_nodes, D, k_pages, v_pages, k_scale,
+                    v_scale, block_table, max_pages, page_size, num_pages, kv_len, slot_mapping, status, stream);
 }
 
 // Query rows of a KV head: their M-groups are a grid dimension, their number an int.

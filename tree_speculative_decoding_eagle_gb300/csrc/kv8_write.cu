@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 3 : 2) kv8_
 struct Commit8Args {
   const void *k_tree, *v_tree;
   int B, n, Hkv, dh, D, log_page, max_pages, num_pages;
+  int skip;  // path entries before the first that is stored: 0 stores the root, 1 finds it stored
   const int32_t *accept_len, *path_nodes;
   uint8_t *k_pages, *v_pages;
   float *k_scale, *v_scale;
@@ -276,18 +277,19 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_commit_kernel(Commit8Arg
   const int P = 1 << a.log_page;
   pdl_wait();
   const int L = a.kv_len[b], acc = a.accept_len[b];
+  const int rows = acc + 1 - a.skip;  // path[skip..acc]
   if (warp == 0) {
-    bool ok = acc >= 0 && acc <= a.D && acc <= 64 && L >= 1 &&
-              static_cast<int64_t>(L) + acc <= (static_cast<int64_t>(a.max_pages) << a.log_page);
+    bool ok = acc >= 0 && acc <= a.D && acc <= 64 && L >= a.skip &&
+              static_cast<int64_t>(L) + rows <= (static_cast<int64_t>(a.max_pages) << a.log_page);
     if (ok) {
-      for (int p = 1 + lane; p <= acc; p += 32) {
+      for (int p = a.skip + lane; p <= acc; p += 32) {
         const int node = a.path_nodes[static_cast<int64_t>(b) * (a.D + 1) + p];
         s_path[p] = node;
-        if (node < 1 || node >= a.n) ok = false;
+        if (p == 0 ? node != 0 : node < 1 || node >= a.n) ok = false;
       }
-      // at most 64 rows in pages of at least 16: five pages
+      // at most 65 rows in pages of at least 16: five pages
       const int lp = (L >> a.log_page) + lane;
-      if (acc > 0 && lp <= (L + acc - 1) >> a.log_page) {
+      if (rows > 0 && lp <= (L + rows - 1) >> a.log_page) {
         const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + lp];
         s_page[lane] = page;
         if (page < 0 || page >= a.num_pages) ok = false;
@@ -306,26 +308,26 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_commit_kernel(Commit8Arg
   }
   pdl_trigger();
   if (!s_ok) return;
-  if (rank == 0 && tid == 0) a.kv_len[b] = L + acc;
+  if (rank == 0 && tid == 0) a.kv_len[b] = L + rows;
   for (int u = rank * kWriteWarps + warp; u < 2 * a.Hkv; u += ctas * kWriteWarps) {
     const int g = u >> 1;
     const bool is_v = u & 1;
     const T *src = reinterpret_cast<const T *>(is_v ? a.v_tree : a.k_tree) +
                    (static_cast<int64_t>(b) * a.Hkv + g) * a.n * a.dh;
-    for (int p = 1, lp = 0; p <= acc; ++lp) {
-      const int first = (L + p - 1) & (P - 1), count = min(acc - p + 1, P - first);
+    for (int r = 0, lp = 0; r < rows; ++lp) {
+      const int first = (L + r) & (P - 1), count = min(rows - r, P - first);
       const int64_t at = static_cast<int64_t>(s_page[lp]) * a.Hkv + g;
-      write_run<T>(PathRows<T>{src, s_path + p, a.dh}, count,
+      write_run<T>(PathRows<T>{src, s_path + a.skip + r, a.dh}, count,
                    (is_v ? a.v_pages : a.k_pages) + (at << a.log_page) * a.dh, (is_v ? a.v_scale : a.k_scale) + at,
                    first, a.dh, 0, 1, 0, nullptr, a.status);
-      p += count;
+      r += count;
     }
   }
   if (a.slot_mapping) {
     for (int i = rank * kWriteWarps * 32 + tid; i < a.n; i += ctas * kWriteWarps * 32) {
-      int slot = i == 0 ? L - 1 : -1;
+      int slot = i == 0 ? L - a.skip : -1;
       for (int p = 1; p <= acc; ++p)
-        if (s_path[p] == i) slot = L + p - 1;
+        if (s_path[p] == i) slot = L + p - a.skip;
       a.slot_mapping[static_cast<int64_t>(b) * a.n + i] = slot;
     }
   }
@@ -364,12 +366,12 @@ cudaError_t launch_kv8_append(const void *k, const void *v, int dtype, int T, in
                              : launch_chained(kv8_append_kernel<float>, grid, dim3(kWriteWarps * 32), 0, st, a);
 }
 
-cudaError_t launch_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh,
+cudaError_t launch_kv8_commit(const void *k_tree, const void *v_tree, int dtype, int B, int n, int Hkv, int dh, bool root,
                               const int32_t *accept_len, const int32_t *path_nodes, int D, uint8_t *k_pages,
                               uint8_t *v_pages, float *k_scale, float *v_scale, const int32_t *block_table,
                               int max_pages, int page_size, int num_pages, int32_t *kv_len, int32_t *slot_mapping,
                               int32_t *status, cudaStream_t st) {
-  Commit8Args a = {k_tree, v_tree, B, n, Hkv, dh, D, log2_page(page_size), max_pages, num_pages, accept_len,
+  Commit8Args a = {k_tree, v_tree, B, n, Hkv, dh, D, log2_page(page_size), max_pages, num_pages, root ? 0 : 1, accept_len,
                    path_nodes, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, slot_mapping, status};
   int ctas = 1;  // a warp for each (head, K or V), eight CTAs at most
   while (ctas < 8 && ctas * kWriteWarps < 2 * Hkv) ctas *= 2;

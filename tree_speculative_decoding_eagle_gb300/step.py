@@ -62,6 +62,12 @@ class TreeStep:
             self.attn_out = torch.empty_like(q)
         return cache.attend(layer, q, k_tree, v_tree, self.tree["mask"], scale, self.attn_out, self.lse)
 
+    def commit_kv8(self, cache, k_trees, v_trees):
+        """After verify(): the root's and the accepted nodes' rows of every layer
+        into a KV8Cache that reserved D + 1 positions; its kv_len grows by
+        accept_len + 1, and the bonus token is the next step's root."""
+        return cache.commit(k_trees, v_trees, self.accept_len, self.path_nodes, root=True)
+
     def verify(self, target, uniforms=None):
         verify(target, self.tree["tok"], self.tree["parent"], self.D, self.mode, self.temperature,
                uniforms, self.accept_len, self.path_nodes, self.out_tokens, self.status,
