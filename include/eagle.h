@@ -11,7 +11,8 @@
  *   eagle_verify      greedy or speculative-sampling verification walk
  * and eagle_step runs the four in order (or replays them as one graph).
  * Around them, for a serving loop whose KV cache is paged and held in 8 bits:
- *   eagle_page_map, eagle_page_release   pages of a free list to requests and back
+ *   eagle_page_map, eagle_page_reserve, eagle_page_release   pages of a free
+ *                                        list to requests and back
  *   eagle_rope                           rotary positions of q and k
  *   eagle_kv8_append, eagle_kv8_commit, eagle_kv8_commit_root   keys and values into the 8-bit cache
  *   eagle_tree_attn_kv8                  the tree attention over that cache
@@ -520,6 +521,23 @@ int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B,
                    const int32_t *free_pages, int32_t *free_count,
                    int32_t *slot_map, int T, int32_t *new_start,
                    int32_t *status, eagle_stream_t stream);
+
+/* eagle_page_map for a loop that does not look at `status` before what comes
+ * next (a captured one cannot).  When the map is refused, slot_map and
+ * new_start would keep what an earlier call left there, and eagle_kv8_append
+ * would write through slots that may belong to another request by then.  Here
+ * a refusal is written out: slot_map becomes -1 throughout (the append skips
+ * such tokens), new_start 0, and
+ *   granted      device int32 [B] (out): new_len, or 0 for every request of a
+ *                refused map: what the requests' lengths may grow by
+ * Everything else is as eagle_page_map leaves it, status included. */
+int eagle_page_reserve(const int32_t *kv_len, const int32_t *new_len, int B,
+                       int page_size, int max_pages, int num_pages,
+                       int32_t *block_table, int32_t *page_count,
+                       const int32_t *free_pages, int32_t *free_count,
+                       int32_t *slot_map, int T, int32_t *new_start,
+                       int32_t *granted, int32_t *status,
+                       eagle_stream_t stream);
 
 /* Pages back to the free list.  Request b keeps its first
  * min(page_count[b], ceil(keep_len[b] / P)) pages (keep_len 0: none; its

@@ -53,3 +53,15 @@ def test_commit_root_refusals():
     for change, code in changes:
         args = [change.get(i, a) for i, a in enumerate(good)]
         assert lib.eagle_kv8_commit_root(*args) == code, change
+
+
+def test_page_reserve_refusals():
+    from tree_speculative_decoding_eagle_gb300 import build
+    build.build()
+    lib = eg.load_library()
+    good = [FAKE, FAKE, 4, 16, 8, 64, FAKE, FAKE, FAKE, FAKE, FAKE, 10, None, FAKE, None, None]
+    changes = [({p: None}, -1) for p in (0, 1, 6, 7, 8, 9, 10, 13)]
+    changes += [(c, -1) for c in ({2: 0}, {3: 24}, {4: 0}, {5: 0}, {5: 1 << 27}, {11: -1}, {11: (1 << 30) + 1})] + [({2: 4097}, -2)]
+    for change, code in changes:
+        args = [change.get(i, a) for i, a in enumerate(good)]
+        assert lib.eagle_page_reserve(*args) == code, change

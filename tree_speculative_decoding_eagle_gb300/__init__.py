@@ -18,8 +18,9 @@ library is missing or a call reports an error, an exception is raised.
     verify_noalloc -> eagle_verify_noalloc (the same without a caller workspace)
     verify_draft -> eagle_verify_draft (sampling walk against draft distributions q)
     selftest_wait -> eagle_selftest_wait (a bounded device wait that must give up)
-    page_map / page_release -> eagle_page_map, eagle_page_release (pages of a
-                   free list to requests and back; slots of new tokens)
+    page_map / page_release -> eagle_page_map, eagle_page_reserve,
+                   eagle_page_release (pages of a free list to requests and
+                   back; slots of new tokens)
     rope        -> eagle_rope         (rotary positions, into the attention's layouts;
                    rope_freqs -> eagle_rope_freqs)
     kv8_append / kv8_commit -> eagle_kv8_append, eagle_kv8_commit,
@@ -49,7 +50,7 @@ EXPORTED = (
     "eagle_tree_attn_workspace_size", "eagle_tree_attn_kernel_count", "eagle_tree_attn",
     "eagle_tree_attn_paged_workspace_size", "eagle_tree_attn_paged", "eagle_kv_commit",
     "eagle_verify_workspace_size", "eagle_verify", "eagle_verify_noalloc", "eagle_verify_draft",
-    "eagle_page_map", "eagle_page_release", "eagle_rope", "eagle_rope_freqs",
+    "eagle_page_map", "eagle_page_reserve", "eagle_page_release", "eagle_rope", "eagle_rope_freqs",
     "eagle_kv8_append", "eagle_kv8_commit", "eagle_kv8_commit_root", "eagle_tree_attn_kv8_workspace_size", "eagle_tree_attn_kv8",
     "eagle_step_workspace_size", "eagle_step", "eagle_step_graph_create", "eagle_step_graph_launch",
     "eagle_step_graph_destroy",
@@ -115,6 +116,7 @@ def load_library(path=LIB_PATH):
         "eagle_verify_noalloc": (I, [P, I, I64, P, P, I, I, I, I, I, F, P, P, P, P, P, P]),
         "eagle_verify_draft": (I, [P, P, I, I64, I64, P, P, P, I, I, I, I, I, F, P, P, P, P, P, P]),
         "eagle_page_map": (I, [P, P, I, I, I, I, P, P, P, P, P, I, P, P, P]),
+        "eagle_page_reserve": (I, [P, P, I, I, I, I, P, P, P, P, P, I, P, P, P, P]),
         "eagle_page_release": (I, [P, I, I, I, I, P, P, P, P, P, P]),
         "eagle_rope": (I, [P, P, P, I, I, I, I, I, I, I64, I64, I64, P, I, I, F, P, P, I, P, P, P, P]),
         "eagle_rope_freqs": (I, [I, ctypes.c_double, I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double, P, P]),
@@ -452,7 +454,7 @@ def _call(what, fn, dev, stream, *args):
 
 
 def page_map(kv_len, new_len, block_table, page_count, free_pages, free_count, page_size, slot_map=None,
-             new_start=None, status=None, stream=None):
+             new_start=None, status=None, stream=None, granted=None):
     """Maps the pages that new_len [B] more tokens need and lists the tokens'
     slots (eagle_page_map).  kv_len, new_len, page_count int32 [B], block_table
     int32 [B, max_pages], free_pages int32 [num_pages], free_count int32 [1];
@@ -460,17 +462,21 @@ def page_map(kv_len, new_len, block_table, page_count, free_pages, free_count, p
     int32 [T] (optional) receives the slots of the new tokens, request by
     request, then -1; new_start int32 [B+1] (optional) their first indices.
     Returns slot_map.  Too few free pages leave everything as it was and set
-    `status` to -6."""
+    `status` to -6; with `granted` int32 [B] (eagle_page_reserve) slot_map is
+    then -1 throughout, and granted 0 instead of new_len."""
     lib = load_library()
     dev, i32 = _device_of(kv_len, "kv_len"), torch.int32
     B, max_pages = block_table.shape
     num_pages = free_pages.shape[0]
-    _call("eagle_page_map", lib.eagle_page_map, dev, stream, _need(kv_len, "kv_len", i32, (B,), dev),
+    name, more = "eagle_page_map", ()
+    if granted is not None:
+        name, more = "eagle_page_reserve", (_need(granted, "granted", i32, (B,), dev),)
+    _call(name, getattr(lib, name), dev, stream, _need(kv_len, "kv_len", i32, (B,), dev),
           _need(new_len, "new_len", i32, (B,), dev), B, page_size, max_pages, num_pages,
           _need(block_table, "block_table", i32, None, dev), _need(page_count, "page_count", i32, (B,), dev),
           _need(free_pages, "free_pages", i32, (num_pages,), dev), _need(free_count, "free_count", i32, (1,), dev),
           _maybe(slot_map, "slot_map", i32, None, dev), 0 if slot_map is None else slot_map.numel(),
-          _maybe(new_start, "new_start", i32, (B + 1,), dev), _maybe(status, "status", i32, None, dev))
+          _maybe(new_start, "new_start", i32, (B + 1,), dev), *more, _maybe(status, "status", i32, None, dev))
     return slot_map
 
 

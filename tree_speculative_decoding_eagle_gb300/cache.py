@@ -3,7 +3,7 @@
 KV8Cache owns the pages (e4m3 numbers and their scales, one pool of keys and one of
 values per layer), the block tables, the free list and the requests' lengths,
 all on the device, and calls the library's entry points on the current stream:
-    reserve  -> eagle_page_map      pages and slots for new tokens
+    reserve  -> eagle_page_reserve  pages and slots for new tokens
     append   -> eagle_kv8_append    a prompt's (or single tokens') keys and values
     attend   -> eagle_tree_attn_kv8 draft nodes or single tokens over the cache
     commit   -> eagle_kv8_commit_root (root=True), eagle_kv8_commit
@@ -59,15 +59,20 @@ class KV8Cache:
         self.kv_len = torch.zeros(B, **i32)
         self.status = torch.zeros(1, **i32)
         self._len = torch.zeros(B, **i32)      # the lengths that all layers but the last commit to
+        # what the last reservation granted: no limit before the first
+        self.granted = torch.full((B,), 2 ** 31 - 1, **i32)
+        self._grown = torch.zeros(B, **i32)
         self._ws = _KeptWorkspace(device)
 
     def _pools(self, layer):
         return self.k_pages[layer], self.v_pages[layer], self.k_scale[layer], self.v_scale[layer]
 
     def reserve(self, new_len, slot_map=None, new_start=None):
-        """Pages for new_len [B] more tokens; their slots into slot_map."""
+        """Pages for new_len [B] more tokens; their slots into slot_map.  With
+        too few free pages nobody gets any: `status` says so, slot_map is -1
+        throughout, so that append() writes nothing, and grow() counts nothing."""
         return page_map(self.kv_len, new_len, self.block_table, self.page_count, self.free_pages, self.free_count,
-                        self.page_size, slot_map=slot_map, new_start=new_start, status=self.status)
+                        self.page_size, slot_map=slot_map, new_start=new_start, status=self.status, granted=self.granted)
 
     def append(self, layer, k, v, slot_map):
         """One layer's keys and values [T, Hkv, dh] to the reserved slots;
@@ -75,7 +80,13 @@ class KV8Cache:
         kv8_append(k, v, slot_map, *self._pools(layer), status=self.status)
 
     def grow(self, new_len):
-        self.kv_len.add_(new_len)
+        """new_len [B] tokens have been appended, no more than the last
+        reservation granted."""
+        if torch.is_tensor(new_len):
+            torch.minimum(self.granted, new_len, out=self._grown)
+        else:
+            torch.clamp(self.granted, max=new_len, out=self._grown)
+        self.kv_len.add_(self._grown)
 
     def attend(self, layer, q, k_tree, v_tree, mask, scale=None, out=None, lse=None, workspace=None):
         return tree_attn_kv8(q, *self._pools(layer), self.block_table, self.kv_len, k_tree, v_tree, mask, scale=scale,

@@ -66,8 +66,8 @@ cudaError_t launch_verify(const void *target, int dtype, int64_t ld, const int32
 // page_map.cu
 cudaError_t launch_page_map(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages,
                             int num_pages, int32_t *block_table, int32_t *page_count, const int32_t *free_pages,
-                            int32_t *free_count, int32_t *slot_map, int T, int32_t *new_start, int32_t *status,
-                            cudaStream_t st);
+                            int32_t *free_count, int32_t *slot_map, int T, int32_t *new_start, int32_t *granted,
+                            int32_t *status, cudaStream_t st);
 cudaError_t launch_page_release(const int32_t *keep_len, int B, int page_size, int max_pages, int num_pages,
                                 int32_t *block_table, int32_t *page_count, int32_t *free_pages, int32_t *free_count,
                                 int32_t *status, cudaStream_t st);
@@ -342,16 +342,33 @@ static bool valid_slots(int max_pages, int page_size, int num_pages) {
   return valid_pages(max_pages, page_size, num_pages) && static_cast<int64_t>(num_pages) * page_size <= INT32_MAX;
 }
 
-int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages, int num_pages,
-                   int32_t *block_table, int32_t *page_count, const int32_t *free_pages, int32_t *free_count,
-                   int32_t *slot_map, int T, int32_t *new_start, int32_t *status, eagle_stream_t stream) {
+static int map_pages(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages, int num_pages,
+                     int32_t *block_table, int32_t *page_count, const int32_t *free_pages, int32_t *free_count,
+                     int32_t *slot_map, int T, int32_t *new_start, int32_t *granted, int32_t *status,
+                     eagle_stream_t stream) {
   if (!kv_len || !new_len || !block_table || !page_count || !free_pages || !free_count) return EAGLE_ERR_INVALID;
   if (B < 1 || T < 0 || T > kMaxTokens || (!slot_map && T) || !valid_slots(max_pages, page_size, num_pages))
     return EAGLE_ERR_INVALID;
   if (B > 4096) return EAGLE_ERR_UNSUPPORTED;  // one CTA's shared memory holds every request's sums
   return from_cuda(launch_page_map(kv_len, new_len, B, page_size, max_pages, num_pages, block_table, page_count,
-                                   free_pages, free_count, slot_map, T, new_start, status,
+                                   free_pages, free_count, slot_map, T, new_start, granted, status,
                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages, int num_pages,
+                   int32_t *block_table, int32_t *page_count, const int32_t *free_pages, int32_t *free_count,
+                   int32_t *slot_map, int T, int32_t *new_start, int32_t *status, eagle_stream_t stream) {
+  return map_pages(kv_len, new_len, B, page_size, max_pages, num_pages, block_table, page_count, free_pages, free_count,
+                   slot_map, T, new_start, nullptr, status, stream);
+}
+
+int eagle_page_reserve(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages,
+                       int num_pages, int32_t *block_table, int32_t *page_count, const int32_t *free_pages,
+                       int32_t *free_count, int32_t *slot_map, int T, int32_t *new_start, int32_t *granted,
+                       int32_t *status, eagle_stream_t stream) {
+  if (!granted) return EAGLE_ERR_INVALID;
+  return map_pages(kv_len, new_len, B, page_size, max_pages, num_pages, block_table, page_count, free_pages, free_count,
+                   slot_map, T, new_start, granted, status, stream);
 }
 
 int eagle_page_release(const int32_t *keep_len, int B, int page_size, int max_pages, int num_pages,

@@ -35,6 +35,7 @@ struct PageArgs {
   int32_t *block_table, *page_count, *free_pages, *free_count;
   int32_t *slot_map, *new_start, *status;
   int T;
+  int32_t *granted;  // map: with it a refusal is written out too
 };
 
 // Shared arrays, B (+ 1) entries each.
@@ -140,6 +141,13 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(PageArgs a) {
   pdl_trigger();
   if (err) {  // the same in every CTA
     if (rank == 0 && tid == 0) report(a.status, err);
+    if (a.granted) {  // nothing granted: no slot, no token
+      for (int t = rank * kPageThreads + tid; t < a.T; t += ctas * kPageThreads) a.slot_map[t] = -1;
+      for (int b = rank * kPageThreads + tid; b <= a.B; b += ctas * kPageThreads) {
+        if (b < a.B) a.granted[b] = 0;
+        if (a.new_start) a.new_start[b] = 0;
+      }
+    }
     return;
   }
   // new table entries, and the requests' own words
@@ -151,6 +159,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(PageArgs a) {
     const int add = s.first[b + 1] - s.first[b];
     if (add) a.page_count[b] = s.count[b] + add;
     if (a.new_start) a.new_start[b] = s.start[b];
+    if (a.granted) a.granted[b] = s.start[b + 1] - s.start[b];
   }
   if (rank == 0 && tid == 0) {
     if (pages) *a.free_count = fc - static_cast<int>(pages);
@@ -241,13 +250,13 @@ static int log2_of(int p) {
 
 cudaError_t launch_page_map(const int32_t *kv_len, const int32_t *new_len, int B, int page_size, int max_pages,
                             int num_pages, int32_t *block_table, int32_t *page_count, const int32_t *free_pages,
-                            int32_t *free_count, int32_t *slot_map, int T, int32_t *new_start, int32_t *status,
-                            cudaStream_t st) {
+                            int32_t *free_count, int32_t *slot_map, int T, int32_t *new_start, int32_t *granted,
+                            int32_t *status, cudaStream_t st) {
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = set_smem_limit_once(page_map_kernel, static_cast<int>(page_smem_bytes(kPageMaxB)), configured);
   if (e != cudaSuccess) return e;
   PageArgs a = {kv_len, new_len, B, log2_of(page_size), max_pages, num_pages, block_table, page_count,
-                const_cast<int32_t *>(free_pages), free_count, slot_map, new_start, status, T};
+                const_cast<int32_t *>(free_pages), free_count, slot_map, new_start, status, T, granted};
   int ctas = 1;
   while (ctas < 8 && ctas * kPageTokensPerCta < T) ctas *= 2;
   return launch_chained_cluster(page_map_kernel, dim3(ctas), dim3(kPageThreads), page_smem_bytes(B), st, ctas, a);
@@ -260,7 +269,7 @@ cudaError_t launch_page_release(const int32_t *keep_len, int B, int page_size, i
   cudaError_t e = set_smem_limit_once(page_release_kernel, static_cast<int>(page_smem_bytes(kPageMaxB)), configured);
   if (e != cudaSuccess) return e;
   PageArgs a = {keep_len, nullptr, B, log2_of(page_size), max_pages, num_pages, block_table, page_count,
-                free_pages, free_count, nullptr, nullptr, status, 0};
+                free_pages, free_count, nullptr, nullptr, status, 0, nullptr};
   return launch_chained(page_release_kernel, dim3(1), dim3(kPageThreads), page_smem_bytes(B), st, a);
 }
 
