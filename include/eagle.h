@@ -511,7 +511,8 @@ int eagle_kv_commit(const void *k_tree, const void *v_tree, int dtype, int B,
  *                [0, num_pages], or more than T new tokens with a slot_map.
  *                Nothing is written then.  A page number outside
  *                [0, num_pages) in either list gives slot -1 and
- *                EAGLE_ERR_INVALID.
+ *                EAGLE_ERR_INVALID (one that is taken from the free list
+ *                becomes block_table entry -1, with or without a slot_map).
  * Limits: 1 <= B <= 4096; T <= 2^30; page rules as for
  * eagle_tree_attn_paged; num_pages * page_size < 2^31.
  * ------------------------------------------------------------------------ */
@@ -549,8 +550,9 @@ int eagle_page_reserve(const int32_t *kv_len, const int32_t *new_len, int B,
  * free_count grows by R.
  *   keep_len     device int32 [B]; the other arrays as in eagle_page_map
  *   status       EAGLE_ERR_INVALID (nothing written) for a page_count outside
- *                [0, max_pages], a free_count below 0 or a free list that
- *                would exceed num_pages entries.
+ *                [0, max_pages], a free_count below 0, a free list that
+ *                would exceed num_pages entries, or an entry to be given back
+ *                that is no page (outside [0, num_pages)).
  * Limits as for eagle_page_map. */
 int eagle_page_release(const int32_t *keep_len, int B, int page_size,
                        int max_pages, int num_pages, int32_t *block_table,

@@ -12,8 +12,9 @@
 // number of tokens); every CTA reads all lengths and makes the sums itself in
 // shared memory (12 bytes a request, from L2 after the first), which
 // costs less than handing them over, and then writes its share of the outputs.
-// Measured, a map and a release together (two launches in a graph): 6.4 us for
-// one request, 11.1 us for 512 requests with up to 32768 new tokens, whose 0.2
+// Measured, a map and a release together (two launches in a graph): 6.8 us for
+// one request, 11.5 us for 512 requests with up to 32768 new tokens (0.3 us of
+// it for looking at every page number before a release writes the first), whose 0.2
 // MB would stream in 0.03 us: the chain is two launches, the lengths, two sums,
 // a bisection and the free list's entries.
 // Everything that is updated in place (page_count, free_count) is written only
@@ -151,9 +152,12 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(PageArgs a) {
     return;
   }
   // new table entries, and the requests' own words
+  bool lost = false;  // a page number outside the pool
   for (int j = rank * kPageThreads + tid; j < pages; j += ctas * kPageThreads) {
-    const int b = owner_of(s.first, a.B, j);
-    a.block_table[static_cast<int64_t>(b) * a.max_pages + s.count[b] + (j - s.first[b])] = a.free_pages[fc - 1 - j];
+    const int b = owner_of(s.first, a.B, j), page = a.free_pages[fc - 1 - j];
+    const bool ok = page >= 0 && page < a.num_pages;
+    lost |= !ok;
+    a.block_table[static_cast<int64_t>(b) * a.max_pages + s.count[b] + (j - s.first[b])] = ok ? page : -1;
   }
   for (int b = rank * kPageThreads + tid; b < a.B; b += ctas * kPageThreads) {
     const int add = s.first[b + 1] - s.first[b];
@@ -168,7 +172,6 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(PageArgs a) {
   // slots: a thread takes four neighbouring tokens, finds the first one's
   // request by bisection and walks on from there
   const int n_tok = static_cast<int>(tokens);
-  bool lost = false;
   for (int t0 = (rank * kPageThreads + tid) * 4; t0 < a.T; t0 += ctas * kPageThreads * 4) {
     int b = t0 < n_tok ? owner_of(s.start, a.B, t0) : 0;
 #pragma unroll
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(kPageThreads) page_release_kernel(PageArgs a) 
     block_exclusive_sum2(x, y, tx, ty, part);
     if (b < a.B) {
       s.kv[b] = keep;
+      s.count[b] = cnt;
       s.first[b] = static_cast<int32_t>(min(pages + y, static_cast<int64_t>(INT32_MAX)));
     }
     pages += ty;
@@ -231,14 +235,45 @@ __global__ void __launch_bounds__(kPageThreads) page_release_kernel(PageArgs a) 
     return;
   }
   const int R = static_cast<int>(pages);
-  for (int j = tid; j < R; j += kPageThreads) {
+  const auto entry_of = [&](int j) {
     const int b = owner_of(s.first, a.B, j);
-    int32_t *entry = a.block_table + static_cast<int64_t>(b) * a.max_pages + s.kv[b] + (j - s.first[b]);
-    a.free_pages[fc + R - 1 - j] = *entry;
-    *entry = -1;
+    return a.block_table + static_cast<int64_t>(b) * a.max_pages + s.kv[b] + (j - s.first[b]);
+  };
+  // every page number is looked at before the first is handed on; a thread's
+  // first kHeldPages stay in registers meanwhile
+  constexpr int kHeldPages = 4;
+  int32_t *entry[kHeldPages];
+  int page[kHeldPages];
+  bool lost = false;  // a number that is no page
+#pragma unroll
+  for (int u = 0; u < kHeldPages; ++u) {
+    const int j = tid + u * kPageThreads;
+    entry[u] = j < R ? entry_of(j) : nullptr;
+    page[u] = entry[u] ? *entry[u] : 0;
+  }
+#pragma unroll
+  for (int u = 0; u < kHeldPages; ++u) lost |= page[u] < 0 || page[u] >= a.num_pages;
+  for (int j = tid + kHeldPages * kPageThreads; j < R; j += kPageThreads) {
+    const int p = *entry_of(j);
+    lost |= p < 0 || p >= a.num_pages;
+  }
+  if (__syncthreads_or(lost)) {
+    if (tid == 0) report(a.status, EAGLE_ERR_INVALID);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < kHeldPages; ++u)
+    if (entry[u]) {
+      a.free_pages[fc + R - 1 - (tid + u * kPageThreads)] = page[u];
+      *entry[u] = -1;
+    }
+  for (int j = tid + kHeldPages * kPageThreads; j < R; j += kPageThreads) {
+    int32_t *e = entry_of(j);
+    a.free_pages[fc + R - 1 - j] = *e;
+    *e = -1;
   }
   for (int b = tid; b < a.B; b += kPageThreads)
-    if (a.page_count[b] != s.kv[b]) a.page_count[b] = s.kv[b];
+    if (s.count[b] != s.kv[b]) a.page_count[b] = s.kv[b];
   if (tid == 0 && R) *a.free_count = fc + R;
 }
 
