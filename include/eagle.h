@@ -641,8 +641,11 @@ int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch,
  *             skipped.  The tokens of one page are neighbours in slot_map with
  *             consecutive rows (as eagle_page_map lists them): a neighbour in
  *             the same page that breaks the sequence is skipped and sets
- *             EAGLE_ERR_INVALID, as does a slot past the pool.  A page that is
- *             listed in two places of slot_map ends up unspecified.
+ *             EAGLE_ERR_INVALID, as does a slot past the pool.  So does a page
+ *             that comes again after skipped tokens (up to 1024 of them) or
+ *             within 32 tokens: its first tokens are written, the later ones
+ *             skipped.  A page that is listed in two places further apart ends
+ *             up unspecified.
  *   status    device int32 (out; may be NULL)
  * Limits: 0 <= T <= 2^30; dh a multiple of 16, at most 512; strides *
  * elemsize multiples of 16 bytes, tensors 16-byte aligned; page_size a power

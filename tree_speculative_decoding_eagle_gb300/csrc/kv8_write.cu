@@ -6,14 +6,16 @@
 // one team's work: the largest magnitude of its rows, the exponent (joined
 // with the page's when earlier rows stay), the rows divided by 2^e and rounded
 // once to e4m3; when the exponent grew, the page's earlier rows are re-encoded
-// at the new one.  Two runs never share a page, so nothing is atomic and the
-// result does not depend on an order.
+// at the new one.  Two runs never share a page (a second one that is near is
+// found and skipped), so nothing is atomic and the result does not depend on an
+// order.
 //
 // What bounds it: HBM for prompts (2 or 4 bytes read, 1 written an element),
 // latency for single tokens and commits.  Measured: 65536 tokens of 8 heads of
-// 128, bf16, pages of 64: 76.4 us (5.3 TB/s, 79 % of a copy's rate; 403 MB); one
-// token of each of 64 requests, 8 heads of 64: 4.0 us; the accepted paths of 8
-// trees, 40 heads of 128: 7.7 us with a copy of kv_len before it.
+// 128, bf16, pages of 64: 77.4 us (5.2 TB/s, 78 % of a copy's rate; 403 MB; 76.5
+// without the look for an interrupted page); one token of each of 64 requests, 8
+// heads of 64: 4.4 us (4.2); the accepted paths of 8 trees, 40 heads of 128: 7.5
+// us with a copy of kv_len before it.
 #include "kv8.cuh"
 #include "sm100.cuh"
 
@@ -176,6 +178,12 @@ __device__ __forceinline__ void write_run(RowOf row_of, int count, uint8_t *page
   }
 }
 
+// Skipped tokens that a run's first token looks past for an earlier one of its
+// page (beside the 32 tokens before its piece, which it always looks at): eight
+// rounds of loads, only where nothing but skipped tokens precedes a run that does
+// not begin a page.
+constexpr int kLookBack = 1024;
+
 struct AppendArgs {
   const void *k, *v;
   int64_t token_stride, head_stride;
@@ -213,10 +221,11 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 3 : 2) kv8_
   int seen = 0;  // leaders before this 32-token piece
   for (int p0 = t0; p0 < t1; p0 += 32) {
     const int slot = p0 + lane < t1 ? a.slot_map[p0 + lane] : -1;
-    const int s_before = p0 > 0 ? a.slot_map[p0 - 1] : -1;
+    const int before = p0 - 32 + lane >= 0 ? a.slot_map[p0 - 32 + lane] : -1;
     int prev = __shfl_up_sync(0xffffffffu, slot, 1);
+    const int s_before = __shfl_sync(0xffffffffu, before, 31);
     if (lane == 0) prev = s_before;
-    const int page = page_of(slot);
+    const int page = page_of(slot), page_before = page_of(before);
     const bool same = page >= 0 && page == page_of(prev);
     // what is skipped: a slot past the pool, a row out of sequence
     if (u0 == 0 && warp == 0 && ((slot >= 0 && page < 0) || (same && slot != prev + 1))) report(a.status, EAGLE_ERR_INVALID);
@@ -226,6 +235,33 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 3 : 2) kv8_
       lead &= lead - 1;
       if (seen++ % teams != team) continue;
       const int s0 = __shfl_sync(0xffffffffu, slot, l), pg = s0 >> a.log_page, first = s0 & (P - 1);
+      // A page whose tokens are interrupted (by skipped ones, or by others): two
+      // runs of it would write its scale and rows at the same time.
+      const uint32_t below = (1u << l) - 1u;
+      bool again = (__ballot_sync(0xffffffffu, page == pg) & below) | __ballot_sync(0xffffffffu, page_before == pg);
+      if (!again && first && !((__ballot_sync(0xffffffffu, page >= 0) & below) | __ballot_sync(0xffffffffu, page_before >= 0))) {
+        bool found = false;
+        for (int back = p0 - 32; !found && back > 0 && back > p0 - 32 - kLookBack; back -= 128) {
+          int pages[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int t = back - 32 * (w + 1) + lane;
+            pages[w] = t >= 0 ? page_of(a.slot_map[t]) : -1;
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t on = __ballot_sync(0xffffffffu, pages[w] >= 0);
+            if (on && !found) {  // the nearest token that is not skipped
+              found = true;
+              again = __shfl_sync(0xffffffffu, pages[w], 31 - __clz(on)) == pg;
+            }
+          }
+        }
+      }
+      if (again) {
+        if (u0 == 0 && tw == 0 && lane == 0) report(a.status, EAGLE_ERR_INVALID);
+        continue;
+      }
       // the run: neighbours with the next slots, within the page; 96 tokens are
       // looked at with one latency
       int count = 1;
