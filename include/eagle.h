@@ -710,10 +710,13 @@ int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
  *              in its place), EAGLE_ERR_TIMEOUT as in eagle_tree_attn
  * A row without any key (kv_len 0, empty mask row) gives zeros and lse =
  * -inf; a row that attends to a NaN of the cache gives NaN.  Rows of a page at
- * or beyond kv_len may be read but never count, whatever they hold.  q, k_tree
- * and v_tree must be finite, mask-excluded rows of the tree too.  k_tree and
- * v_tree count down to 2^-25 of the largest magnitude among their neighbours
- * (16 to 128 nodes of a head); what is smaller is rounded there.
+ * or beyond kv_len may be read but never count, whatever they hold; nor do
+ * tree nodes that no row of the mask names.  q, and k_tree and v_tree of the
+ * nodes that some row names, must be finite.  An element of k_tree or v_tree is
+ * exact down to 2^-25 of the largest magnitude M among its neighbours and off by
+ * up to 2^-33 M below that; neighbours are the nodes of one block of 16 to 128
+ * of a head (page_size decides) that any of up to 256 neighbouring query rows
+ * names, so a large node costs rows bits that do not name it.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};
  * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31;
  * n * Hq/Hkv <= 2^23.

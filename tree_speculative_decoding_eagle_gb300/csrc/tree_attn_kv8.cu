@@ -70,11 +70,12 @@ struct Kv8Shape {
   static constexpr int kBarOff = kStagingOff + S8 * 2 * kByteTile;
   static constexpr int kGroups = NK / 16;
   static constexpr int kNumBars = 4 * S8 + 4 * SF + 4 * MT + 2 + (ONE ? 2 : 0);
-  // barriers, tensor-memory slot and abort flag, scales of the tiles' groups,
-  // exponents of the query rows
+  static constexpr int kNamedWords = QR == 64 ? 1 : 64;   // mask words of n nodes (64 rows: 64 nodes at most)
+  // barriers, tensor-memory slot and abort flag, scales of the tiles' groups, the
+  // nodes that the CTA's rows name, exponents of the query rows
   static constexpr int kScaleSlots = S8 + SF + 3;         // tiles between K's producer and the softmax
   static constexpr int kScaleOff = (kNumBars * 8 + 8 + 15) / 16 * 16;
-  static constexpr int kBarBytes = kScaleOff + kScaleSlots * kGroups * 8 + (ONE ? 32 : 0) + MT * QR;
+  static constexpr int kBarBytes = kScaleOff + kScaleSlots * kGroups * 8 + kNamedWords * 8 + (ONE ? 32 : 0) + MT * QR;
   // The barriers sit in the gap before the 1 KB-aligned buffers when it holds
   // them, else after the buffers.
   static constexpr int kSmem = kBarOff + (1008 > 2 * kBarBytes - 16 ? 1008 : 2 * kBarBytes - 16);
@@ -230,8 +231,9 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tree_sync + (ONE ? 2 : 0));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   uint2 *scales = reinterpret_cast<uint2 *>(ctl + Sh::kScaleOff);                   // [kScaleSlots][GR]
-  volatile float *tree_max = reinterpret_cast<volatile float *>(scales + Sh::kScaleSlots * GR);  // [K, V][4 converter warps]
-  signed char *q_exp = reinterpret_cast<signed char *>(scales + Sh::kScaleSlots * GR) + (ONE ? 32 : 0);      // [MT * QR]
+  unsigned short *named = reinterpret_cast<unsigned short *>(scales + Sh::kScaleSlots * GR);  // a bit a node, 16 to a group
+  volatile float *tree_max = reinterpret_cast<volatile float *>(named + 4 * Sh::kNamedWords);  // [K, V][4 converter warps]
+  signed char *q_exp = reinterpret_cast<signed char *>(named + 4 * Sh::kNamedWords) + (ONE ? 32 : 0);  // [MT * QR]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, mg = blockIdx.y;
@@ -261,12 +263,41 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  if (tid >= 64 && tid < 64 + 2 * Sh::kNamedWords) reinterpret_cast<uint32_t *>(named)[tid - 64] = 0;
+  __syncthreads();
   pdl_wait();  // inputs of this step come from earlier kernels
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, Sh::kTmemCols);
     tmem_relinquish();
   }
-  const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
+  const int kv_len = a.kv_len[b];
+  const int rows_total = n * a.G;
+  if (split == a.S - 1) {
+    // The nodes that any of the CTA's rows names: their mask words or'ed, so that
+    // padding decides no block's power of two.  Threads are words, and rows where
+    // there are fewer words.  Here, while kv_len is on its way, since a role's code
+    // pays for every register: in a warp of its own 70B takes 188 us, in the
+    // converters 160, here 152 (148 without).
+    const uint64_t *words = a.mask + static_cast<int64_t>(b) * n * a.W;
+    const int i1 = (min(rows_total, (mg + 1) * MT * 128) - 1) / a.G;
+    const int wl = a.W > 16 ? 32 : a.W > 8 ? 16 : a.W > 4 ? 8 : a.W > 2 ? 4 : a.W;  // words side by side
+    for (int w = lane & (wl - 1); w < ((a.W + wl - 1) & ~(wl - 1)); w += wl) {
+      uint64_t any = 0;
+#pragma unroll 4
+      for (int i = mg * MT * 128 / a.G + tid / wl; i <= i1; i += Sh::kThreads / wl)
+        if (w < a.W) any |= words[static_cast<int64_t>(i) * a.W + w];
+      uint32_t lo = static_cast<uint32_t>(any), hi = static_cast<uint32_t>(any >> 32);
+      for (int o = wl; o < 32; o *= 2) {
+        lo |= __shfl_xor_sync(0xffffffffu, lo, o);
+        hi |= __shfl_xor_sync(0xffffffffu, hi, o);
+      }
+      if (lane < wl && w < a.W) {
+        atomicOr(reinterpret_cast<uint32_t *>(named) + 2 * w, lo);
+        atomicOr(reinterpret_cast<uint32_t *>(named) + 2 * w + 1, hi);
+      }
+    }
+  }
+  const int L = static_cast<int>(min(static_cast<int64_t>(max(kv_len, 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
   const int n_ptiles = (L + NK - 1) / NK;
   const int tps = (n_ptiles + a.S - 1) / a.S;
   const int p0 = min(n_ptiles, split * tps), p1 = min(n_ptiles, p0 + tps);
@@ -275,7 +306,6 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
   // that the producers' scales never wait for them.
   const int np = p1 - p0, ntt = (split == a.S - 1) ? (n + NK - 1) / NK : 0, T = np + ntt;
   const int pfx0 = ntt == 1 ? 1 : 0, tree0 = ntt == 1 ? 0 : np;
-  const int rows_total = n * a.G;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -457,20 +487,24 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
       } else {
         // tree nodes: bf16 over a power of two, the group's or (ONE) the tile's;
         // all of a warp's groups are then loaded at once and their largest
-        // magnitude is exchanged with the other warps'
+        // magnitude is exchanged with the other warps'.  Nodes that no query row
+        // of this CTA names are zeros, so that what they hold decides nothing.
         constexpr int GW = ONE ? GR / 4 : 1;
         const __nv_bfloat16 *src = (kv ? a.v_tree : a.k_tree) + (static_cast<int64_t>(bg) * n + key0) * DH;
         bool gave_up = false;
         for (int g0 = cw; g0 < GR; g0 += 4 * GW) {
           uint4 x[GW][STEPS], y[GW][STEPS];
           float amax = 0.f;
+          uint32_t live = 0;  // bit 16 w + c: node c of the warp's group w
+#pragma unroll
+          for (int w = 0; w < GW; ++w) live |= static_cast<uint32_t>(named[(key0 >> 4) + g0 + 4 * w]) << (16 * w);
 #pragma unroll
           for (int w = 0; w < GW; ++w)
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
               const int r = (g0 + 4 * w) * 16 + row_of(s);
               x[w][s] = y[w][s] = make_uint4(0, 0, 0, 0);
-              if (r < valid) {
+              if (r < valid && ((live >> (16 * w + row_of(s))) & 1u)) {
                 const uint4 *p = reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * DH + cc * 16);
                 x[w][s] = p[0];
                 y[w][s] = p[1];

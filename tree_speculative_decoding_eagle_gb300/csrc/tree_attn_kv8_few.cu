@@ -311,13 +311,16 @@ __global__ void __launch_bounds__(128, 3)
       const __nv_bfloat16 *vt = a.v_tree + (static_cast<int64_t>(bg) * a.n + n0) * DH;
       uint4 x[2][DH / 32], y[4][DH / 64];
       float kmax = 0.f, vmax = 0.f;
+      // the nodes that a row attends to (there are at most kFewRows rows of nodes, so
+      // a lane each and one mask word); the others are zeros and decide nothing
+      uint32_t attended = 0;
+      if (lane < a.n) attended = static_cast<uint32_t>(a.mask[static_cast<int64_t>(b) * a.n + lane] >> n0) & 0xffffu;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) {
           x[h][i] = make_uint4(0, 0, 0, 0);
           if (n0 + gr + 8 * h < a.n) x[h][i] = *reinterpret_cast<const uint4 *>(kt + (gr + 8 * h) * DH + t * (DH / 4) + i * 8);
-          kmax = fmaxf(kmax, amax8(x[h][i]));
         }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -326,6 +329,20 @@ __global__ void __launch_bounds__(128, 3)
           const int r = 2 * t + (q & 1) + 8 * (q >> 1);
           y[q][i] = make_uint4(0, 0, 0, 0);
           if (n0 + r < a.n) y[q][i] = *reinterpret_cast<const uint4 *>(vt + r * DH + gr * (DH / 8) + i * 8);
+        }
+      attended = __reduce_or_sync(0xffffffffu, attended);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) {
+          if (!((attended >> (gr + 8 * h)) & 1u)) x[h][i] = make_uint4(0, 0, 0, 0);
+          kmax = fmaxf(kmax, amax8(x[h][i]));
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < DH / 64; ++i) {
+          if (!((attended >> (2 * t + (q & 1) + 8 * (q >> 1))) & 1u)) y[q][i] = make_uint4(0, 0, 0, 0);
           vmax = fmaxf(vmax, amax8(y[q][i]));
         }
       uint32_t bits[2];
@@ -333,7 +350,7 @@ __global__ void __launch_bounds__(128, 3)
       for (int r = 0; r < 2; ++r) {
         bits[r] = 0;
         if (node[r] >= 0)
-          bits[r] = static_cast<uint32_t>(a.mask[(static_cast<int64_t>(b) * a.n + node[r]) * a.W + (n0 >> 6)] >> (n0 & 63)) & 0xffffu;
+          bits[r] = static_cast<uint32_t>(a.mask[static_cast<int64_t>(b) * a.n + node[r]] >> n0) & 0xffffu;
         if (n0 + 16 > a.n) bits[r] &= (1u << (a.n - n0)) - 1u;
       }
       const int ke = half_exponent(warp_max(kmax)), ve = half_exponent(warp_max(vmax));
