@@ -716,7 +716,9 @@ int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
  * exact down to 2^-25 of the largest magnitude M among its neighbours and off by
  * up to 2^-33 M below that; neighbours are the nodes of one block of 16 to 128
  * of a head (page_size decides) that any of up to 256 neighbouring query rows
- * names, so a large node costs rows bits that do not name it.
+ * names, so a large node costs rows bits that do not name it.  Scores are
+ * float32: where one passes 2^127, rows that name its key are undefined; scores
+ * of 0 are 0 whatever q and k are multiplied with.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};
  * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31;
  * n * Hq/Hkv <= 2^23.

@@ -616,10 +616,11 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
       if (unlikely(!prefix) && unlikely(!wait_bounded(&tile_full[SF + j % SF], (j / SF) & 1, abort_flag))) { ok = false; break; }
       const uint2 *sc = scales + (j % Sh::kScaleSlots) * GR;
       const bool dense = prefix && (p0 + jp + 1) * NK <= L;  // no key of the tile is masked
-      // never 0: it multiplies the -inf of masked keys
+      // never 0, since it multiplies the -inf of masked keys, nor infinite: a dot
+      // product of finite numbers may be 0
       const auto group = [&](int q) {  // (factor, ve)
         const uint2 gs = sc[q];
-        return make_float2(fmaxf(row_scale * __uint_as_float(gs.x & 0xffff0000u), 1.2e-38f), __uint_as_float(gs.y));
+        return make_float2(fminf(fmaxf(row_scale * __uint_as_float(gs.x & 0xffff0000u), 1.2e-38f), 1e38f), __uint_as_float(gs.y));
       };
       // Four groups' are kept for both passes; eight are read again (measured:
       // 70B 154 -> 152 us with four kept, GPT-OSS 734 -> 757 with eight).
