@@ -115,7 +115,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// True in one lane of a converged warp.
+// True in one lane of a converged warp, the same lane in every election among the
+// same lanes.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -799,9 +800,12 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
   if (*abort_flag) {
     if (tid == 0) report(a.status, EAGLE_ERR_TIMEOUT);
     volatile int never = 0;
-    if (warp == kMmaWarp && lane == 0) {
-      mma_commit(teardown);  // every MMA issued so far completes before tensor memory is released
-      mbar_wait(teardown, 0, &never, 100000000ull);
+    if (warp == kMmaWarp) {
+      __syncwarp();
+      if (elect_one()) {  // the thread that issued the MMAs (the election is the same each time): a commit covers its own
+        mma_commit(teardown);  // every MMA issued so far completes before tensor memory is released
+        mbar_wait(teardown, 0, &never, 100000000ull);
+      }
     }
     if (warp >= kProducerWarp && warp < kMmaWarp && lane == 0) {
       // copies still in flight complete before shared memory is released
