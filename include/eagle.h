@@ -88,7 +88,9 @@ int eagle_version(void);
  * nothing will ever complete and waits on it with the same helper the
  * kernels use, for `limit_ns` nanoseconds:
  *   which       0: the CTA-local wait; 1: the polling wait used for
- *               barriers that other CTAs of a cluster arrive on
+ *               barriers that other CTAs of a cluster arrive on; 3: the short
+ *               wait of eagle_tree_attn_kv8's roles; 4: the same when another
+ *               role has given up already, which ends it before the limit
  *   status      device int32 (required): EAGLE_ERR_TIMEOUT when the wait
  *               gave up as designed, EAGLE_ERR_INVALID if it returned as
  *               though the barrier had completed

@@ -674,7 +674,8 @@ def tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_
 
 def selftest_wait(limit_ns=1_000_000, which=0, stream=None):
     """Runs eagle_selftest_wait: one warp waits on an mbarrier that nothing
-    completes, with the kernels' own bounded-wait helper.  Returns (status
+    completes, with the kernels' own bounded-wait helper number `which` (0,
+    1, 3 or 4, see include/eagle.h).  Returns (status
     code written by the device, nanoseconds waited); the status is
     EAGLE_ERR_TIMEOUT (-5) when the wait gave up as designed."""
     lib = load_library()

@@ -89,6 +89,26 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
+// The same in few instructions, of a whole warp or of one elected thread, for a
+// kernel whose roles share the instruction cache: a wait written out in each place
+// costs more in fetches than in waiting.  Every lane polls, so the warp stays
+// together; a poll sleeps in the barrier, and the clock and the abort flag are
+// looked at on every sixteenth, so it gives up within about 2 ms of the limit.
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                             uint64_t limit_ns = 2000000000ull) {
+  uint64_t t0 = 0;
+  for (uint32_t polls = 1; !mbar_try_wait(bar, parity); ++polls) {
+    if (polls & 15u) continue;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort || now - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---- thread-block clusters -----------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

@@ -181,23 +181,6 @@ __device__ __forceinline__ void tmem_ld32x2(uint32_t taddr, float (&a)[32], floa
   }
 }
 
-// Bounded wait (two seconds of wall time) of a whole warp, or of one elected
-// thread, in few instructions: this kernel's roles share the instruction cache,
-// and a wait written out in each place costs more in fetches than in waiting.
-// Every lane polls, so the warp stays together.
-__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  uint64_t t0 = 0;
-  for (uint32_t polls = 1; !mbar_try_wait(bar, parity); ++polls) {
-    if (polls & 15u) continue;  // a poll sleeps in the barrier; the clock is looked at now and then
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (*abort || now - t0 > 2000000000ull) {
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
 __device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
 
 // MERGE: 0 the grid does not split the KV range; 1 the S splits of an item are
