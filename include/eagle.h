@@ -723,7 +723,7 @@ int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
  * of 0 are 0 whatever q and k are multiplied with.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};
  * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31;
- * n * Hq/Hkv <= 2^23.
+ * n * Hq/Hkv <= 2^23; workspace 16-byte aligned (else EAGLE_ERR_INVALID).
  * ------------------------------------------------------------------------ */
 size_t eagle_tree_attn_kv8_workspace_size(int dtype, int B, int n, int Hq,
                                           int Hkv, int dh, int max_pages,

@@ -65,3 +65,24 @@ def test_page_reserve_refusals():
     for change, code in changes:
         args = [change.get(i, a) for i, a in enumerate(good)]
         assert lib.eagle_page_reserve(*args) == code, change
+
+
+def test_tree_attn_kv8_refuses_a_workspace_off_its_boundary():
+    """Partial results are stored as float4s."""
+    from tree_speculative_decoding_eagle_gb300 import build
+    build.build()
+    lib = eg.load_library()
+    size = lib.eagle_tree_attn_kv8_workspace_size(1, 1, 61, 8, 8, 128, 64, 64)
+    assert size > 0
+    args = [FAKE] * 6 + [64, 64, 64] + [FAKE] * 4 + [1, 1, 61, 8, 8, 128, ctypes.c_float(0.1), FAKE, None, None,
+                                                    ctypes.c_void_p(0x1004), size, None]
+    assert lib.eagle_tree_attn_kv8(*args) == -1
+    args[-2] = size - 1
+    args[-3] = FAKE
+    assert lib.eagle_tree_attn_kv8(*args) == -4
+
+
+def test_a_cache_names_its_device_once():
+    from tree_speculative_decoding_eagle_gb300.cache import KV8Cache
+    cache = KV8Cache(1, 1, 64, 16, 2, 2, device="cpu")
+    assert cache._ws.device == cache.kv_len.device

@@ -44,3 +44,13 @@ def test_orthogonal_queries_and_keys(n, G, dh, P, q_exp, ke, kt_exp):
     # weights are one power of two and exact; the sums (whole numbers) too; 1 / l, the product and bf16 round
     assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() * (1 + 2.0 ** -8) + 2.0 ** -22).all()
     assert ((lse.double() - count.log().cuda()[None, :, None]).abs() <= 2.0 ** -21 * 6).all()
+
+
+def test_a_workspace_of_another_device_is_refused():
+    n, dh, P = 61, 128, 64
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")
+    pool, scale, table = z(64, 8, P, dh, dtype=torch.uint8), z(64, 8, dtype=torch.float32), z(1, 64, dtype=torch.int32)
+    args = (z(1, n, 8, dh), pool, pool, scale, scale, table, z(1, dtype=torch.int32), z(1, 8, n, dh), z(1, 8, n, dh),
+            z(1, n, 1, dtype=torch.int64))
+    with pytest.raises(eg.EagleError, match="workspace"):
+        eg.tree_attn_kv8(*args, workspace=eg.Workspace("cpu"))

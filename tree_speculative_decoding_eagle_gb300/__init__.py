@@ -661,6 +661,8 @@ def tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_
         raise EagleError("q must have the pages' head dimension")
     need = lib.eagle_tree_attn_kv8_workspace_size(code, B, n, Hq, Hkv, dh, max_pages, page_size)
     buf, nbytes = (workspace or Workspace(q.device)).get(need)
+    if buf is not None and buf.get_device() != dev:
+        raise EagleError(f"the workspace must be on device {dev}, not on {buf.device}")
     _call("eagle_tree_attn_kv8", lib.eagle_tree_attn_kv8, dev, None, _need(q, "q", dt, None, dev),
           *_pools(k_pages, v_pages, k_scale, v_scale, dev),
           _need(block_table, "block_table", torch.int32, (B, max_pages), dev), max_pages, page_size, num_pages,

@@ -62,7 +62,7 @@ class KV8Cache:
         # what the last reservation granted: no limit before the first
         self.granted = torch.full((B,), 2 ** 31 - 1, **i32)
         self._grown = torch.zeros(B, **i32)
-        self._ws = _KeptWorkspace(device)
+        self._ws = _KeptWorkspace(self.kv_len.device)      # not `device`: "cuda" is another one later
 
     def _pools(self, layer):
         return self.k_pages[layer], self.v_pages[layer], self.k_scale[layer], self.v_scale[layer]

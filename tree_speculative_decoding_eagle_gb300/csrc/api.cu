@@ -494,7 +494,7 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages, const uint8_t *v_
       !valid_query_rows(n, Hq, Hkv))
     return EAGLE_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_tree) || !aligned16(v_tree) ||
-      !aligned16(out))
+      !aligned16(out) || !aligned16(workspace))  // partial results are float4s
     return EAGLE_ERR_INVALID;
   const int sms = current_num_sms();
   const size_t need = attn_kv8_workspace_bytes(B, n, Hq, Hkv, dh, max_pages * page_size, sms);
