@@ -582,7 +582,8 @@ int eagle_page_release(const int32_t *keep_len, int B, int page_size,
  *   k_tree     dtype [B, Hkv, n, dh]  (out)
  *   v_tree     dtype [B, Hkv, n, dh]  (out: v in that layout)
  * Other outputs must not overlap the inputs.  Angles are reduced in 64-bit
- * fixed point (turns), so far positions lose nothing; cos, sin and the
+ * fixed point (turns): one is off by at most 2^-25 pi + position * inv_freq *
+ * 2^-52 radians (1e-7 up to positions of 2^27, 6e-7 at 2^31).  cos, sin and the
  * rotation are float32, rounded once to the output type.
  * Limits: n >= 1; B*n <= 2^24; Hq, Hkv >= 1; rot_dim even, 2 <= rot_dim <=
  * dh <= 512; dh*elemsize and ld*elemsize multiples of 16 bytes, tensors

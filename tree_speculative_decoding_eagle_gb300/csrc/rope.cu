@@ -2,10 +2,13 @@
 //
 // Pair j of a head at position p turns by the angle p * f_j.  The angle is
 // wanted modulo a turn for positions up to 2^31: f_j / 2pi is taken as a 64-bit
-// fixed-point fraction of a turn, and p * that, wrapping, is the reduced phase
-// exactly; its top 32 bits are the turns that sincospi gets (a float's 24 bits
-// of them: the angle is off by at most 2^-25 half turns, 1e-7).  No float64
-// arithmetic is done per position.
+// fixed-point fraction of a turn, and p * that, wrapping, reduces it without
+// another rounding; its top 32 bits are the turns that sincospi gets (a float's 24
+// bits of them).  The angle is off by at most 2^-25 half turns, 1e-7, and what the
+// rounding of f_j / 2pi in float64 grows to, p f_j 2^-52 (the product's half step
+// and the constant's): 5e-7 at 2^31.  That product and its fraction, a handful of
+// float64 operations, are done once a pair and CTA, the float64 reduction of p f_j
+// itself never.
 //
 // What bounds it: HBM (each element read once and written once), and latency
 // for one tree.  A CTA takes one node and a run of its heads; the node's cos and
