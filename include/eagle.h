@@ -604,13 +604,15 @@ int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B,
  *   EAGLE_ROPE_BANDS   by the turns t_j = orig_len f_j / 2pi that pair j makes
  *                      over the trained context: f_j / stretch at t_j <= low,
  *                      f_j at t_j >= high, linear in t_j between
- *   EAGLE_ROPE_YARN    the same ends at low and high turns, but linear in the
- *                      pair's index between, and *factor =
- *                      0.1 ln(stretch) + 1 (1 for the others)
+ *   EAGLE_ROPE_YARN    the same ends, as pair indexes rounded outwards to whole
+ *                      pairs, but linear in the pair's index between, and
+ *                      *factor = 0.1 ln(stretch) + 1 (1 for the others).  A
+ *                      model whose ramp keeps the ends unrounded (GPT-OSS's
+ *                      does) passes its own inv_freq to eagle_rope
  *   inv_freq  HOST double [rot_dim/2] (out);  factor  HOST float (out; may be
  *             NULL)
  * Limits: rot_dim even, >= 2; theta > 1; stretch >= 1; BANDS and YARN:
- * orig_len >= 1, 0 < low < high. */
+ * orig_len >= 1, 0 < low < high; all of them finite. */
 #define EAGLE_ROPE_PLAIN 0
 #define EAGLE_ROPE_LINEAR 1
 #define EAGLE_ROPE_BANDS 2

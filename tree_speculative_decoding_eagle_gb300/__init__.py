@@ -495,12 +495,15 @@ def page_release(keep_len, block_table, page_count, free_pages, free_count, page
           _need(free_count, "free_count", i32, (1,), dev), _maybe(status, "status", i32, None, dev))
 
 
-def rope_freqs(rot_dim, theta=10000.0, kind="plain", stretch=1.0, orig_len=4096, low=1.0, high=32.0, device=None):
+def rope_freqs(rot_dim, theta=10000.0, kind="plain", stretch=1.0, orig_len=4096, low=1.0, high=None, device=None):
     """Frequencies of rope() (eagle_rope_freqs): (inv_freq float64 [rot_dim/2]
     on `device`, factor).  kind: "plain", "linear", "bands" (stretched below
-    `low` turns over orig_len tokens, kept above `high`) or "yarn"."""
+    `low` turns over orig_len tokens, kept above `high`) or "yarn".  `high` is
+    4 for "bands" and 32 for "yarn" where it is not given."""
     if kind not in ROPE_KINDS:
         raise EagleError(f"unknown kind {kind!r}: one of {sorted(ROPE_KINDS)}")
+    if high is None:
+        high = 4.0 if kind == "bands" else 32.0
     out = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
     factor = ctypes.c_float()
     _check(load_library().eagle_rope_freqs(int(rot_dim), float(theta), ROPE_KINDS[kind], float(stretch),

@@ -3,6 +3,8 @@
 // throws, allocates or synchronises.
 #include <cuda_runtime.h>
 
+#include <limits>
+
 #include "common.cuh"
 
 namespace eagle {
@@ -406,9 +408,11 @@ int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B, in
 
 int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch, int orig_len, double low, double high,
                      double *inv_freq, float *factor) {
-  if (!inv_freq || rot_dim < 2 || rot_dim % 2 || !(theta > 1.0) || !(stretch >= 1.0)) return EAGLE_ERR_INVALID;
+  constexpr double kMax = std::numeric_limits<double>::max();  // no NaN, no infinity
+  if (!inv_freq || rot_dim < 2 || rot_dim % 2 || !(theta > 1.0 && theta <= kMax) || !(stretch >= 1.0 && stretch <= kMax))
+    return EAGLE_ERR_INVALID;
   if (kind < EAGLE_ROPE_PLAIN || kind > EAGLE_ROPE_YARN) return EAGLE_ERR_INVALID;
-  if (kind >= EAGLE_ROPE_BANDS && (orig_len < 1 || !(low > 0.0) || !(high > low))) return EAGLE_ERR_INVALID;
+  if (kind >= EAGLE_ROPE_BANDS && (orig_len < 1 || !(low > 0.0) || !(high > low && high <= kMax))) return EAGLE_ERR_INVALID;
   rope_freqs(rot_dim, theta, kind, stretch, orig_len, low, high, inv_freq, factor);
   return EAGLE_OK;
 }
