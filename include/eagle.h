@@ -583,7 +583,7 @@ int eagle_page_release(const int32_t *keep_len, int B, int page_size,
  *   v_tree     dtype [B, Hkv, n, dh]  (out: v in that layout)
  * Other outputs must not overlap the inputs.  Angles are reduced in 64-bit
  * fixed point (turns): one is off by at most 2^-25 pi + position * inv_freq *
- * 2^-52 radians (1e-7 up to positions of 2^27, 6e-7 at 2^31).  cos, sin and the
+ * 2^-52 radians (1.3e-7 up to positions of 2^27, 6e-7 at 2^31).  cos, sin and the
  * rotation are float32, rounded once to the output type.
  * Limits: n >= 1; B*n <= 2^24; Hq, Hkv >= 1; rot_dim even, 2 <= rot_dim <=
  * dh <= 512; dh*elemsize and ld*elemsize multiples of 16 bytes, tensors
@@ -721,7 +721,12 @@ int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
  * exact down to 2^-25 of the largest magnitude M among its neighbours and off by
  * up to 2^-33 M below that; neighbours are the nodes of one block of 16 to 128
  * of a head (page_size decides) that any of up to 256 neighbouring query rows
- * names, so a large node costs rows bits that do not name it.  Scores are
+ * names, so a large node costs rows bits that do not name it.  A weight p_k meets
+ * its value in f16, with the value's scale 2^e_k (a page's, or a tree block's
+ * power of two) joined to it: key k is off by up to |v_k| (2^-11 p_k + 2^-31
+ * 2^-e_k max_j(p_j 2^e_j)).  Where one row's value scales lie 2^20 and more apart,
+ * an outlier on one page thus costs the keys of the others bits, in every column.
+ * Scores are
  * float32: where one passes 2^127, rows that name its key are undefined; scores
  * of 0 are 0 whatever q and k are multiplied with.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};

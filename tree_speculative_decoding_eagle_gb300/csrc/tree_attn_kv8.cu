@@ -1,9 +1,11 @@
 // Stage 3 over the 8-bit paged cache: tree-masked attention whose prefix keys
 // and values are e4m3 numbers with a power-of-two scale for each page and head.
 //
-// The mathematics.  Everything runs in f16 on the tensor cores, and exactly: an
-// e4m3 number is an f16 number, and a bf16 row (queries, tree keys and values)
-// becomes f16 after division by a power of two of its own.  The powers of two
+// The mathematics.  Everything runs in f16 on the tensor cores.  An e4m3 number is
+// an f16 number.  A bf16 query row becomes f16 over a power of two of its own, tree
+// keys and values over one that a block of nodes shares (16, or a tile of 64 or 128
+// in the one-scale form); both put the largest magnitude M at 2^8 to 2^9, so what is
+// above 2^-25 M is exact and the rest off by up to 2^-33 M.  The powers of two
 // never touch the tiles; they go into the softmax's float32 arithmetic.  With
 // q = 2^a q', k = 2^ke k', v = 2^ve v' (ke, ve of a group of 16 keys, which no
 // page splits):
@@ -13,7 +15,9 @@
 //   lse = ln 2 (m - 6 + log2 l)
 // so P' stays below 2^14 and is rounded to 11 bits (bf16 would leave 8), down
 // to 2^-20 of the row's largest; smaller ones are off by up to 2^-31 of it
-// (f16's subnormals).  Neither K nor V is rounded at all.
+// (f16's subnormals).  ve is part of P': on a page whose value scale is 2^-20 of
+// another's, weights as large have those bits no more.  The cache's K and V are not
+// rounded at all.
 //
 // One CTA per (sequence b, KV head g, group of MT 128-row M-tiles, KV split);
 // query rows are (node, head-in-group) pairs, key tiles hold NK keys, first the
