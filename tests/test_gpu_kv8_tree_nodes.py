@@ -41,6 +41,21 @@ def test_nodes_that_no_row_names_decide_nothing(n, G, dh, P, what):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("n,G,dh,P", [(4096, 1, 64, 16), (2100, 2, 128, 64), (4096, 1, 128, 4096), (1300, 4, 64, 128)])
+def test_long_chains_with_padding_between(n, G, dh, P):
+    """A prompt chunk up to the largest, every eleventh node padding."""
+    keep = torch.ones((1, n, n)).tril().bool()
+    pad = torch.arange(n) % 11 == 5
+    keep[:, :, pad] = False
+    keep[:, pad] = False
+    c = Case([70], n, G, 1, dh, P, keep=keep)
+    args = list(c.args())
+    for i in (7, 8):
+        args[i] = args[i].clone()
+        args[i][:, :, pad.cuda()] = math.nan
+    c.check(*eg.tree_attn_kv8(*args))
+
+
 class Uneven(Case):
     """The tolerance with blocks of `block` nodes and what a large node costs the
     others: every element of k_tree and v_tree is off by up to 2^-33 of its
