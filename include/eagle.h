@@ -720,8 +720,9 @@ int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
  * nodes that some row names, must be finite.  An element of k_tree or v_tree is
  * exact down to 2^-25 of the largest magnitude M among its neighbours and off by
  * up to 2^-33 M below that; neighbours are the nodes of one block of 16 to 128
- * of a head (page_size decides) that any of up to 256 neighbouring query rows
- * names, so a large node costs rows bits that do not name it.  A weight p_k meets
+ * of a head (page_size decides) that any row names (with more than 64 nodes: any
+ * of up to 256 neighbouring query rows), so a large node costs rows bits that do
+ * not name it.  A weight p_k meets
  * its value in f16, with the value's scale 2^e_k (a page's, or a tree block's
  * power of two) joined to it: key k is off by up to |v_k| (2^-11 p_k + 2^-31
  * 2^-e_k max_j(p_j 2^e_j)).  Where one row's value scales lie 2^20 and more apart,

@@ -37,10 +37,11 @@
 // the one-scale form) they waited in 360; tensor pipe 32 %, ex2 33 %, issue slots
 // 57 % of active cycles; HBM 12 %.  With few rows, each CTA's chain (length -
 // page number - bytes - f16 - S - P - O) through the warps.  Measured (the same
-// call on a 16-bit cache): 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 148 us
-// (184; 714 TFLOP/s, 37 % of cuBLAS's bf16 rate); 64 x 61 nodes, 64 heads on 8 of
-// 64, 8192 keys 684 us (688; 766 TFLOP/s, 40 %); 61 nodes, 32 heads of 128, 2048
-// keys 21.6 us (17.8); 8 x 51 nodes, 40 heads of 128, 1024 to 4096 keys 131 us (142).
+// call on a 16-bit cache): 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 150 us
+// (184; 704 TFLOP/s, 37 % of cuBLAS's bf16 rate); 64 x 61 nodes, 64 heads on 8 of
+// 64, 8192 keys 690 us (688; 760 TFLOP/s, 40 %); 61 nodes, 32 heads of 128, 2048
+// keys 22.0 us (17.8); 8 x 51 nodes, 40 heads of 128, 1024 to 4096 keys 127 us (125);
+// a chain of 1024 nodes, 64 heads on 8 of 128, after 4096 keys 226 us.
 // Two M-tiles a CTA (one converter warpgroup, which then takes K and V in turn)
 // from 129 rows on, since a tile's conversion is shared by its M-tiles; two CTAs an
 // SM up to 64 rows, where latency counts.
@@ -59,7 +60,7 @@ using namespace sm100;
 // ONE: every key tile has one scale (pages no shorter than a tile; the tree's
 // nodes then share a tile's power of two), so the softmax does nothing group by
 // group.  Measured with it / without: 64 x 61 nodes, 64 heads on 8 of 64, 8192
-// keys 684 / 731 us; 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 148 / 152 us.  A
+// keys 690 / 737 us; 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 150 / 157 us.  A
 // choice made per tile in one kernel costs more than it gains (registers spill).
 template <int DH, int MT, int NK, int SF, int S8, int QR, int OCC, bool ONE>
 struct Kv8Shape {
@@ -74,7 +75,7 @@ struct Kv8Shape {
   static constexpr int kBarOff = kStagingOff + S8 * 2 * kByteTile;
   static constexpr int kGroups = NK / 16;
   static constexpr int kNumBars = 4 * S8 + 4 * SF + 4 * MT + 2 + (ONE ? 2 : 0);
-  static constexpr int kNamedWords = QR == 64 ? 1 : 64;   // mask words of n nodes (64 rows: 64 nodes at most)
+  static constexpr int kNamedWords = MT == 1 ? QR / 64 : 64;   // mask words of n nodes (no more nodes than rows)
   // barriers, tensor-memory slot and abort flag, scales of the tiles' groups, the
   // nodes that the CTA's rows name, exponents of the query rows
   static constexpr int kScaleSlots = S8 + SF + 3;         // tiles between K's producer and the softmax
@@ -251,8 +252,10 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (tid >= 64 && tid < 64 + 2 * Sh::kNamedWords) reinterpret_cast<uint32_t *>(named)[tid - 64] = 0;
-  __syncthreads();
+  if (MT > 1 && a.W > 1) {
+    if (tid >= 64 && tid < 64 + 2 * Sh::kNamedWords) reinterpret_cast<uint32_t *>(named)[tid - 64] = 0;
+    __syncthreads();
+  }
   pdl_wait();  // inputs of this step come from earlier kernels
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, Sh::kTmemCols);
@@ -260,12 +263,24 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
   }
   const int kv_len = a.kv_len[b];
   const int rows_total = n * a.G;
-  if (split == a.S - 1) {
-    // The nodes that any of the CTA's rows names: their mask words or'ed, so that
-    // padding decides no block's power of two.  Threads are words, and rows where
-    // there are fewer words.  Here, while kv_len is on its way, since a role's code
-    // pays for every register: in a warp of its own 70B takes 188 us, in the
-    // converters 160, here 152 (148 without).
+  // The nodes that any of the CTA's rows names: their mask words or'ed, so that
+  // padding decides no block's power of two.  Here, while kv_len is on its way, since
+  // a role's code pays for every register: in a warp's role of its own 70B takes 188
+  // us, in the converters 160, here 150 (148 without).
+  if (MT == 1 || a.W == 1) {  // at most 128 nodes (one M-tile), or 64: one warp, every row
+    if (split == a.S - 1 && warp == kMmaWarp + 1) {
+      const uint64_t *words = a.mask + static_cast<int64_t>(b) * n * a.W;
+      for (int w = 0; w < a.W; ++w) {
+        uint64_t any = 0;
+#pragma unroll
+        for (int u = 0; u < (MT == 1 ? QR : 64) / 32; ++u)
+          if (lane + 32 * u < n) any |= words[(lane + 32 * u) * a.W + w];
+        const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+        const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32));
+        if (lane == 0) reinterpret_cast<uint2 *>(named)[w] = make_uint2(lo, hi);
+      }
+    }
+  } else if (split == a.S - 1) {  // threads are words, and rows where there are fewer words
     const uint64_t *words = a.mask + static_cast<int64_t>(b) * n * a.W;
     const int i1 = (min(rows_total, (mg + 1) * MT * 128) - 1) / a.G;
     const int wl = a.W > 16 ? 32 : a.W > 8 ? 16 : a.W > 4 ? 8 : a.W > 2 ? 4 : a.W;  // words side by side
