@@ -531,8 +531,8 @@ int eagle_page_map(const int32_t *kv_len, const int32_t *new_len, int B,
  * would write through slots that may belong to another request by then.  Here
  * a refusal is written out: slot_map becomes -1 throughout (the append skips
  * such tokens), new_start 0, and
- *   granted      device int32 [B] (out): new_len, or 0 for every request of a
- *                refused map: what the requests' lengths may grow by
+ *   granted      device int32 [1] (out): 1, or 0 when the map is refused, so
+ *                that kv_len + granted * new_len are the lengths after it
  * Everything else is as eagle_page_map leaves it, status included. */
 int eagle_page_reserve(const int32_t *kv_len, const int32_t *new_len, int B,
                        int page_size, int max_pages, int num_pages,

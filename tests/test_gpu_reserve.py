@@ -47,16 +47,16 @@ def test_a_refusal_is_written_out(B, T, why, code):
         room = T - 1
     t, c, f, n = i32(table), i32(count), i32(free), i32([fc])
     slots, starts = torch.full((room,), 77, dtype=torch.int32, device="cuda"), torch.full((B + 1,), 77, dtype=torch.int32, device="cuda")
-    granted, status = torch.full((B,), 77, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    granted, status = torch.full((1,), 77, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     eg.page_map(i32(kv), i32(new), t, c, f, n, page, slot_map=slots, new_start=starts, status=status, granted=granted)
     assert int(status) == code
     if code:
-        assert (slots == -1).all() and not starts.any() and not granted.any()
+        assert (slots == -1).all() and not starts.any() and granted.item() == 0
         assert t.tolist() == table.tolist() and c.tolist() == count.tolist() and n.item() == fc
     else:
         err, t_o, c_o, fc_o, slots_o, starts_o = opages.page_map(kv.tolist(), new.tolist(), table.tolist(), count.tolist(),
                                                                  free.tolist(), fc, page, N, T=room)
-        assert err is None and granted.tolist() == new.tolist()
+        assert err is None and granted.item() == 1
         assert slots.tolist() == slots_o and starts.tolist() == starts_o and t.tolist() == t_o and n.item() == fc_o
     assert f.tolist() == free.tolist()
 
@@ -99,9 +99,9 @@ def test_a_captured_loop_runs_out_of_pages_and_recovers():
     assert float(c.k_pages[0][page0, 0, 0, 0].float() * c.k_scale[0][page0, 0]) == 384.0
 
 
-def test_grow_takes_numbers_and_tensors_and_stops_at_the_grant():
+def test_grow_takes_numbers_and_tensors_and_counts_nothing_after_a_refusal():
     c = KV8Cache(2, 1, 64, 16, 2, 8)
-    c.grow(3)                                          # before any reservation nothing limits it
+    c.grow(3)                                          # before any reservation: as it is told
     assert c.kv_len.tolist() == [3, 3]
     c.kv_len.zero_()
     c.reserve(i32([5, 20]))                            # three pages of two
@@ -112,3 +112,9 @@ def test_grow_takes_numbers_and_tensors_and_stops_at_the_grant():
     c.grow(4)
     c.grow(torch.tensor([1, 12], device="cuda"))
     assert int(c.status) == 0 and c.kv_len.tolist() == [5, 16]
+    c.reserve(i32([3, 0]))                             # two reservations, then what both were for
+    c.reserve(i32([0, 0]))
+    c.grow(i32([3, 0]))
+    assert int(c.status) == 0 and c.kv_len.tolist() == [8, 16]
+    c.grow(-2)
+    assert c.kv_len.tolist() == [6, 14]

@@ -462,15 +462,15 @@ def page_map(kv_len, new_len, block_table, page_count, free_pages, free_count, p
     int32 [T] (optional) receives the slots of the new tokens, request by
     request, then -1; new_start int32 [B+1] (optional) their first indices.
     Returns slot_map.  Too few free pages leave everything as it was and set
-    `status` to -6; with `granted` int32 [B] (eagle_page_reserve) slot_map is
-    then -1 throughout, and granted 0 instead of new_len."""
+    `status` to -6; with `granted` int32 [1] (eagle_page_reserve) slot_map is
+    then -1 throughout, and granted 0 instead of 1."""
     lib = load_library()
     dev, i32 = _device_of(kv_len, "kv_len"), torch.int32
     B, max_pages = block_table.shape
     num_pages = free_pages.shape[0]
     name, more = "eagle_page_map", ()
     if granted is not None:
-        name, more = "eagle_page_reserve", (_need(granted, "granted", i32, (B,), dev),)
+        name, more = "eagle_page_reserve", (_need(granted, "granted", i32, (1,), dev),)
     _call(name, getattr(lib, name), dev, stream, _need(kv_len, "kv_len", i32, (B,), dev),
           _need(new_len, "new_len", i32, (B,), dev), B, page_size, max_pages, num_pages,
           _need(block_table, "block_table", i32, None, dev), _need(page_count, "page_count", i32, (B,), dev),

@@ -59,9 +59,7 @@ class KV8Cache:
         self.kv_len = torch.zeros(B, **i32)
         self.status = torch.zeros(1, **i32)
         self._len = torch.zeros(B, **i32)      # the lengths that all layers but the last commit to
-        # what the last reservation granted: no limit before the first
-        self.granted = torch.full((B,), 2 ** 31 - 1, **i32)
-        self._grown = torch.zeros(B, **i32)
+        self.granted = torch.ones(1, **i32)    # whether the last reservation was served
         self._ws = _KeptWorkspace(self.kv_len.device)      # not `device`: "cuda" is another one later
 
     def _pools(self, layer):
@@ -80,13 +78,12 @@ class KV8Cache:
         kv8_append(k, v, slot_map, *self._pools(layer), status=self.status)
 
     def grow(self, new_len):
-        """new_len [B] tokens have been appended, no more than the last
-        reservation granted."""
+        """new_len [B] (or one number) tokens have been appended; counts nothing
+        where the last reservation was refused, since append() wrote none."""
         if torch.is_tensor(new_len):
-            torch.minimum(self.granted, new_len, out=self._grown)
+            self.kv_len.addcmul_(self.granted, new_len.to(torch.int32))
         else:
-            torch.clamp(self.granted, max=new_len, out=self._grown)
-        self.kv_len.add_(self._grown)
+            torch.add(self.kv_len, self.granted, alpha=new_len, out=self.kv_len)
 
     def attend(self, layer, q, k_tree, v_tree, mask, scale=None, out=None, lse=None, workspace=None):
         return tree_attn_kv8(q, *self._pools(layer), self.block_table, self.kv_len, k_tree, v_tree, mask, scale=scale,

@@ -144,10 +144,9 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(PageArgs a) {
     if (rank == 0 && tid == 0) report(a.status, err);
     if (a.granted) {  // nothing granted: no slot, no token
       for (int t = rank * kPageThreads + tid; t < a.T; t += ctas * kPageThreads) a.slot_map[t] = -1;
-      for (int b = rank * kPageThreads + tid; b <= a.B; b += ctas * kPageThreads) {
-        if (b < a.B) a.granted[b] = 0;
-        if (a.new_start) a.new_start[b] = 0;
-      }
+      if (a.new_start)
+        for (int b = rank * kPageThreads + tid; b <= a.B; b += ctas * kPageThreads) a.new_start[b] = 0;
+      if (rank == 0 && tid == 0) *a.granted = 0;
     }
     return;
   }
@@ -163,11 +162,11 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(PageArgs a) {
     const int add = s.first[b + 1] - s.first[b];
     if (add) a.page_count[b] = s.count[b] + add;
     if (a.new_start) a.new_start[b] = s.start[b];
-    if (a.granted) a.granted[b] = s.start[b + 1] - s.start[b];
   }
   if (rank == 0 && tid == 0) {
     if (pages) *a.free_count = fc - static_cast<int>(pages);
     if (a.new_start) a.new_start[a.B] = static_cast<int32_t>(tokens);
+    if (a.granted) *a.granted = 1;
   }
   // slots: a thread takes four neighbouring tokens, finds the first one's
   // request by bisection and walks on from there
