@@ -12,9 +12,8 @@
 // number of tokens); every CTA reads all lengths and makes the sums itself in
 // shared memory (12 bytes a request, from L2 after the first), which
 // costs less than handing them over, and then writes its share of the outputs.
-// Measured, a map and a release together (two launches in a graph): 6.8 us for
-// one request, 11.5 us for 512 requests with up to 32768 new tokens (0.3 us of
-// it for looking at every page number before a release writes the first), whose 0.2
+// Measured, a map and a release together (two launches in a graph): 6.7 us for
+// one request, 11.6 us for 512 requests with up to 32768 new tokens, whose 0.2
 // MB would stream in 0.03 us: the chain is two launches, the lengths, two sums,
 // a bisection and the free list's entries.
 // Everything that is updated in place (page_count, free_count) is written only
@@ -193,6 +192,51 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(PageArgs a) {
   if (lost) report(a.status, EAGLE_ERR_INVALID);
 }
 
+// R pages to the free list, U a thread at a time.  Every page number is looked at
+// before the first is handed on; a thread's first U stay in registers meanwhile.
+// False (and nothing written) where one is no page; the same in every thread.
+template <int U>
+__device__ __forceinline__ bool give_back(const PageArgs &a, const PageSmem &s, int fc, int R) {
+  const int tid = threadIdx.x;
+  const auto entry_of = [&](int j) {
+    const int b = owner_of(s.first, a.B, j);
+    return a.block_table + static_cast<int64_t>(b) * a.max_pages + s.kv[b] + (j - s.first[b]);
+  };
+  int32_t *entry[U];
+  int page[U];
+  bool lost = false;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int j = tid + u * kPageThreads;
+    entry[u] = j < R ? entry_of(j) : nullptr;
+    page[u] = entry[u] ? *entry[u] : 0;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) lost |= page[u] < 0 || page[u] >= a.num_pages;
+  if (U > 1)
+    for (int j = tid + U * kPageThreads; j < R; j += kPageThreads) {
+      const int p = *entry_of(j);
+      lost |= p < 0 || p >= a.num_pages;
+    }
+  if (__syncthreads_or(lost)) {
+    if (tid == 0) report(a.status, EAGLE_ERR_INVALID);
+    return false;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (entry[u]) {
+      a.free_pages[fc + R - 1 - (tid + u * kPageThreads)] = page[u];
+      *entry[u] = -1;
+    }
+  if (U > 1)
+    for (int j = tid + U * kPageThreads; j < R; j += kPageThreads) {
+      int32_t *e = entry_of(j);
+      a.free_pages[fc + R - 1 - j] = *e;
+      *e = -1;
+    }
+  return true;
+}
+
 // Gives pages back.  One CTA: a step returns a handful, and the largest
 // release is one word read and two written a page.
 __global__ void __launch_bounds__(kPageThreads) page_release_kernel(PageArgs a) {
@@ -234,43 +278,8 @@ __global__ void __launch_bounds__(kPageThreads) page_release_kernel(PageArgs a) 
     return;
   }
   const int R = static_cast<int>(pages);
-  const auto entry_of = [&](int j) {
-    const int b = owner_of(s.first, a.B, j);
-    return a.block_table + static_cast<int64_t>(b) * a.max_pages + s.kv[b] + (j - s.first[b]);
-  };
-  // every page number is looked at before the first is handed on; a thread's
-  // first kHeldPages stay in registers meanwhile
-  constexpr int kHeldPages = 4;
-  int32_t *entry[kHeldPages];
-  int page[kHeldPages];
-  bool lost = false;  // a number that is no page
-#pragma unroll
-  for (int u = 0; u < kHeldPages; ++u) {
-    const int j = tid + u * kPageThreads;
-    entry[u] = j < R ? entry_of(j) : nullptr;
-    page[u] = entry[u] ? *entry[u] : 0;
-  }
-#pragma unroll
-  for (int u = 0; u < kHeldPages; ++u) lost |= page[u] < 0 || page[u] >= a.num_pages;
-  for (int j = tid + kHeldPages * kPageThreads; j < R; j += kPageThreads) {
-    const int p = *entry_of(j);
-    lost |= p < 0 || p >= a.num_pages;
-  }
-  if (__syncthreads_or(lost)) {
-    if (tid == 0) report(a.status, EAGLE_ERR_INVALID);
-    return;
-  }
-#pragma unroll
-  for (int u = 0; u < kHeldPages; ++u)
-    if (entry[u]) {
-      a.free_pages[fc + R - 1 - (tid + u * kPageThreads)] = page[u];
-      *entry[u] = -1;
-    }
-  for (int j = tid + kHeldPages * kPageThreads; j < R; j += kPageThreads) {
-    int32_t *e = entry_of(j);
-    a.free_pages[fc + R - 1 - j] = *e;
-    *e = -1;
-  }
+  // a step's release in few instructions: they come from memory too (6.7 us against 7.1 with a map)
+  if (!(R <= kPageThreads ? give_back<1>(a, s, fc, R) : give_back<4>(a, s, fc, R))) return;
   for (int b = tid; b < a.B; b += kPageThreads)
     if (s.count[b] != s.kv[b]) a.page_count[b] = s.kv[b];
   if (tid == 0 && R) *a.free_count = fc + R;
