@@ -12,9 +12,9 @@
 //
 // What bounds it: HBM for prompts (2 or 4 bytes read, 1 written an element),
 // latency for single tokens and commits.  Measured: 65536 tokens of 8 heads of
-// 128, bf16, pages of 64: 77.4 us (5.2 TB/s, 78 % of a copy's rate; 403 MB; 76.5
+// 128, bf16, pages of 64: 77.6 us (5.2 TB/s, 78 % of a copy's rate; 403 MB; 76.8
 // without the look for an interrupted page); one token of each of 64 requests, 8
-// heads of 64: 4.4 us (4.2); the accepted paths of 8 trees, 40 heads of 128: 7.5
+// heads of 64: 4.3 us (4.2); the accepted paths of 8 trees, 40 heads of 128: 7.9
 // us with a copy of kv_len before it.
 #include "kv8.cuh"
 #include "sm100.cuh"
@@ -201,7 +201,8 @@ struct AppendArgs {
 // fastest, so that CTAs that run together read neighbouring heads of the same
 // tokens.  A team finds its runs once for all of its pairs: finding one costs
 // about what rounding a page of one head does (measured on 65536 tokens of 8
-// heads of 128, pages of 64: 101 us with one pair a CTA, 84 with two, 76 with four, 80 with eight).
+// heads of 128, pages of 64: 101 us with one pair a CTA, 84 with two, 76 with four, 80 with eight, before the look for
+// interrupted pages).
 template <typename T>
 __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 3 : 2) kv8_append_kernel(AppendArgs a) {
   __shared__ float red[kWriteWarps];

@@ -14,8 +14,8 @@
 // for one tree.  A CTA takes one node and a run of its heads; the node's cos and
 // sin are computed once per CTA into shared memory, while the heads' 16-byte
 // vectors are on their way.  Measured: 8191 nodes of 120 heads of 128 in f32
-// 174 us (5.8 TB/s, 86 % of a copy's rate); 3904 nodes of 80 heads of 64 in
-// bf16 16.5 us (4.8 TB/s, 72 %); 61 nodes of 96 heads of 128 3.4 us.
+// 175 us (5.8 TB/s, 86 % of a copy's rate); 3904 nodes of 80 heads of 64 in
+// bf16 16.9 us (4.7 TB/s, 71 %); 61 nodes of 96 heads of 128 3.3 us.
 #include <math.h>
 
 #include "common.cuh"

@@ -34,13 +34,13 @@
 //
 // What bounds it.  With grouped heads, the softmax warps: of 3300 cycles that a
 // 128-key tile of two M-tiles took at dh 64 (a trace of each role's waits, before
-// the one-scale form) they waited in 360; tensor pipe 32 %, ex2 33 %, issue slots
-// 57 % of active cycles; HBM 12 %.  With few rows, each CTA's chain (length -
+// the one-scale form) they waited in 360; in the one-scale form tensor pipe 34 %,
+// ex2 35 %, issue slots 54 % of active cycles, HBM 9 %.  With few rows, each CTA's chain (length -
 // page number - bytes - f16 - S - P - O) through the warps.  Measured (the same
 // call on a 16-bit cache): 16 x 49 nodes, 64 heads on 8 of 128, 4096 keys 150 us
-// (184; 704 TFLOP/s, 37 % of cuBLAS's bf16 rate); 64 x 61 nodes, 64 heads on 8 of
+// (184; 702 TFLOP/s, 37 % of cuBLAS's bf16 rate); 64 x 61 nodes, 64 heads on 8 of
 // 64, 8192 keys 690 us (688; 760 TFLOP/s, 40 %); 61 nodes, 32 heads of 128, 2048
-// keys 22.0 us (17.8); 8 x 51 nodes, 40 heads of 128, 1024 to 4096 keys 127 us (125);
+// keys 22.1 us (17.8); 8 x 51 nodes, 40 heads of 128, 1024 to 4096 keys 127 us (125);
 // a chain of 1024 nodes, 64 heads on 8 of 128, after 4096 keys 226 us.
 // Two M-tiles a CTA (one converter warpgroup, which then takes K and V in turn)
 // from 129 rows on, since a tile's conversion is shared by its M-tiles; two CTAs an
@@ -878,9 +878,11 @@ cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void 
 
 // Query rows of a KV head up to which the few-row kernel runs: its warp-level
 // MMAs cost a row tile of 16 what the bytes cost at two tiles.  Measured (us,
-// few-row kernel / this one): 30 rows, dh 128, 320 heads of U[1024, 4096] keys
-// 149 / 170; 20 rows, dh 64, 64 such heads 27 / 34; 51 rows, dh 128, 320 heads
-// 208 / 166; 56 rows, dh 64, 256 heads of 4096 keys 145 / 88.
+// few-row kernel / this one): 20 rows, dh 64, 64 heads of U[1024, 4096] keys 25.1 /
+// 25.6; 30 rows, dh 128, 320 such heads 138 / 112 (149 / 170 when the bound was set:
+// at dh 128 with many heads it now belongs between 16 and 32).  With more row tiles
+// the few-row kernel took 208 us at 51 rows, dh 128, 320 heads, against 127, and 145
+// at 56 rows, dh 64, 256 heads of 4096 keys, against 94.
 constexpr int kFewRows = 32;
 
 struct Kv8Plan {

@@ -17,8 +17,8 @@
 //   * the running maximum is looked at across a quad only when a lane's own
 //     exceeds it by more than 2^8.
 // Measured: 64 single tokens, 64 heads on 8, dh 128, 1024 to 8192 keys: 122 us
-// (607 MB, 5.0 TB/s, 74 % of a copy's rate; 81 % at 8192 keys each, 90 % at
-// 16384), against 238 us for the 16-bit cache; what is lost is each CTA's chain
+// (607 MB, 5.0 TB/s, 74 % of a copy's rate; 84 % at 8192 keys each, 93 % at
+// 16384), against 237 us for the 16-bit cache; what is lost is each CTA's chain
 // length - page number - bytes, and the last CTAs of the grid.
 // A CTA of four warps is KG = 4 / RG groups of keys times RG = 1 or 2 tiles of 16
 // rows; the RG warps of a key group share its ring.  Three CTAs an SM keep up
