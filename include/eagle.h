@@ -726,7 +726,9 @@ int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
  * its value in f16, with the value's scale 2^e_k (a page's, or a tree block's
  * power of two) joined to it: key k is off by up to |v_k| (2^-11 p_k + 2^-31
  * 2^-e_k max_j(p_j 2^e_j)).  Where one row's value scales lie 2^20 and more apart,
- * an outlier on one page thus costs the keys of the others bits, in every column.
+ * an outlier on one page thus costs the keys of the others bits, in every column;
+ * up to 2^100 apart they keep their weight in the sum (below 2^-32 of it is lost),
+ * further apart out and lse may leave them out.
  * Scores are
  * float32: where one passes 2^127, rows that name its key are undefined; scores
  * of 0 are 0 whatever q and k are multiplied with.
