@@ -717,21 +717,23 @@ int eagle_kv8_commit_root(const void *k_tree, const void *v_tree, int dtype,
  * -inf; a row that attends to a NaN of the cache gives NaN.  Rows of a page at
  * or beyond kv_len may be read but never count, whatever they hold; nor do
  * tree nodes that no row of the mask names.  q, and k_tree and v_tree of the
- * nodes that some row names, must be finite.  An element of k_tree or v_tree is
- * exact down to 2^-25 of the largest magnitude M among its neighbours and off by
- * up to 2^-33 M below that; neighbours are the nodes of one block of 16 to 128
- * of a head (page_size decides) that any row names (with more than 64 nodes: any
- * of up to 256 neighbouring query rows), so a large node costs rows bits that do
- * not name it.  A weight p_k meets
- * its value in f16, with the value's scale 2^e_k (a page's, or a tree block's
- * power of two) joined to it: key k is off by up to |v_k| (2^-11 p_k + 2^-31
- * 2^-e_k max_j(p_j 2^e_j)).  Where one row's value scales lie 2^20 and more apart,
- * an outlier on one page thus costs the keys of the others bits, in every column;
- * up to 2^100 apart they keep their weight in the sum (below 2^-32 of it is lost),
- * further apart out and lse may leave them out.
- * Scores are
- * float32: where one passes 2^127, rows that name its key are undefined; scores
- * of 0 are 0 whatever q and k are multiplied with.
+ * nodes that some row names, must be finite.
+ * What is rounded beside the output:
+ *   - An element of k_tree or v_tree is exact down to 2^-25 of the largest
+ *     magnitude M among its neighbours and off by up to 2^-33 M below that.
+ *     Neighbours are the nodes of one block of 16 to 128 of a head (page_size
+ *     decides) that any row names (with more than 64 nodes: any of up to 256
+ *     neighbouring query rows), so a large node costs rows bits that do not
+ *     name it.
+ *   - A weight p_k meets its value in f16, with the value's scale 2^e_k (a
+ *     page's, or a tree block's power of two) joined to it: key k is off by up
+ *     to |v_k| (2^-11 p_k + 2^-31 2^-e_k max_j(p_j 2^e_j)).  Where one row's
+ *     value scales lie 2^20 and more apart, an outlier on one page thus costs
+ *     the keys of the others bits, in every column; up to 2^100 apart they
+ *     keep their weight in the sum (below 2^-32 of it is lost), further apart
+ *     out and lse may leave them out.
+ *   - Scores are float32: where one passes 2^127, rows that name its key are
+ *     undefined; scores of 0 are 0 whatever q and k are multiplied with.
  * Limits: dtype EAGLE_BF16 (else EAGLE_ERR_UNSUPPORTED); dh in {64, 128};
  * scale > 0; page rules as for eagle_tree_attn_paged; num_pages*Hkv < 2^31;
  * n * Hq/Hkv <= 2^23; workspace 16-byte aligned (else EAGLE_ERR_INVALID).

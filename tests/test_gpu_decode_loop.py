@@ -50,8 +50,9 @@ class Model:
         t = torch.as_tensor(tok).long()
         return (x[layer][t].to(bf).cuda() for x in (self.q, self.k, self.v))
 
-    def check(self, out, layer, seq, tok, parent):
-        """Every node's row against causal attention over seq and its ancestors."""
+    def check(self, out, layer, seq, tok, parent, weights=2.0 ** -11, half=2.0 ** -8):
+        """Every node's row against causal attention over seq and its ancestors;
+        `weights`, `half`: half a step of the types that weights and outputs are rounded to."""
         n, L = len(tok), len(seq)
         live = np.zeros((n, n), bool)
         depth = np.zeros(n, int)
@@ -73,7 +74,7 @@ class Model:
             p /= p.sum(1, keepdims=True)
             ref, A = p @ val, p @ np.abs(val)
             w = 2 * (dh * 2.0 ** -23 * smax + 2.0 ** -21) + 2 * (L + n) * 2.0 ** -24
-            tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -8) + (2.0 ** -11 + w) * A + (L + n) * 2.0 ** -25
+            tol = half * np.abs(ref) * (1 + half) + (weights + w) * A + (L + n) * 2.0 ** -25
             assert (np.abs(out[:, h] - ref) <= tol).all(), (layer, L, float((np.abs(out[:, h] - ref) / tol).max()))
 
 
@@ -258,3 +259,42 @@ def test_the_loop_in_a_graph():
             assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(getattr(a, name), getattr(b, name)))
         assert all(torch.equal(s, t) for s, t in zip(a.k_scale + a.v_scale, b.k_scale + b.v_scale))
     assert int(caches[0].status) == 0 and caches[0].kv_len.tolist() == [30, 10]
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_the_16_bit_loop_follows_the_same_rule(paged):
+    """eagle_tree_attn(_paged) with the positions before the root; the caller
+    stores the root's row; eagle_kv_commit with one position more."""
+    B, n, Lmax = 2, 6, 64
+    model, g = Model(11), torch.Generator().manual_seed(11)
+    dtype = bf if paged else torch.float32
+    parent = [-1, 0, 0, 1, 3, 2]
+    path = i32([[0, 1, 3, 4]] * B)
+    mask, depth = eg.tree_mask(i32([parent] * B)), i32([[0, 1, 1, 2, 3, 2]] * B)
+    freqs = torch.from_numpy(FREQS).cuda()
+    shape = (B * Lmax // P, Hkv, P, dh) if paged else (B, Hkv, Lmax, dh)
+    kc, vc = (torch.full(shape, 7.0, dtype=dtype, device="cuda") for _ in range(2))
+    table = torch.randperm(B * Lmax // P, generator=g).view(B, -1).int().cuda() if paged else None
+    seqs, kv_len = [[], []], torch.zeros(B, dtype=torch.int32, device="cuda")
+    for step in range(7):
+        tok = torch.randint(0, V, (B, n), generator=g)
+        q, kk, v = (t.to(dtype) for t in model.qkv(0, tok))
+        q, kt, vt = eg.rope(q, kk, v, freqs, pos_base=kv_len, pos_off=depth)
+        if paged:
+            out, _ = eg.tree_attn_paged(q, kc, vc, table, kv_len, kt, vt, mask)
+        else:
+            out, _ = eg.tree_attn(q, kc, vc, kv_len, kt, vt, mask)
+        acc = [step % 4, (step + 2) % 4]
+        for b in range(B):
+            model.check(f64(out[b]), 0, seqs[b], tok[b].tolist(), parent, weights=2.0 ** -8 if paged else 0.0, half=2.0 ** -8 if paged else 2.0 ** -24)
+            at = int(kv_len[b])
+            for c, t in ((kc, kt), (vc, vt)):
+                if paged:
+                    c[int(table[b, at // P]), :, at % P] = t[b, :, 0]
+                else:
+                    c[b, :, at] = t[b, :, 0]
+            seqs[b] += [int(tok[b, i]) for i in [0, 1, 3, 4][:acc[b] + 1]]
+        kv_len += 1
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        eg.kv_commit(kt, vt, i32(acc), path, kc, vc, kv_len, block_table=table, status=status)
+        assert int(status) == 0 and kv_len.tolist() == [len(s) for s in seqs]

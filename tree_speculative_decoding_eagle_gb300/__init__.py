@@ -583,8 +583,8 @@ def _pools(k_pages, v_pages, k_scale, v_scale, device):
 
 def kv8_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, status=None, stream=None):
     """Writes tokens' keys and values (k, v [T, Hkv, dh], any token and head
-    strides but those of a broadcast, the same for both) to the slots slot_map int32 [T] of the 8-bit
-    cache (eagle_kv8_append): k_pages, v_pages float8_e4m3fn [num_pages, Hkv,
+    strides but those of a broadcast, the same for both) to the slots slot_map
+    int32 [T] of the 8-bit cache (eagle_kv8_append): k_pages, v_pages float8_e4m3fn [num_pages, Hkv,
     page_size, dh], k_scale, v_scale float32 [num_pages, Hkv]."""
     lib = load_library()
     dev, shape, stride = _device_of(k, "k"), k.shape, k.stride()
