@@ -14,8 +14,11 @@
  *   eagle_page_map, eagle_page_reserve, eagle_page_release   pages of a free
  *                                        list to requests and back
  *   eagle_rope                           rotary positions of q and k
+ *   eagle_qk_norm_rope                   norms of their heads and rotary positions
  *   eagle_kv8_append, eagle_kv8_commit, eagle_kv8_commit_root   keys and values into the 8-bit cache
  *   eagle_tree_attn_kv8                  the tree attention over that cache
+ *   eagle_kv8_bounds, eagle_kv8_select, eagle_tree_attn_kv8_pages   the same over the
+ *                                        pages that a query's score selects
  *
  * Sources (the pages the method is taken from):
  *   [EAGLE-2] "論文解説: EAGLE-2 - 動的ドラフトツリーによるLLM推論の高速化"
@@ -596,6 +599,28 @@ int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B,
                const int32_t *pos_off, int shift, void *q_out, void *k_tree,
                void *v_tree, eagle_stream_t stream);
 
+/* eagle_rope after a norm of each head of q and k, in one pass: with
+ *   r = 1 / sqrt(mean over the head's dh columns of x_c^2 + eps),
+ *   y_c = x_c * r * (weight[c] + weight_offset)
+ * the head y turns as eagle_rope turns x (so columns past rot_dim are y); v is
+ * copied.
+ *   q_weight, k_weight  dtype [dh], the same for every head; NULL: y_c = x_c * r
+ *              (weight_offset counts for nothing then)
+ * The other arguments are eagle_rope's.  Everything between the element read and
+ * the one written is float32, rounded once; sums of squares past float32's range
+ * give zeros.  A head that holds an infinity or NaN gives NaN in its own columns
+ * alone.
+ * Limits: those of eagle_rope; eps > 0 and finite, weight_offset finite, weights
+ * 16-byte aligned; B*n*(Hq + 2 Hkv) <= 2^33. */
+int eagle_qk_norm_rope(const void *q, const void *k, const void *v, int dtype,
+                       int B, int n, int Hq, int Hkv, int dh, int64_t ld_q,
+                       int64_t ld_k, int64_t ld_v, const void *q_weight,
+                       const void *k_weight, float weight_offset, float eps,
+                       const double *inv_freq, int rot_dim, int interleaved,
+                       float factor, const int32_t *pos_base,
+                       const int32_t *pos_off, int shift, void *q_out,
+                       void *k_tree, void *v_tree, eagle_stream_t stream);
+
 /* The frequencies of eagle_rope, computed on the host in double:
  * f_j = theta^(-2j / rot_dim), stretched for contexts longer than the
  * orig_len tokens a model was trained on:
@@ -752,6 +777,108 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages,
                         void *out, float *lse, int32_t *status,
                         void *workspace, size_t workspace_bytes,
                         eagle_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Long contexts: attention to the pages that a query selects.
+ * Three calls: bounds of each page's keys, kept beside the pages; the pages whose
+ * bounds allow a query the greatest products; the attention over those pages and
+ * the tree.  A query is a node of the tree and a KV head (the heads that share it
+ * choose together), and what it selects depends on nothing but itself and the
+ * cache: not on the tree around it, the batch or the launch.  So a verification
+ * over selected pages accepts what decoding token by token over selected pages
+ * would produce.
+ *
+ * eagle_kv8_bounds renews the bounds of every page that holds positions
+ * from_len[b] .. kv_len[b]-1 of a request, from all of the page's rows before
+ * kv_len[b]: after an append or a commit, with the length before it (a call that
+ * re-encoded a page's earlier rows touched that page).
+ *   k_pages    as in eagle_kv8_append; block_table, max_pages, page_size,
+ *              num_pages as in eagle_tree_attn_paged
+ *   from_len, kv_len   device int32 [B]; nothing is done where kv_len <= from_len;
+ *              a negative from_len counts as 0, kv_len is clamped to max_pages *
+ *              page_size
+ *   k_bounds   uint8 [num_pages, Hkv, 2, dh]  (in/out): e4m3 numbers in units of
+ *              the page's k_scale: over the page's rows, the least number of each
+ *              column rounded down to a multiple of 1/2, then the greatest rounded
+ *              up (both are e4m3 numbers); -448 and 448 where a row holds NaN.
+ *              Pages that are not touched keep theirs
+ *   status     EAGLE_ERR_INVALID for a block-table entry outside [0, num_pages)
+ *              on a touched page (it is skipped).  A page belongs to one request:
+ *              the bounds of one that two requests touch are unspecified
+ * Limits: dh in {64, 128}; B <= 65535 (else EAGLE_ERR_UNSUPPORTED);
+ * num_pages*Hkv < 2^31; page rules as for eagle_tree_attn_paged.
+ * ------------------------------------------------------------------------ */
+int eagle_kv8_bounds(const uint8_t *k_pages, const int32_t *block_table,
+                     int max_pages, int page_size, int num_pages,
+                     const int32_t *from_len, const int32_t *kv_len, int B,
+                     int Hkv, int dh, uint8_t *k_bounds, int32_t *status,
+                     eagle_stream_t stream);
+
+/* The `top` pages of each node i and KV head g, out of the ceil(kv_len[b] / P)
+ * pages of its sequence's prefix.  A query row (node i, head h) counts as whole
+ * numbers q'_c = rint(q_c / 2^e) with 64 <= max |q'_c| <= 128 (e between -32 and 32,
+ * |q'_c| at most 128 beyond; an element that is not finite counts as 0), and the
+ * score of a page with bounds lo, hi and scale s is
+ *   max over the heads h of g of  2^e s (sum over q'_c > 0 of q'_c hi_c
+ *                                        + sum over q'_c < 0 of q'_c lo_c),
+ * the greatest product with q' of any key within the bounds.
+ * Every score is exact in float32, in any order of the sum.  Selected are the first
+ * `first` and the last `last` pages of the prefix, then the greatest scores, ties to
+ * the lower page; all of them where the prefix has no more than `top`.
+ *   q          dtype [B, n, Hq, dh], as for the attention (rotated)
+ *   k_bounds   as above;  k_scale as in eagle_kv8_append (read as the power of two
+ *              below, clamped to its range)
+ *   sel        device int32 [B, n, Hkv, top] (out): logical page numbers,
+ *              ascending, then -1
+ *   score      device float [B, n, Hkv, top] (out; may be NULL): their scores, also
+ *              of pages that are selected without one, then -inf
+ *   status     EAGLE_ERR_INVALID for a block-table entry outside [0, num_pages)
+ *              (page 0's bounds are read in its place)
+ * Workspace: the scores of all pages, one float for each node, KV head and page.
+ * Limits: dtype EAGLE_BF16, dh in {64, 128}, Hq/Hkv <= 32, max_pages and top <=
+ * 16384, B*Hkv <= 65535, B*n*Hkv <= 2^24, num_pages*Hkv < 2^31 (else
+ * EAGLE_ERR_UNSUPPORTED); 1 <= n <= 4096; 0 <= first, last; first + last <= top;
+ * page rules as for eagle_tree_attn_paged; workspace 16-byte aligned. */
+size_t eagle_kv8_select_workspace_size(int dtype, int B, int n, int Hq, int Hkv,
+                                       int dh, int max_pages, int page_size);
+
+int eagle_kv8_select(const void *q, int dtype, const uint8_t *k_bounds,
+                     const float *k_scale, const int32_t *block_table,
+                     int max_pages, int page_size, int num_pages,
+                     const int32_t *kv_len, int B, int n, int Hq, int Hkv,
+                     int dh, int top, int first, int last, int32_t *sel,
+                     float *score, int32_t *status, void *workspace,
+                     size_t workspace_bytes, eagle_stream_t stream);
+
+/* eagle_tree_attn_kv8 with the prefix of node i and KV head g cut down to the pages
+ * that sel[b, i, g] lists: the keys are the positions below kv_len[b] of those
+ * pages and the tree nodes of the node's mask row.
+ *   sel        device int32 [B, n, Hkv, top], as eagle_kv8_select writes it: logical
+ *              pages, ascending, ended by a negative entry or by `top`
+ *   status     as in eagle_tree_attn_kv8; EAGLE_ERR_INVALID also for a listed page
+ *              at or past the prefix's end (it counts for nothing) and for one that
+ *              does not ascend (the rows of that node and head are unspecified then;
+ *              nothing is read out of range)
+ * Everything else, what is rounded and a row without any key included, is as for
+ * eagle_tree_attn_kv8; only the nodes that a row's own mask names share its
+ * powers of two.
+ * Limits: those of eagle_tree_attn_kv8; Hq/Hkv <= 32 and B*n*Hkv <= 2^24 (else
+ * EAGLE_ERR_UNSUPPORTED); top >= 1, top * page_size <= 2^24. */
+size_t eagle_tree_attn_kv8_pages_workspace_size(int dtype, int B, int n, int Hq,
+                                                int Hkv, int dh, int top,
+                                                int max_pages, int page_size);
+
+int eagle_tree_attn_kv8_pages(const void *q, const uint8_t *k_pages,
+                              const uint8_t *v_pages, const float *k_scale,
+                              const float *v_scale, const int32_t *block_table,
+                              int max_pages, int page_size, int num_pages,
+                              const int32_t *kv_len, const void *k_tree,
+                              const void *v_tree, const uint64_t *mask,
+                              const int32_t *sel, int top, int dtype, int B,
+                              int n, int Hq, int Hkv, int dh, float scale,
+                              void *out, float *lse, int32_t *status,
+                              void *workspace, size_t workspace_bytes,
+                              eagle_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The whole step in one call, and as one recorded graph.

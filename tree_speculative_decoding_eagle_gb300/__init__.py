@@ -23,10 +23,14 @@ library is missing or a call reports an error, an exception is raised.
                    back; slots of new tokens)
     rope        -> eagle_rope         (rotary positions, into the attention's layouts;
                    rope_freqs -> eagle_rope_freqs)
+    qk_norm_rope -> eagle_qk_norm_rope (norms of the heads of q and k before them)
     kv8_append / kv8_commit -> eagle_kv8_append, eagle_kv8_commit,
                    eagle_kv8_commit_root (keys and values into the paged cache
                    of e4m3 numbers)
     tree_attn_kv8 -> eagle_tree_attn_kv8 (tree attention over that cache)
+    kv8_bounds / kv8_select / tree_attn_kv8_pages -> eagle_kv8_bounds,
+                   eagle_kv8_select, eagle_tree_attn_kv8_pages (the same over
+                   the pages that each query's score selects)
     run_step / StepGraph -> eagle_step, eagle_step_graph_* (the four stages
                    in one call, or recorded once as a graph and replayed)
 """
@@ -52,6 +56,8 @@ EXPORTED = (
     "eagle_verify_workspace_size", "eagle_verify", "eagle_verify_noalloc", "eagle_verify_draft",
     "eagle_page_map", "eagle_page_reserve", "eagle_page_release", "eagle_rope", "eagle_rope_freqs",
     "eagle_kv8_append", "eagle_kv8_commit", "eagle_kv8_commit_root", "eagle_tree_attn_kv8_workspace_size", "eagle_tree_attn_kv8",
+    "eagle_qk_norm_rope", "eagle_kv8_bounds", "eagle_kv8_select_workspace_size", "eagle_kv8_select",
+    "eagle_tree_attn_kv8_pages_workspace_size", "eagle_tree_attn_kv8_pages",
     "eagle_step_workspace_size", "eagle_step", "eagle_step_graph_create", "eagle_step_graph_launch",
     "eagle_step_graph_destroy",
 )
@@ -125,6 +131,12 @@ def load_library(path=LIB_PATH):
         "eagle_kv8_commit_root": (I, [P, P, I, I, I, I, I, P, P, I, P, P, P, P, P, I, I, I, P, P, P, P]),
         "eagle_tree_attn_kv8_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
         "eagle_tree_attn_kv8": (I, [P, P, P, P, P, P, I, I, I, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, SZ, P]),
+        "eagle_qk_norm_rope": (I, [P, P, P, I, I, I, I, I, I, I64, I64, I64, P, P, F, F, P, I, I, F, P, P, I, P, P, P, P]),
+        "eagle_kv8_bounds": (I, [P, P, I, I, I, P, P, I, I, I, P, P, P]),
+        "eagle_kv8_select_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
+        "eagle_kv8_select": (I, [P, I, P, P, P, I, I, I, P, I, I, I, I, I, I, I, I, P, P, P, P, SZ, P]),
+        "eagle_tree_attn_kv8_pages_workspace_size": (SZ, [I, I, I, I, I, I, I, I, I]),
+        "eagle_tree_attn_kv8_pages": (I, [P, P, P, P, P, P, I, I, I, P, P, P, P, P, I, I, I, I, I, I, I, F, P, P, P, P, SZ, P]),
         "eagle_step_workspace_size": (SZ, [ctypes.POINTER(StepArgs)]),
         "eagle_step": (I, [ctypes.POINTER(StepArgs), P, SZ, P]),
         "eagle_step_graph_create": (I, [ctypes.POINTER(StepArgs), P, SZ, ctypes.POINTER(P)]),
@@ -529,18 +541,9 @@ def _heads(t, name, B, n, dh, dtype, device):
     return sn
 
 
-def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, interleaved=False, q_out=None,
-         k_tree=None, v_tree=None, stream=None):
-    """Rotary positions (eagle_rope).  q [B, n, Hq, dh], k and v [B, n, Hkv, dh]
-    (v may be None), nodes evenly spaced, so slices of one fused projection do
-    -> q_out [B, n, Hq, dh], k_tree and v_tree [B, Hkv, n, dh], as tree_attn
-    takes them.  Node i of sequence b is at position pos_base[b] + pos_off[b,
-    i] + shift (0 and i where they are None).  inv_freq float64 [rot_dim/2]
-    and factor as rope_freqs gives them."""
-    if stream is not None:     # what is allocated here belongs to that stream
-        with torch.cuda.stream(stream):
-            return rope(q, k, v, inv_freq, pos_base, pos_off, shift, factor, interleaved, q_out, k_tree, v_tree)
-    lib = load_library()
+def _rope_args(q, k, v, inv_freq, pos_base, pos_off, shift, factor, interleaved, q_out, k_tree, v_tree):
+    """What rope() and qk_norm_rope() hand on, checked: the arguments up to the
+    strides, and those from the frequencies on with the three outputs behind them."""
     dev, dt = _device_of(q, "q"), q.dtype
     if q.dim() != 4 or k.dim() != 4:
         raise EagleError("q and k must be [B, n, heads, dh]")
@@ -559,13 +562,49 @@ def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, in
     if v_tree is None and v is not None:
         v_tree = q.new_empty((B, Hkv, n, dh))
     i32 = torch.int32
-    _call("eagle_rope", lib.eagle_rope, dev, None, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(),
-          _dtype_code(q), B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v,
-          _need(inv_freq, "inv_freq", torch.float64, None, dev), 2 * inv_freq.numel(), int(interleaved), factor,
-          _maybe(pos_base, "pos_base", i32, (B,), dev), _maybe(pos_off, "pos_off", i32, (B, n), dev), shift,
-          _need(q_out, "q_out", dt, (B, n, Hq, dh), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),
-          _maybe(v_tree, "v_tree", dt, (B, Hkv, n, dh), dev))
-    return q_out, k_tree, v_tree
+    head = (q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), _dtype_code(q), B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v)
+    tail = [_need(inv_freq, "inv_freq", torch.float64, None, dev), 2 * inv_freq.numel(), int(interleaved), factor,
+            _maybe(pos_base, "pos_base", i32, (B,), dev), _maybe(pos_off, "pos_off", i32, (B, n), dev), shift,
+            _need(q_out, "q_out", dt, (B, n, Hq, dh), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),
+            _maybe(v_tree, "v_tree", dt, (B, Hkv, n, dh), dev), (q_out, k_tree, v_tree)]
+    return head, tail
+
+
+def rope(q, k, v, inv_freq, pos_base=None, pos_off=None, shift=0, factor=1.0, interleaved=False, q_out=None,
+         k_tree=None, v_tree=None, stream=None):
+    """Rotary positions (eagle_rope).  q [B, n, Hq, dh], k and v [B, n, Hkv, dh]
+    (v may be None), nodes evenly spaced, so slices of one fused projection do
+    -> q_out [B, n, Hq, dh], k_tree and v_tree [B, Hkv, n, dh], as tree_attn
+    takes them.  Node i of sequence b is at position pos_base[b] + pos_off[b,
+    i] + shift (0 and i where they are None).  inv_freq float64 [rot_dim/2]
+    and factor as rope_freqs gives them."""
+    if stream is not None:     # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return rope(q, k, v, inv_freq, pos_base, pos_off, shift, factor, interleaved, q_out, k_tree, v_tree)
+    lib = load_library()
+    head, tail = _rope_args(q, k, v, inv_freq, pos_base, pos_off, shift, factor, interleaved, q_out, k_tree, v_tree)
+    out = tail.pop()
+    _call("eagle_rope", lib.eagle_rope, q.get_device(), None, *head, *tail)
+    return out
+
+
+def qk_norm_rope(q, k, v, inv_freq, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, pos_base=None, pos_off=None,
+                 shift=0, factor=1.0, interleaved=False, q_out=None, k_tree=None, v_tree=None, stream=None):
+    """rope() after a norm of each head of q and k (eagle_qk_norm_rope): a head
+    x becomes x / sqrt(mean(x^2) + eps) * (weight + weight_offset), then turns.
+    q_weight, k_weight [dh] of q's type, or None for a norm without a weight; the
+    other arguments and what is returned are rope()'s."""
+    if stream is not None:     # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(q, k, v, inv_freq, q_weight, k_weight, eps, weight_offset, pos_base, pos_off, shift, factor,
+                                interleaved, q_out, k_tree, v_tree)
+    lib = load_library()
+    head, tail = _rope_args(q, k, v, inv_freq, pos_base, pos_off, shift, factor, interleaved, q_out, k_tree, v_tree)
+    out = tail.pop()
+    dev, dt, shape = q.get_device(), q.dtype, q.shape[3:]
+    _call("eagle_qk_norm_rope", lib.eagle_qk_norm_rope, dev, None, *head, _maybe(q_weight, "q_weight", dt, shape, dev),
+          _maybe(k_weight, "k_weight", dt, shape, dev), weight_offset, eps, *tail)
+    return out
 
 
 _POOL_TYPES = (torch.float8_e4m3fn, torch.uint8)
@@ -672,6 +711,100 @@ def tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_
           _need(kv_len, "kv_len", torch.int32, (B,), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),
           _need(v_tree, "v_tree", dt, (B, Hkv, n, dh), dev),
           _need(mask, "mask", torch.int64, (B, n, (n + 63) // 64), dev), code, B, n, Hq, Hkv, dh, scale,
+          _need(out, "out", dt, (B, n, Hq, dh), dev), _need(lse, "lse", torch.float32, (B, n, Hq), dev),
+          _maybe(status, "status", torch.int32, None, dev), None if buf is None else buf.data_ptr(), nbytes)
+    return out, lse
+
+
+def _bounds(k_bounds, num_pages, Hkv, dh, dev):
+    if k_bounds.dtype not in _POOL_TYPES:
+        raise EagleError("k_bounds must be float8_e4m3fn (or uint8) [num_pages, Hkv, 2, dh]")
+    return _need(k_bounds, "k_bounds", k_bounds.dtype, (num_pages, Hkv, 2, dh), dev)
+
+
+def kv8_bounds(k_pages, block_table, from_len, kv_len, k_bounds, status=None, stream=None):
+    """Renews the bounds k_bounds float8_e4m3fn [num_pages, Hkv, 2, dh] (the least
+    and the greatest number of each column, rounded outwards to halves, in units
+    of the page's scale) of the pages that hold positions from_len[b] ..
+    kv_len[b]-1 (eagle_kv8_bounds): after an append or a commit, with the
+    lengths before it."""
+    lib = load_library()
+    dev, i32 = _device_of(k_pages, "k_pages"), torch.int32
+    if k_pages.dtype not in _POOL_TYPES or k_pages.dim() != 4:
+        raise EagleError("k_pages must be float8_e4m3fn (or uint8) [num_pages, Hkv, page_size, dh]")
+    num_pages, Hkv, page_size, dh = k_pages.shape
+    B, max_pages = block_table.shape
+    _call("eagle_kv8_bounds", lib.eagle_kv8_bounds, dev, stream, _need(k_pages, "k_pages", k_pages.dtype, None, dev),
+          _need(block_table, "block_table", i32, (B, max_pages), dev), max_pages, page_size, num_pages,
+          _need(from_len, "from_len", i32, (B,), dev), _need(kv_len, "kv_len", i32, (B,), dev), B, Hkv, dh,
+          _bounds(k_bounds, num_pages, Hkv, dh, dev), _maybe(status, "status", i32, None, dev))
+
+
+def kv8_select(q, k_bounds, k_scale, block_table, kv_len, page_size, top, first=1, last=1, out=None, score=None, workspace=None,
+               status=None, stream=None):
+    """The pages of the prefix that each node and KV head is to attend to
+    (eagle_kv8_select): q [B, n, Hq, dh] bf16, k_bounds as kv8_bounds writes them,
+    k_scale float32 [num_pages, Hkv], block_table int32 [B, max_pages] -> sel int32
+    [B, n, Hkv, top], logical pages in ascending order, then -1: the first `first` and
+    the last `last` pages of the prefix and those whose bounds allow the greatest
+    product with the query.  `score` float32 of the same shape receives theirs."""
+    if stream is not None:     # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return kv8_select(q, k_bounds, k_scale, block_table, kv_len, page_size, top, first, last, out, score, workspace, status)
+    lib = load_library()
+    dev, i32 = _device_of(q, "q"), torch.int32
+    B, n, Hq, dh = q.shape
+    num_pages, Hkv = k_scale.shape
+    max_pages = block_table.shape[1]
+    if out is None:
+        out = torch.empty((B, n, Hkv, top), dtype=i32, device=q.device)
+    code = _dtype_code(q)
+    need = lib.eagle_kv8_select_workspace_size(code, B, n, Hq, Hkv, dh, max_pages, page_size)
+    buf, nbytes = (workspace or Workspace(q.device)).get(need)
+    if buf is not None and buf.get_device() != dev:
+        raise EagleError(f"the workspace must be on device {dev}, not on {buf.device}")
+    _call("eagle_kv8_select", lib.eagle_kv8_select, dev, None, _need(q, "q", q.dtype, None, dev), code,
+          _bounds(k_bounds, num_pages, Hkv, dh, dev), _need(k_scale, "k_scale", torch.float32, None, dev),
+          _need(block_table, "block_table", i32, (B, max_pages), dev), max_pages, page_size, num_pages,
+          _need(kv_len, "kv_len", i32, (B,), dev), B, n, Hq, Hkv, dh, top, first, last,
+          _need(out, "out", i32, (B, n, Hkv, top), dev), _maybe(score, "score", torch.float32, (B, n, Hkv, top), dev),
+          _maybe(status, "status", i32, None, dev), None if buf is None else buf.data_ptr(), nbytes)
+    return out
+
+
+def tree_attn_kv8_pages(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_tree, v_tree, mask, sel, scale=None,
+                        out=None, lse=None, workspace=None, status=None, stream=None):
+    """tree_attn_kv8 with the prefix of each node and KV head cut down to the
+    pages that sel int32 [B, n, Hkv, top] lists, as kv8_select writes it
+    (eagle_tree_attn_kv8_pages)."""
+    if stream is not None:     # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return tree_attn_kv8_pages(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, k_tree, v_tree, mask, sel,
+                                       scale, out, lse, workspace, status)
+    lib = load_library()
+    dev, dt = _device_of(q, "q"), q.dtype
+    B, n, Hq, dh = q.shape
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    max_pages, top = block_table.shape[1], sel.shape[-1]
+    scale = dh ** -0.5 if scale is None else scale
+    if out is None:
+        out = torch.empty((B, n, Hq, dh), dtype=dt, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, n, Hq), dtype=torch.float32, device=q.device)
+    code = _dtype_code(q)
+    if k_pages.shape[3] != dh:
+        raise EagleError("q must have the pages' head dimension")
+    need = lib.eagle_tree_attn_kv8_pages_workspace_size(code, B, n, Hq, Hkv, dh, top, max_pages, page_size)
+    buf, nbytes = (workspace or Workspace(q.device)).get(need)
+    if buf is not None and buf.get_device() != dev:
+        raise EagleError(f"the workspace must be on device {dev}, not on {buf.device}")
+    _call("eagle_tree_attn_kv8_pages", lib.eagle_tree_attn_kv8_pages, dev, None, _need(q, "q", dt, None, dev),
+          *_pools(k_pages, v_pages, k_scale, v_scale, dev),
+          _need(block_table, "block_table", torch.int32, (B, max_pages), dev), max_pages, page_size, num_pages,
+          _need(kv_len, "kv_len", torch.int32, (B,), dev), _need(k_tree, "k_tree", dt, (B, Hkv, n, dh), dev),
+          _need(v_tree, "v_tree", dt, (B, Hkv, n, dh), dev),
+          _need(mask, "mask", torch.int64, (B, n, (n + 63) // 64), dev),
+          _need(sel, "sel", torch.int32, (B, n, Hkv, top), dev), top, code, B, n, Hq, Hkv, dh, scale,
           _need(out, "out", dt, (B, n, Hq, dh), dev), _need(lse, "lse", torch.float32, (B, n, Hq), dev),
           _maybe(status, "status", torch.int32, None, dev), None if buf is None else buf.data_ptr(), nbytes)
     return out, lse

@@ -9,6 +9,10 @@ all on the device, and calls the library's entry points on the current stream:
     commit   -> eagle_kv8_commit_root (root=True), eagle_kv8_commit
                                     the accepted path, in every layer
     release  -> eagle_page_release  pages back: of requests that ended, or past kv_len
+and for long contexts, in a cache made with bounds=True:
+    select   -> eagle_kv8_select    the pages that each node and KV head attends to
+    attend_pages -> eagle_tree_attn_kv8_pages   draft nodes or single tokens over those
+whose bounds (eagle_kv8_bounds) grow() and commit() renew for the pages they touched.
 kv_len counts the positions before the tree's root, which is node 0 of the tree,
 at position kv_len.  So one step over a tree of depth D is
     reserve(D + 1) -> rope(pos_base=kv_len, pos_off=depth) -> attend -> verify
@@ -23,7 +27,8 @@ Workspace each.  The layers share block tables and lengths.
 """
 import torch
 
-from . import EagleError, Workspace, kv8_append, kv8_commit, page_map, page_release, tree_attn_kv8
+from . import (EagleError, Workspace, kv8_append, kv8_bounds, kv8_commit, kv8_select, page_map, page_release, tree_attn_kv8,
+               tree_attn_kv8_pages)
 
 
 class _KeptWorkspace(Workspace):
@@ -42,7 +47,7 @@ class _KeptWorkspace(Workspace):
 
 
 class KV8Cache:
-    def __init__(self, B, Hkv, dh, page_size, num_pages, max_pages, layers=1, device="cuda"):
+    def __init__(self, B, Hkv, dh, page_size, num_pages, max_pages, layers=1, device="cuda", bounds=False):
         if layers < 1:
             raise EagleError("a cache needs a layer")
         i32 = dict(dtype=torch.int32, device=device)
@@ -52,6 +57,11 @@ class KV8Cache:
         self.v_pages = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(layers)]
         self.k_scale = [torch.ones((num_pages, Hkv), device=device) for _ in range(layers)]
         self.v_scale = [torch.ones((num_pages, Hkv), device=device) for _ in range(layers)]
+        self.k_bounds = None
+        if bounds:
+            shape = (num_pages, Hkv, 2, dh)
+            self.k_bounds = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(layers)]
+            self._before = torch.zeros(B, **i32)      # the lengths before grow() or commit()
         self.block_table = torch.full((B, max_pages), -1, **i32)
         self.page_count = torch.zeros(B, **i32)
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)      # page 0 on top
@@ -79,15 +89,37 @@ class KV8Cache:
 
     def grow(self, new_len):
         """new_len [B] (or one number) tokens have been appended; counts nothing
-        where the last reservation was refused, since append() wrote none."""
+        where the last reservation was refused, since append() wrote none.
+        Renews the bounds of the pages they are in, where the cache has bounds."""
+        if self.k_bounds is not None:
+            self._before.copy_(self.kv_len)
         if torch.is_tensor(new_len):
             self.kv_len.addcmul_(self.granted, new_len.to(torch.int32))
         else:
             torch.add(self.kv_len, self.granted, alpha=new_len, out=self.kv_len)
+        self._renew_bounds()
+
+    def _renew_bounds(self):
+        if self.k_bounds is not None:
+            for pages, bounds in zip(self.k_pages, self.k_bounds):
+                kv8_bounds(pages, self.block_table, self._before, self.kv_len, bounds, status=self.status)
 
     def attend(self, layer, q, k_tree, v_tree, mask, scale=None, out=None, lse=None, workspace=None):
         return tree_attn_kv8(q, *self._pools(layer), self.block_table, self.kv_len, k_tree, v_tree, mask, scale=scale,
                              out=out, lse=lse, workspace=workspace or self._ws, status=self.status)
+
+    def select(self, layer, q, top, first=1, last=1, out=None, score=None, workspace=None):
+        """The pages of the prefix that each node and KV head of q [B, n, Hq, dh]
+        is to attend to: sel int32 [B, n, Hkv, top] (kv8_select)."""
+        if self.k_bounds is None:
+            raise EagleError("select takes a cache made with bounds=True")
+        return kv8_select(q, self.k_bounds[layer], self.k_scale[layer], self.block_table, self.kv_len, self.page_size, top,
+                          first=first, last=last, out=out, score=score, workspace=workspace or self._ws, status=self.status)
+
+    def attend_pages(self, layer, q, k_tree, v_tree, mask, sel, scale=None, out=None, lse=None, workspace=None):
+        """attend() over the pages that sel lists, as select() returns it."""
+        return tree_attn_kv8_pages(q, *self._pools(layer), self.block_table, self.kv_len, k_tree, v_tree, mask, sel, scale=scale,
+                                   out=out, lse=lse, workspace=workspace or self._ws, status=self.status)
 
     def commit(self, k_trees, v_trees, accept_len, path_nodes, slot_mapping=None, root=False):
         """The accepted path of every layer (lists of k_tree, v_tree).  With
@@ -98,6 +130,8 @@ class KV8Cache:
         last = len(self.k_pages) - 1
         if len(k_trees) != last + 1 or len(v_trees) != last + 1:
             raise EagleError("commit takes the tree K/V of every layer")
+        if self.k_bounds is not None:
+            self._before.copy_(self.kv_len)
         for layer, (k, v) in enumerate(zip(k_trees, v_trees)):
             lens = self.kv_len
             if layer < last:
@@ -105,6 +139,7 @@ class KV8Cache:
                 lens.copy_(self.kv_len)
             slot_mapping = kv8_commit(k, v, accept_len, path_nodes, *self._pools(layer), lens, self.block_table,
                                       slot_mapping=slot_mapping, status=self.status, root=root)
+        self._renew_bounds()
         return slot_mapping
 
     def trim(self):

@@ -57,6 +57,31 @@ cudaError_t launch_tree_attn_tc(const void *q, const void *k_cache, const void *
                                 const void *k_tree, const void *v_tree, const uint64_t *mask, int B, int n,
                                 int Hq, int Hkv, int dh, int Lmax, float scale, void *out, float *lse, void *ws,
                                 int32_t *status, int num_sms, cudaStream_t st);
+// qk_norm_rope.cu
+cudaError_t launch_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv,
+                                int dh, int64_t ld_q, int64_t ld_k, int64_t ld_v, const void *q_weight,
+                                const void *k_weight, float weight_offset, float eps, const double *inv_freq,
+                                int rot_dim, int interleaved, float factor, const int32_t *pos_base,
+                                const int32_t *pos_off, int shift, void *q_out, void *k_tree, void *v_tree,
+                                cudaStream_t st);
+// kv8_bounds.cu
+cudaError_t launch_kv8_bounds(const uint8_t *k_pages, const int32_t *block_table, int max_pages, int page_size,
+                              int num_pages, const int32_t *from_len, const int32_t *kv_len, int B, int Hkv, int dh,
+                              uint8_t *bounds, int32_t *status, int num_sms, cudaStream_t st);
+// kv8_select.cu
+size_t kv8_select_workspace_bytes(int B, int n, int Hkv, int max_pages);
+cudaError_t launch_kv8_select(const void *q, const uint8_t *bounds, const float *k_scale, const int32_t *block_table,
+                              int max_pages, int page_size, int num_pages, const int32_t *kv_len, int B, int n, int Hq,
+                              int Hkv, int dh, int top, int first, int last, int32_t *sel, float *score, void *ws,
+                              int32_t *status, int num_sms, cudaStream_t st);
+// tree_attn_kv8_few.cu
+size_t attn_kv8_pages_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int top, int max_pages, int page_size, int num_sms);
+cudaError_t launch_tree_attn_kv8_pages(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
+                                       const float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                                       int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
+                                       const uint64_t *mask, const int32_t *sel, int top, int B, int n, int Hq, int Hkv,
+                                       int dh, float scale, void *out, float *lse, void *ws, int32_t *status, int num_sms,
+                                       cudaStream_t st);
 // verify.cu
 size_t verify_workspace_bytes(int B, int m, int V);
 cudaError_t launch_verify(const void *target, int dtype, int64_t ld, const int32_t *node_tok,
@@ -383,10 +408,10 @@ int eagle_page_release(const int32_t *keep_len, int B, int page_size, int max_pa
                                        free_pages, free_count, status, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv, int dh,
-               int64_t ld_q, int64_t ld_k, int64_t ld_v, const double *inv_freq, int rot_dim, int interleaved,
-               float factor, const int32_t *pos_base, const int32_t *pos_off, int shift, void *q_out, void *k_tree,
-               void *v_tree, eagle_stream_t stream) {
+// Shared by eagle_rope and eagle_qk_norm_rope.
+static int check_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv, int dh,
+                      int64_t ld_q, int64_t ld_k, int64_t ld_v, const double *inv_freq, int rot_dim, const void *q_out,
+                      const void *k_tree, const void *v_tree) {
   if (!q || !k || !inv_freq || !q_out || !k_tree || (v && !v_tree) || !valid_dtype(dtype)) return EAGLE_ERR_INVALID;
   if (B < 1 || n < 1 || Hq < 1 || Hkv < 1 || dh < 1 || rot_dim < 2 || rot_dim % 2 || rot_dim > dh)
     return EAGLE_ERR_INVALID;
@@ -401,9 +426,35 @@ int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B, in
       !aligned16(v_tree))
     return EAGLE_ERR_INVALID;
   if (q_out == q && ld_q != static_cast<int64_t>(Hq) * dh) return EAGLE_ERR_INVALID;
+  return EAGLE_OK;
+}
+
+int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv, int dh,
+               int64_t ld_q, int64_t ld_k, int64_t ld_v, const double *inv_freq, int rot_dim, int interleaved,
+               float factor, const int32_t *pos_base, const int32_t *pos_off, int shift, void *q_out, void *k_tree,
+               void *v_tree, eagle_stream_t stream) {
+  const int rc = check_rope(q, k, v, dtype, B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v, inv_freq, rot_dim, q_out, k_tree, v_tree);
+  if (rc != EAGLE_OK) return rc;
   return from_cuda(launch_rope(q, k, v, dtype, B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v, inv_freq, rot_dim, interleaved,
                                factor, pos_base, pos_off, shift, q_out, k_tree, v_tree,
                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv, int dh,
+                       int64_t ld_q, int64_t ld_k, int64_t ld_v, const void *q_weight, const void *k_weight,
+                       float weight_offset, float eps, const double *inv_freq, int rot_dim, int interleaved,
+                       float factor, const int32_t *pos_base, const int32_t *pos_off, int shift, void *q_out,
+                       void *k_tree, void *v_tree, eagle_stream_t stream) {
+  const int rc = check_rope(q, k, v, dtype, B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v, inv_freq, rot_dim, q_out, k_tree, v_tree);
+  if (rc != EAGLE_OK) return rc;
+  constexpr float kMax = std::numeric_limits<float>::max();  // no NaN, no infinity
+  if (!(eps > 0.f && eps <= kMax) || !(weight_offset >= -kMax && weight_offset <= kMax)) return EAGLE_ERR_INVALID;
+  if (!aligned16(q_weight) || !aligned16(k_weight)) return EAGLE_ERR_INVALID;
+  // a CTA takes eight heads or more: the grid stays below 2^31
+  if (static_cast<int64_t>(B) * n * (static_cast<int64_t>(Hq) + 2ll * Hkv) > (1ll << 33)) return EAGLE_ERR_UNSUPPORTED;
+  return from_cuda(launch_qk_norm_rope(q, k, v, dtype, B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v, q_weight, k_weight,
+                                       weight_offset, eps, inv_freq, rot_dim, interleaved, factor, pos_base, pos_off,
+                                       shift, q_out, k_tree, v_tree, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch, int orig_len, double low, double high,
@@ -506,6 +557,91 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages, const uint8_t *v_
   return from_cuda(launch_tree_attn_kv8(q, k_pages, v_pages, k_scale, v_scale, block_table, max_pages, page_size,
                                         num_pages, kv_len, k_tree, v_tree, mask, B, n, Hq, Hkv, dh, scale, out, lse,
                                         workspace, status, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kv8_bounds(const uint8_t *k_pages, const int32_t *block_table, int max_pages, int page_size, int num_pages,
+                     const int32_t *from_len, const int32_t *kv_len, int B, int Hkv, int dh, uint8_t *k_bounds,
+                     int32_t *status, eagle_stream_t stream) {
+  if (!k_pages || !block_table || !from_len || !kv_len || !k_bounds) return EAGLE_ERR_INVALID;
+  if (B < 1 || Hkv < 1 || !valid_pages(max_pages, page_size, num_pages)) return EAGLE_ERR_INVALID;
+  if ((dh != 64 && dh != 128) || B > 65535 || static_cast<int64_t>(num_pages) * Hkv > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
+  if (!aligned16(k_pages) || !aligned16(k_bounds)) return EAGLE_ERR_INVALID;
+  return from_cuda(launch_kv8_bounds(k_pages, block_table, max_pages, page_size, num_pages, from_len, kv_len, B, Hkv, dh,
+                                     k_bounds, status, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+constexpr int kMaxSelectPages = 16384;  // a request's pages: a row's scores are held by the threads of one CTA
+
+// Nodes by KV heads of a call with selected pages, and heads of a KV head: EAGLE_OK or what is wrong.
+static int check_nodes(int B, int n, int Hq, int Hkv, int dh) {
+  if (B < 1 || n < 1 || n > 4096 || Hq < 1 || Hkv < 1 || Hq % Hkv) return EAGLE_ERR_INVALID;
+  if ((dh != 64 && dh != 128) || Hq / Hkv > 32 || static_cast<int64_t>(B) * Hkv > 65535 ||
+      static_cast<int64_t>(B) * n * Hkv > (1 << 24))
+    return EAGLE_ERR_UNSUPPORTED;
+  return EAGLE_OK;
+}
+
+size_t eagle_kv8_select_workspace_size(int dtype, int B, int n, int Hq, int Hkv, int dh, int max_pages, int page_size) {
+  if (dtype != EAGLE_BF16 || check_nodes(B, n, Hq, Hkv, dh) != EAGLE_OK || !valid_pages(max_pages, page_size, 1) ||
+      max_pages > kMaxSelectPages)
+    return 0;
+  return kv8_select_workspace_bytes(B, n, Hkv, max_pages);
+}
+
+int eagle_kv8_select(const void *q, int dtype, const uint8_t *k_bounds, const float *k_scale, const int32_t *block_table,
+                     int max_pages, int page_size, int num_pages, const int32_t *kv_len, int B, int n, int Hq, int Hkv,
+                     int dh, int top, int first, int last, int32_t *sel, float *score, int32_t *status, void *workspace,
+                     size_t workspace_bytes, eagle_stream_t stream) {
+  if (!q || !k_bounds || !k_scale || !block_table || !kv_len || !sel) return EAGLE_ERR_INVALID;
+  if (!valid_dtype(dtype) || !valid_pages(max_pages, page_size, num_pages) || top < 1 || first < 0 || last < 0 ||
+      first > top || last > top - first)
+    return EAGLE_ERR_INVALID;
+  const int rc = check_nodes(B, n, Hq, Hkv, dh);
+  if (rc != EAGLE_OK) return rc;
+  if (dtype != EAGLE_BF16 || max_pages > kMaxSelectPages || top > kMaxSelectPages ||
+      static_cast<int64_t>(num_pages) * Hkv > INT32_MAX)
+    return EAGLE_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_bounds) || !aligned16(workspace)) return EAGLE_ERR_INVALID;
+  if (!workspace || workspace_bytes < kv8_select_workspace_bytes(B, n, Hkv, max_pages)) return EAGLE_ERR_WORKSPACE;
+  return from_cuda(launch_kv8_select(q, k_bounds, k_scale, block_table, max_pages, page_size, num_pages, kv_len, B, n, Hq,
+                                     Hkv, dh, top, first, last, sel, score, workspace, status, current_num_sms(),
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Positions of a list of selected pages, as for a block table.
+static bool valid_list(int top, int page_size) { return top >= 1 && static_cast<int64_t>(top) * page_size <= (1 << 24); }
+
+size_t eagle_tree_attn_kv8_pages_workspace_size(int dtype, int B, int n, int Hq, int Hkv, int dh, int top, int max_pages,
+                                                int page_size) {
+  if (dtype != EAGLE_BF16 || check_nodes(B, n, Hq, Hkv, dh) != EAGLE_OK || !valid_pages(max_pages, page_size, 1) ||
+      !valid_list(top, page_size))
+    return 0;
+  return attn_kv8_pages_workspace_bytes(B, n, Hq, Hkv, dh, top, max_pages, page_size, current_num_sms());
+}
+
+int eagle_tree_attn_kv8_pages(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
+                              const float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                              int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
+                              const uint64_t *mask, const int32_t *sel, int top, int dtype, int B, int n, int Hq, int Hkv,
+                              int dh, float scale, void *out, float *lse, int32_t *status, void *workspace,
+                              size_t workspace_bytes, eagle_stream_t stream) {
+  if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !kv_len || !k_tree || !v_tree || !mask ||
+      !sel || !out)
+    return EAGLE_ERR_INVALID;
+  if (!valid_dtype(dtype) || !(scale > 0.f) || !valid_pages(max_pages, page_size, num_pages) || !valid_list(top, page_size))
+    return EAGLE_ERR_INVALID;
+  const int rc = check_nodes(B, n, Hq, Hkv, dh);
+  if (rc != EAGLE_OK) return rc;
+  if (dtype != EAGLE_BF16 || static_cast<int64_t>(num_pages) * Hkv > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_tree) || !aligned16(v_tree) ||
+      !aligned16(out) || !aligned16(workspace))  // partial results are float4s
+    return EAGLE_ERR_INVALID;
+  const int sms = current_num_sms();
+  const size_t need = attn_kv8_pages_workspace_bytes(B, n, Hq, Hkv, dh, top, max_pages, page_size, sms);
+  if (workspace_bytes < need || (need && !workspace)) return EAGLE_ERR_WORKSPACE;
+  return from_cuda(launch_tree_attn_kv8_pages(q, k_pages, v_pages, k_scale, v_scale, block_table, max_pages, page_size,
+                                              num_pages, kv_len, k_tree, v_tree, mask, sel, top, B, n, Hq, Hkv, dh, scale,
+                                              out, lse, workspace, status, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -52,9 +52,22 @@ __device__ __forceinline__ int o_chunk(int r, int c) {
   return r * (DH / 4) + (c ^ key);
 }
 
-template <int DH, int RG, int MERGE>
+// What the launch with selected pages has beside: B and n of Kv8Args are B * nodes
+// and 1 there.
+struct Kv8SelArgs : Kv8Args {
+  const int32_t *sel;
+  int top, nodes;
+};
+template <bool SEL> struct FewArgs { using type = Kv8Args; };
+template <> struct FewArgs<true> { using type = Kv8SelArgs; };
+
+// SEL: a "sequence" is one node of a sequence, with the pages that its row of `sel`
+// lists for the KV head in place of the whole prefix, and the nodes of its mask row;
+// its rows are the head's grouped queries alone.
+template <int DH, int RG, int MERGE, bool SEL>
 __global__ void __launch_bounds__(128, 3)
-    tree_attn_kv8_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, Kv8Args a) {
+    tree_attn_kv8_few_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                             typename FewArgs<SEL>::type a) {
   constexpr int KG = 4 / RG;
   constexpr int STAGE = 32 * DH;                    // 16 keys' K, then V
   constexpr int DEPTH = kRingBytes / KG / STAGE;
@@ -69,12 +82,20 @@ __global__ void __launch_bounds__(128, 3)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   const int kg = warp / RG, rg = warp % RG;
-  const int split = blockIdx.x, bg = blockIdx.z, b = bg / a.Hkv, g = bg % a.Hkv;
+  const int split = SEL ? blockIdx.x % a.S : blockIdx.x, bg = SEL ? blockIdx.x / a.S : blockIdx.z;
+  const int b = bg / a.Hkv, g = bg % a.Hkv;
+  int seq = b, nodes = a.n;  // whose cache and tree, its nodes
+  const int32_t *list = nullptr;
+  if constexpr (SEL) {
+    seq = b / a.nodes;
+    nodes = a.nodes;
+    list = a.sel + static_cast<int64_t>(bg) * a.top;
+  }
   unsigned char *ring = ring0 + kg * DEPTH * STAGE;
   uint64_t *kfull = full + kg * DEPTH, *kempty = empty + kg * DEPTH;
 
   if (tid == 0) {
-    prefetch_l2(a.kv_len + b);
+    prefetch_l2(a.kv_len + seq);
     prefetch_tmap(&k_map);
     prefetch_tmap(&v_map);
     for (int i = 0; i < KG * DEPTH; ++i) {
@@ -99,21 +120,50 @@ __global__ void __launch_bounds__(128, 3)
             a.q + ((static_cast<int64_t>(b) * a.n + rho / a.G) * a.Hq + g * a.G + rho % a.G) * DH + t * (DH / 4) + c * 8);
     }
   }
-  const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
-  const int groups = (L + 15) >> 4, per = (groups + a.S - 1) / a.S;
+  const int L = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[seq], 0)), static_cast<int64_t>(a.max_pages) << a.log_page));
+  int groups = (L + 15) >> 4;
+  if constexpr (SEL) {  // of the entries before the first -1, the last one's page as far as the prefix goes
+    int entries = 0;
+    for (bool whole = true; whole && entries < a.top;) {
+      const uint32_t on = __ballot_sync(0xffffffffu, entries + lane < a.top && list[entries + lane] >= 0);
+      entries += on == 0xffffffffu ? 32 : __ffs(~on) - 1;
+      whole = on == 0xffffffffu;
+    }
+    const int64_t tail = entries ? L - (static_cast<int64_t>(list[entries - 1]) << a.log_page) : 0;
+    if (entries && tail <= 0) report(a.status, EAGLE_ERR_INVALID);  // past the prefix: nothing of it is read
+    groups = entries ? ((entries - 1) << (a.log_page - 4)) +
+                           ((static_cast<int>(min(max(tail, static_cast<int64_t>(0)), static_cast<int64_t>(a.page_size))) + 15) >> 4)
+                     : 0;
+  }
+  const int per = (groups + a.S - 1) / a.S;
   const int g0 = min(groups, split * per) + kg, g1 = min(groups, split * per + per);
   const int n_it = g1 > g0 ? (g1 - g0 + KG - 1) / KG : 0;  // this warp's groups: g0, g0 + KG, ..
 
   // Lane i of batch k looks after iteration 32k + i: its page, then its scales.
-  const auto page_at = [&](int batch) {
+  // SEL: `keys` becomes the prefix's positions from its group's first on (16 or more:
+  // all of the group counts; 0: none does).
+  const auto page_at = [&](int batch, int &keys) {
     const int it = batch * 32 + lane;
+    keys = 0;
     if (it >= n_it) return 0;
-    const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + (((g0 + it * KG) << 4) >> a.log_page)];
+    int lp = ((g0 + it * KG) << 4) >> a.log_page;
+    if constexpr (SEL) {
+      const int before = lp ? list[lp - 1] : -1;
+      lp = list[lp];
+      const int64_t first = (static_cast<int64_t>(lp) << a.log_page) + (((g0 + it * KG) << 4) & (a.page_size - 1));
+      if (lp <= before || first >= L) {  // out of order, or past the prefix
+        report(a.status, EAGLE_ERR_INVALID);
+        return 0;
+      }
+      keys = L - static_cast<int>(first);
+    }
+    const int page = a.block_table[static_cast<int64_t>(seq) * a.max_pages + lp];
     if (page >= 0 && page < a.num_pages) return page;
     report(a.status, EAGLE_ERR_INVALID);  // outside the pool: read page 0
     return 0;
   };
-  int page = page_at(0), page_next = page_at(1);
+  int keys = 0, keys_next = 0;
+  int page = page_at(0, keys), page_next = page_at(1, keys_next);
   __syncthreads();
   const auto issue = [&](int it, int pg) {  // lane 0
     unsigned char *dst = ring + (it % DEPTH) * STAGE;
@@ -214,7 +264,8 @@ __global__ void __launch_bounds__(128, 3)
     if ((it & 31) == 0) {
       if (it) {
         page = page_next; ks = ks_next; vs = vs_next;
-        page_next = page_at((it >> 5) + 1);
+        keys = keys_next;
+        page_next = page_at((it >> 5) + 1, keys_next);
         page_ahead = page_next;
       }
       ks_next = a.k_scale[static_cast<int64_t>(page_next) * a.Hkv + g];
@@ -224,7 +275,8 @@ __global__ void __launch_bounds__(128, 3)
     if (!warp_wait(&kfull[st], (it / DEPTH) & 1, abort_flag)) { ok = false; break; }
     __syncwarp();
     const unsigned char *kst = ring + st * STAGE, *vst = kst + STAGE / 2;
-    const int valid = L - ((g0 + it * KG) << 4);  // below 16 in the prefix's last group only
+    // below 16 in the prefix's last group only
+    const int valid = SEL ? __shfl_sync(0xffffffffu, keys, it & 31) : L - ((g0 + it * KG) << 4);
     uint32_t kw[2][KW], vw[4][VW];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -306,21 +358,25 @@ __global__ void __launch_bounds__(128, 3)
 
   // ---- the tree: groups of 16 nodes, bf16 over the group's powers of two -----
   if (ok && split == a.S - 1) {
-    for (int n0 = kg * 16; n0 < a.n; n0 += KG * 16) {
-      const __nv_bfloat16 *kt = a.k_tree + (static_cast<int64_t>(bg) * a.n + n0) * DH;
-      const __nv_bfloat16 *vt = a.v_tree + (static_cast<int64_t>(bg) * a.n + n0) * DH;
+    for (int n0 = kg * 16; n0 < nodes; n0 += KG * 16) {
+      const int64_t tree = ((SEL ? static_cast<int64_t>(seq) * a.Hkv + g : bg) * static_cast<int64_t>(nodes) + n0) * DH;
+      const __nv_bfloat16 *kt = a.k_tree + tree, *vt = a.v_tree + tree;
       uint4 x[2][DH / 32], y[4][DH / 64];
       float kmax = 0.f, vmax = 0.f;
       // the nodes that a row attends to (there are at most kFewRows rows of nodes, so
       // a lane each and one mask word); the others are zeros and decide nothing
       uint32_t attended = 0;
-      if (lane < a.n) attended = static_cast<uint32_t>(a.mask[static_cast<int64_t>(b) * a.n + lane] >> n0) & 0xffffu;
+      if constexpr (SEL) {
+        attended = static_cast<uint32_t>(a.mask[static_cast<int64_t>(b) * a.W + (n0 >> 6)] >> (n0 & 63)) & 0xffffu;
+        if (n0 + 16 > nodes) attended &= (1u << (nodes - n0)) - 1u;
+        if (!attended) continue;  // the same in the whole warp
+      } else if (lane < a.n) attended = static_cast<uint32_t>(a.mask[static_cast<int64_t>(b) * a.n + lane] >> n0) & 0xffffu;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) {
           x[h][i] = make_uint4(0, 0, 0, 0);
-          if (n0 + gr + 8 * h < a.n) x[h][i] = *reinterpret_cast<const uint4 *>(kt + (gr + 8 * h) * DH + t * (DH / 4) + i * 8);
+          if (n0 + gr + 8 * h < nodes && (!SEL || ((attended >> (gr + 8 * h)) & 1u))) x[h][i] = *reinterpret_cast<const uint4 *>(kt + (gr + 8 * h) * DH + t * (DH / 4) + i * 8);
         }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -328,9 +384,9 @@ __global__ void __launch_bounds__(128, 3)
         for (int i = 0; i < DH / 64; ++i) {
           const int r = 2 * t + (q & 1) + 8 * (q >> 1);
           y[q][i] = make_uint4(0, 0, 0, 0);
-          if (n0 + r < a.n) y[q][i] = *reinterpret_cast<const uint4 *>(vt + r * DH + gr * (DH / 8) + i * 8);
+          if (n0 + r < nodes && (!SEL || ((attended >> r) & 1u))) y[q][i] = *reinterpret_cast<const uint4 *>(vt + r * DH + gr * (DH / 8) + i * 8);
         }
-      attended = __reduce_or_sync(0xffffffffu, attended);
+      if constexpr (!SEL) attended = __reduce_or_sync(0xffffffffu, attended);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -349,6 +405,10 @@ __global__ void __launch_bounds__(128, 3)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         bits[r] = 0;
+        if (SEL) {
+          bits[r] = node[r] >= 0 ? attended : 0u;
+          continue;
+        }
         if (node[r] >= 0)
           bits[r] = static_cast<uint32_t>(a.mask[static_cast<int64_t>(b) * a.n + node[r]] >> n0) & 0xffffu;
         if (n0 + 16 > a.n) bits[r] &= (1u << (a.n - n0)) - 1u;
@@ -483,31 +543,51 @@ size_t attn_kv8_few_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int L
   return p.S <= 1 ? 0 : static_cast<size_t>(B) * Hkv * p.S * ((rows + 7) / 8 * 8) * (dh + 2) * sizeof(float);
 }
 
-template <int DH, int RG, int MERGE>
-static cudaError_t launch_few_v(const CUtensorMap *maps, const Kv8Args &a, cudaStream_t st) {
+// The merge where B * Hkv passes a grid's z dimension: the items of all (b, g) in one row.
+template <int DH>
+__global__ void __launch_bounds__(256) tree_attn_kv8_merge_flat_kernel(Kv8Args a) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int per = a.n * a.G * (DH / 4);
+  pdl_wait();  // the partial results come from the attention kernel
+  const int64_t bg = item / per;
+  if (bg < static_cast<int64_t>(a.B) * a.Hkv) {
+    const int at = static_cast<int>(item - bg * per);
+    kv8_merge_item<DH>(a, static_cast<int>(bg), 0, 1, at / (DH / 4), at % (DH / 4));
+  }
+}
+
+template <int DH, int RG, int MERGE, bool SEL>
+static cudaError_t launch_few_v(const CUtensorMap *maps, const typename FewArgs<SEL>::type &a, cudaStream_t st) {
   static std::atomic<unsigned long long> configured{0};
   constexpr int kSmem = kRingBytes + 1024;
-  cudaError_t e = set_smem_limit_once(tree_attn_kv8_few_kernel<DH, RG, MERGE>, kSmem, configured);
+  const auto kernel = tree_attn_kv8_few_kernel<DH, RG, MERGE, SEL>;
+  cudaError_t e = set_smem_limit_once(kernel, kSmem, configured);
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.S, 1, a.B * a.Hkv);
+  const dim3 grid(SEL ? a.S * a.B * a.Hkv : a.S, 1, SEL ? 1 : a.B * a.Hkv);
   if constexpr (MERGE == 1)
-    return launch_chained_cluster(tree_attn_kv8_few_kernel<DH, RG, MERGE>, grid, dim3(128), kSmem, st, a.S, maps[0], maps[1], a);
-  e = launch_chained(tree_attn_kv8_few_kernel<DH, RG, MERGE>, grid, dim3(128), kSmem, st, maps[0], maps[1], a);
+    return launch_chained_cluster(kernel, grid, dim3(128), kSmem, st, a.S, maps[0], maps[1], a);
+  e = launch_chained(kernel, grid, dim3(128), kSmem, st, maps[0], maps[1], a);
   if (e != cudaSuccess || MERGE == 0) return e;
+  if constexpr (SEL) {
+    const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * a.n * a.G * (DH / 4);
+    return launch_chained(tree_attn_kv8_merge_flat_kernel<DH>, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0,
+                          st, static_cast<const Kv8Args &>(a));
+  }
   return launch_chained(tree_attn_kv8_merge_kernel<DH>, dim3((a.slot_rows * (DH / 4) + 255) / 256, 1, a.B * a.Hkv), dim3(256), 0,
                         st, a, 1);
 }
 
-template <int DH, int RG>
-static cudaError_t launch_few_t(const CUtensorMap *maps, const Kv8Args &a, const FewPlan &p, cudaStream_t st) {
-  if (p.S == 1) return launch_few_v<DH, RG, 0>(maps, a, st);
-  return p.cluster ? launch_few_v<DH, RG, 1>(maps, a, st) : launch_few_v<DH, RG, 2>(maps, a, st);
+template <int DH, int RG, bool SEL>
+static cudaError_t launch_few_t(const CUtensorMap *maps, const typename FewArgs<SEL>::type &a, const FewPlan &p, cudaStream_t st) {
+  if (p.S == 1) return launch_few_v<DH, RG, 0, SEL>(maps, a, st);
+  return p.cluster ? launch_few_v<DH, RG, 1, SEL>(maps, a, st) : launch_few_v<DH, RG, 2, SEL>(maps, a, st);
 }
 
-cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void *v_pages, int dh, void *ws, int num_sms,
-                                     cudaStream_t st) {
+template <bool SEL>
+static cudaError_t launch_few(typename FewArgs<SEL>::type a, const void *k_pages, const void *v_pages, int dh, int Lmax, void *ws,
+                              int num_sms, cudaStream_t st) {
   const int rows = a.n * a.G;
-  const FewPlan p = few_plan(a.B, rows, a.Hkv, a.max_pages * a.page_size, num_sms);
+  const FewPlan p = few_plan(a.B, rows, a.Hkv, Lmax, num_sms);
   if (p.S > 1 && !ws) return cudaErrorInvalidValue;
   a.S = p.S;
   a.page_box = 16;
@@ -519,11 +599,45 @@ cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void 
       !make_pool_map(&maps[1], v_pages, blocks, a.page_size, dh, 16, true))
     return cudaErrorInvalidValue;
   if (dh == 64) {
-    if (p.RG == 1) return launch_few_t<64, 1>(maps, a, p, st);
-    return launch_few_t<64, 2>(maps, a, p, st);
+    if (p.RG == 1) return launch_few_t<64, 1, SEL>(maps, a, p, st);
+    return launch_few_t<64, 2, SEL>(maps, a, p, st);
   }
-  if (p.RG == 1) return launch_few_t<128, 1>(maps, a, p, st);
-  return launch_few_t<128, 2>(maps, a, p, st);
+  if (p.RG == 1) return launch_few_t<128, 1, SEL>(maps, a, p, st);
+  return launch_few_t<128, 2, SEL>(maps, a, p, st);
+}
+
+cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void *v_pages, int dh, void *ws, int num_sms,
+                                     cudaStream_t st) {
+  return launch_few<false>(a, k_pages, v_pages, dh, a.max_pages * a.page_size, ws, num_sms, st);
+}
+
+// Positions a node's list holds at most.
+static int listed_positions(int top, int max_pages, int page_size) { return (top < max_pages ? top : max_pages) * page_size; }
+
+size_t attn_kv8_pages_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int top, int max_pages, int page_size, int num_sms) {
+  return attn_kv8_few_workspace_bytes(B * n, 1, Hq, Hkv, dh, listed_positions(top, max_pages, page_size), num_sms);
+}
+
+cudaError_t launch_tree_attn_kv8_pages(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
+                                       const float *v_scale, const int32_t *block_table, int max_pages, int page_size,
+                                       int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
+                                       const uint64_t *mask, const int32_t *sel, int top, int B, int n, int Hq, int Hkv,
+                                       int dh, float scale, void *out, float *lse, void *ws, int32_t *status, int num_sms,
+                                       cudaStream_t st) {
+  Kv8SelArgs a = {};
+  a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+  a.k_tree = reinterpret_cast<const __nv_bfloat16 *>(k_tree);
+  a.v_tree = reinterpret_cast<const __nv_bfloat16 *>(v_tree);
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.block_table = block_table; a.kv_len = kv_len; a.mask = mask;
+  a.B = B * n; a.n = 1; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.W = (n + 63) / 64;
+  a.page_size = page_size; a.max_pages = max_pages; a.num_pages = num_pages;
+  while ((1 << a.log_page) < page_size) ++a.log_page;
+  a.scale_log2 = scale * kLog2e;
+  a.out = reinterpret_cast<__nv_bfloat16 *>(out);
+  a.lse = lse; a.status = status;
+  a.sel = sel; a.top = top; a.nodes = n;
+  return launch_few<true>(a, k_pages, v_pages, dh, listed_positions(top, max_pages, page_size), ws, num_sms, st);
 }
 
 }  // namespace eagle

@@ -42,6 +42,7 @@ class TreeStep:
         self.ws_attn = Workspace(device)
         self.ws_verify = Workspace(device)
         self.attn_out = None
+        self.sel = None
 
     def draft(self, draft_logits):
         draft_topk(draft_logits, self.k, self.tok, self.conf, self.stats, self.ws_draft, self.status)
@@ -55,11 +56,19 @@ class TreeStep:
         tree_attn(q, k_cache, v_cache, kv_len, k_tree, v_tree, self.tree["mask"], scale,
                   self.attn_out, self.lse, self.ws_attn, self.status)
 
-    def attend_kv8(self, cache, layer, q, k_tree, v_tree, scale=None):
+    def attend_kv8(self, cache, layer, q, k_tree, v_tree, scale=None, top=None, first=1, last=1):
         """attend() over one layer of a KV8Cache (cache.py): the prefix in
-        e4m3 pages.  Returns (out, lse)."""
+        e4m3 pages, or (top given, a cache with bounds) the first `first`, the
+        last `last` and the best other pages of it, `top` in all, that each
+        node and KV head selects.  Returns (out, lse)."""
         if self.attn_out is None or self.attn_out.shape != q.shape or self.attn_out.dtype != q.dtype:
             self.attn_out = torch.empty_like(q)
+        if top is not None:
+            shape = (self.B, self.m + 1, self.Hkv, top)
+            if self.sel is None or self.sel.shape != shape:
+                self.sel = torch.empty(shape, dtype=torch.int32, device=q.device)
+            cache.select(layer, q, top, first, last, out=self.sel)
+            return cache.attend_pages(layer, q, k_tree, v_tree, self.tree["mask"], self.sel, scale, self.attn_out, self.lse)
         return cache.attend(layer, q, k_tree, v_tree, self.tree["mask"], scale, self.attn_out, self.lse)
 
     def commit_kv8(self, cache, k_trees, v_trees):
