@@ -62,7 +62,7 @@ cudaError_t launch_qk_norm_rope(const void *q, const void *k, const void *v, int
                                 int dh, int64_t ld_q, int64_t ld_k, int64_t ld_v, const void *q_weight,
                                 const void *k_weight, float weight_offset, float eps, const double *inv_freq,
                                 int rot_dim, int interleaved, float factor, const int32_t *pos_base,
-                                const int32_t *pos_off, int shift, void *q_out, void *k_tree, void *v_tree,
+                                const int32_t *pos_off, int shift, void *q_out, void *k_tree, void *v_tree, int num_sms,
                                 cudaStream_t st);
 // kv8_bounds.cu
 cudaError_t launch_kv8_bounds(const uint8_t *k_pages, const int32_t *block_table, int max_pages, int page_size,
@@ -450,11 +450,12 @@ int eagle_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, i
   constexpr float kMax = std::numeric_limits<float>::max();  // no NaN, no infinity
   if (!(eps > 0.f && eps <= kMax) || !(weight_offset >= -kMax && weight_offset <= kMax)) return EAGLE_ERR_INVALID;
   if (!aligned16(q_weight) || !aligned16(k_weight)) return EAGLE_ERR_INVALID;
-  // a CTA takes eight heads or more: the grid stays below 2^31
-  if (static_cast<int64_t>(B) * n * (static_cast<int64_t>(Hq) + 2ll * Hkv) > (1ll << 33)) return EAGLE_ERR_UNSUPPORTED;
+  // heads are numbered in 31 bits
+  if (static_cast<int64_t>(B) * n * (static_cast<int64_t>(Hq) + 2ll * Hkv) > (1ll << 30)) return EAGLE_ERR_UNSUPPORTED;
   return from_cuda(launch_qk_norm_rope(q, k, v, dtype, B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v, q_weight, k_weight,
                                        weight_offset, eps, inv_freq, rot_dim, interleaved, factor, pos_base, pos_off,
-                                       shift, q_out, k_tree, v_tree, reinterpret_cast<cudaStream_t>(stream)));
+                                       shift, q_out, k_tree, v_tree, current_num_sms(),
+                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int eagle_rope_freqs(int rot_dim, double theta, int kind, double stretch, int orig_len, double low, double high,

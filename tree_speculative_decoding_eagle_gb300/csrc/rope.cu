@@ -26,7 +26,7 @@ constexpr int kRopeThreads = 256;
 
 // cos and sin of the node's angles into shared memory.
 __device__ __forceinline__ void node_turns(const RopeArgs &a, int pos, float2 *cs) {
-  for (int j = threadIdx.x; j < a.half; j += kRopeThreads) cs[j] = turn_of(a, pos, j);
+  for (int j = threadIdx.x; j < a.half; j += kRopeThreads) cs[j] = turn_at(turn_step(a.inv_freq[j]), pos, a.factor);
 }
 
 // 16-byte vectors.  An item of a head is what one thread turns: two vectors half

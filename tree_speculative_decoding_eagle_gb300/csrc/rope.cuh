@@ -16,15 +16,18 @@ struct RopeArgs {
   float factor;
 };
 
-// cos and sin (times the factor) of pair j at a position.
-__device__ __forceinline__ float2 turn_of(const RopeArgs &a, int pos, int j) {
-  double t = a.inv_freq[j] * 0.15915494309189533577;  // turns per position
+// A frequency as turns a position, in 64-bit fixed point.
+__device__ __forceinline__ uint64_t turn_step(double inv_freq) {
+  double t = inv_freq * 0.15915494309189533577;  // turns per position
   t -= rint(t);
-  const uint64_t inc = static_cast<uint64_t>(static_cast<int64_t>(t * 18446744073709551616.0));
-  const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * inc;
+  return static_cast<uint64_t>(static_cast<int64_t>(t * 18446744073709551616.0));
+}
+// cos and sin (times the factor) at a position.
+__device__ __forceinline__ float2 turn_at(uint64_t step, int pos, float factor) {
+  const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * step;
   float sn, c;
   sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &sn, &c);
-  return make_float2(c * a.factor, sn * a.factor);
+  return make_float2(c * factor, sn * factor);
 }
 __device__ __forceinline__ int position_of(const RopeArgs &a, int node, int b, int i) {
   return (a.pos_base ? a.pos_base[b] : 0) + (a.pos_off ? a.pos_off[node] : i) + a.shift;
