@@ -9,15 +9,16 @@
 // whose largest number lies in (224, 448].
 //
 // What bounds it: HBM for prompts (one byte read an element), latency for single
-// tokens.  A warp takes a page of a head: a lane looks after four neighbouring
-// columns (two f16 pairs each way, e4m3 to f16 being exact), so a row is one
-// coalesced request and nothing passes between lanes but where 16 lanes hold a row
-// of 64; sixteen requests a lane are in flight.
+// tokens.  A warp takes a page of a head: a lane looks after 16 neighbouring columns
+// of every fourth (or eighth) row, 16 bytes a request with up to 16 requests in
+// flight, as f16 pairs (e4m3 to f16 is exact, and f16 has packed minima and maxima);
+// the lanes of a column then hand their results down, halving the columns that a
+// lane still looks after at each step.
 #include "kv8.cuh"
 
 namespace eagle {
 
-constexpr int kBoundWarps = 4, kBoundAhead = 16;
+constexpr int kBoundWarps = 4;
 
 struct BoundArgs {
   const uint8_t *k_pages;
@@ -38,7 +39,8 @@ __device__ __forceinline__ uint32_t half2_to_e4m3(uint32_t w) {
 
 template <int DH>
 __global__ void __launch_bounds__(kBoundWarps * 32) kv8_bounds_kernel(BoundArgs a) {
-  constexpr int LANES = DH / 4, ROWS = 32 / LANES;  // lanes a row, rows a request
+  constexpr int LANES = DH / 16, ROWS = 32 / LANES;  // lanes a row, rows a request
+  constexpr int AHEAD = 64 / ROWS;                   // requests in flight: 64 rows
   const int b = blockIdx.y, lane = threadIdx.x & 31, col = lane % LANES, sub = lane / LANES;
   const int P = 1 << a.log_page;
   pdl_wait();
@@ -58,49 +60,56 @@ __global__ void __launch_bounds__(kBoundWarps * 32) kv8_bounds_kernel(BoundArgs 
     }
     const int rows = min(P, L - (lp << a.log_page));
     const int64_t block = static_cast<int64_t>(page) * a.Hkv + g;
-    const uint8_t *src = a.k_pages + (block << a.log_page) * DH + col * 4;
-    __half2 hi[2], lo[2];
-    hi[0] = hi[1] = as_half2(0xfc00fc00u);  // -inf
-    lo[0] = lo[1] = as_half2(0x7c007c00u);
-    const auto take = [&](uint32_t w) {
+    const uint8_t *src = a.k_pages + (block << a.log_page) * DH + col * 16;
+    uint32_t hi[8], lo[8];  // columns 2i, 2i + 1 of the lane's 16
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const __half2 x = as_half2(e4m3_to_half2(i ? w >> 16 : w & 0xffffu));
-        hi[i] = __hmax2_nan(hi[i], x);
-        lo[i] = __hmin2_nan(lo[i], x);
-      }
-    };
-    for (int r0 = sub; r0 < rows; r0 += ROWS * kBoundAhead) {
-      uint32_t w[kBoundAhead];
-#pragma unroll
-      for (int i = 0; i < kBoundAhead; ++i) {  // past the last row: the last one again
-        const int r = min(r0 + i * ROWS, rows - 1);
-        w[i] = __ldg(reinterpret_cast<const uint32_t *>(src + static_cast<int64_t>(r) * DH));
-      }
-#pragma unroll
-      for (int i = 0; i < kBoundAhead; ++i) take(w[i]);
+    for (int i = 0; i < 8; ++i) {
+      hi[i] = 0xfc00fc00u;  // -inf
+      lo[i] = 0x7c007c00u;
     }
-    if constexpr (ROWS == 2) {
+    for (int r0 = 0; r0 < rows; r0 += ROWS * AHEAD) {
+      uint4 x[AHEAD];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        hi[i] = __hmax2_nan(hi[i], as_half2(__shfl_xor_sync(0xffffffffu, as_u32(hi[i]), 16)));
-        lo[i] = __hmin2_nan(lo[i], as_half2(__shfl_xor_sync(0xffffffffu, as_u32(lo[i]), 16)));
+      for (int i = 0; i < AHEAD; ++i)  // in the last request, past the last row: that row again
+        if (r0 + i * ROWS < rows) x[i] = ld_stream16(src + static_cast<int64_t>(min(r0 + i * ROWS + sub, rows - 1)) * DH);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (r0 + i * ROWS >= rows) break;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t v = e4m3_to_half2(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
+          hi[j] = as_u32(__hmax2_nan(as_half2(hi[j]), as_half2(v)));
+          lo[j] = as_u32(__hmin2_nan(as_half2(lo[j]), as_half2(v)));
+        }
       }
     }
-    uint32_t out[2] = {0, 0};  // lo, hi
+    // Lanes sub and sub ^ 1, ^ 2 (and ^ 4) share the columns: each step a lane keeps
+    // half of those it has and hands the other half over.
+    int c0 = 0;  // the first pair that this lane still looks after
+#pragma unroll
+    for (int o = 1, keep = 4; o < ROWS; o *= 2, keep /= 2) {
+      const bool upper = sub & o;
+#pragma unroll
+      for (int i = 0; i < keep; ++i) {
+        const uint32_t gh = upper ? hi[i] : hi[i + keep], gl = upper ? lo[i] : lo[i + keep];
+        const uint32_t mh = upper ? hi[i + keep] : hi[i], ml = upper ? lo[i + keep] : lo[i];
+        hi[i] = as_u32(__hmax2_nan(as_half2(mh), as_half2(__shfl_xor_sync(0xffffffffu, gh, o * LANES))));
+        lo[i] = as_u32(__hmin2_nan(as_half2(ml), as_half2(__shfl_xor_sync(0xffffffffu, gl, o * LANES))));
+      }
+      if (upper) c0 += keep;
+    }
+    constexpr int KEPT = 8 / ROWS;  // pairs a lane ends up with: two (DH = 128) or one
     const __half2 two = __float2half2_rn(2.f), half = __float2half2_rn(0.5f);
+    uint16_t *dst = reinterpret_cast<uint16_t *>(a.bounds + block * 2 * DH) + col * 8 + c0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < KEPT; ++i) {
       // a NaN among the rows: as wide as it can be
-      const uint32_t bad = __vcmpgtu2(as_u32(hi[i]) & 0x7fff7fffu, 0x7c007c00u);
-      const uint32_t l = as_u32(__hmul2(h2floor(__hmul2(lo[i], two)), half)), h = as_u32(__hmul2(h2ceil(__hmul2(hi[i], two)), half));
-      out[0] |= half2_to_e4m3((l & ~bad) | (0xdf00df00u & bad)) << (16 * i);  // -448
-      out[1] |= half2_to_e4m3((h & ~bad) | (0x5f005f00u & bad)) << (16 * i);
-    }
-    if (sub == 0) {
-      uint32_t *dst = reinterpret_cast<uint32_t *>(a.bounds + block * 2 * DH) + col;
-      dst[0] = out[0];
-      dst[LANES] = out[1];
+      const uint32_t bad = __vcmpgtu2(hi[i] & 0x7fff7fffu, 0x7c007c00u);
+      const uint32_t l = as_u32(__hmul2(h2floor(__hmul2(as_half2(lo[i]), two)), half));
+      const uint32_t h = as_u32(__hmul2(h2ceil(__hmul2(as_half2(hi[i]), two)), half));
+      dst[i] = static_cast<uint16_t>(half2_to_e4m3((l & ~bad) | (0xdf00df00u & bad)));           // -448
+      dst[DH / 2 + i] = static_cast<uint16_t>(half2_to_e4m3((h & ~bad) | (0x5f005f00u & bad)));
     }
   }
 }
