@@ -124,6 +124,21 @@ def test_the_largest_sums_are_exact():
         c.check(9, 0, 0)
 
 
+def test_the_largest_sums_are_exact_for_many_rows():
+    """The same on the tiles for many rows: odd multiples of half a unit at the top of the range."""
+    for dh in (64, 128):
+        c = Case([300 * 16], 40, 4, 1, dh, 16, spread=0)
+        rng = np.random.default_rng(dh)
+        c.q[:] = 127.5
+        c.q[:, 1::2, :, 1::2] *= -1
+        c.q[..., 7] = 1.0
+        c.codes[..., 0, :] = kv8.encode(np.full(c.codes[..., 0, :].shape, -448.0))
+        c.codes[..., 1, :] = kv8.encode(np.full(c.codes[..., 1, :].shape, 448.0))
+        c.codes[..., 1, 7] = kv8.encode(rng.integers(0, 8, c.codes[..., 1, 7].shape) * 0.5)
+        c.check(9, 0, 0)
+        c.check(299, 0, 0)
+
+
 def test_magnitudes_and_odd_queries():
     c = Case([50 * 16], 8, 4, 2, 64, 16, spread=64)
     c.scale[0], c.scale[1] = 2.0 ** 64, 2.0 ** -64

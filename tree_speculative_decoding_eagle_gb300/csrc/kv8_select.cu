@@ -19,22 +19,9 @@
 // converted, because the order of the columns in the sum is free.  Choice: a row's
 // scores as ordered 32-bit keys in registers, bisection on the key that `top` of
 // them reach, ties to the lower pages, one prefix sum for the places.
-#include "kv8.cuh"
+#include "kv8_select.cuh"
 
 namespace eagle {
-
-struct SelectArgs {
-  const __nv_bfloat16 *q;
-  const uint8_t *bounds;
-  const float *k_scale;
-  const int32_t *block_table, *kv_len;
-  float *scores;  // workspace [B * n * Hkv, stride]
-  int32_t *sel;
-  float *sel_score;
-  int32_t *status;
-  int B, n, Hq, Hkv, G, log_g;  // 2^log_g: heads of a KV head, padded
-  int log_page, max_pages, num_pages, stride, top, first, last;
-};
 
 constexpr int kScoreWarps = 4;
 
@@ -44,34 +31,19 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Pages of a request's prefix.
-__device__ __forceinline__ int live_pages(const SelectArgs &a, int b) {
-  const int64_t L = min(static_cast<int64_t>(max(a.kv_len[b], 0)), static_cast<int64_t>(a.max_pages) << a.log_page);
-  return static_cast<int>((L + (1 << a.log_page) - 1) >> a.log_page);
-}
-__device__ __forceinline__ float finite_or_zero(float x) { return fabsf(x) <= 3.402823466e38f ? x : 0.f; }
-// Two of a row's numbers as whole numbers in f16.
-__device__ __forceinline__ uint32_t whole_half2(uint32_t w, float f) {
-  const float lo = rintf(finite_or_zero(bf16_lo(w)) * f), hi = rintf(finite_or_zero(bf16_hi(w)) * f);
-  const __half2 h = __floats2half2_rn(fminf(fmaxf(lo, -128.f), 128.f), fminf(fmaxf(hi, -128.f), 128.f));
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t half2_max0(uint32_t w) {
-  const __half2 h = __hmax2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(0.f));
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t half2_min0(uint32_t w) {
-  const __half2 h = __hmin2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(0.f));
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Scores of a tile of rows against the pages tile0.., eight a step.  blockIdx.x:
+// Scores of a tile of rows against the pages of a chunk, eight a step.  blockIdx.x:
 // chunk of pages, blockIdx.y: (sequence, KV head), blockIdx.z: tiles of rows.
 // Row r of tile T of 16: padded row T * 16 + r = node << log_g | head.  With more
 // than 16 heads a node's two tiles belong to one warp (MT = 2).
+// The bounds come through a ring of asynchronous copies, kStages steps ahead; a lane
+// reads back what it copied itself, so no lane waits for another.  Page numbers and
+// scales are read for four steps (a batch) at a time, a batch ahead of the copies.
+constexpr int kStages = 4;
+
 template <int DH, int MT>
 __global__ void __launch_bounds__(kScoreWarps * 32) kv8_score_kernel(SelectArgs a, int row_warps, int pages_per_cta) {
   constexpr int STEPS = DH / 16, NV = DH / 64;  // MMA steps a bound, 16-byte pieces of a lane
+  __shared__ uint4 ring[kScoreWarps][kStages][2 * NV][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
   const int bg = blockIdx.y, b = bg / a.Hkv, g = bg % a.Hkv;
   const int rw = warp % row_warps, pw = warp / row_warps, page_warps = kScoreWarps / row_warps;
@@ -80,7 +52,42 @@ __global__ void __launch_bounds__(kScoreWarps * 32) kv8_score_kernel(SelectArgs 
   pdl_wait();
   const int np = live_pages(a, b);
   const int p_begin = blockIdx.x * pages_per_cta, p_end = min(np, p_begin + pages_per_cta);
-  if (p_begin >= p_end || tile * 16 >= rows) return;
+  const int p_first = p_begin + pw * 8, p_step = page_warps * 8;  // this warp's steps
+  if (p_first >= p_end || tile * 16 >= rows) return;
+  const int steps = (p_end - p_first + p_step - 1) / p_step;
+
+  // lane 8 s + i of batch k looks after page i of step 4 k + s: its block of the pool
+  const int32_t *table = a.block_table + static_cast<int64_t>(b) * a.max_pages;
+  const auto block_at = [&](int batch) {
+    const int p = p_first + (batch * 4 + (lane >> 3)) * p_step + (lane & 7);
+    int page = 0;
+    if (p < p_end) {
+      page = table[p];
+      if (page < 0 || page >= a.num_pages) {
+        report(a.status, EAGLE_ERR_INVALID);  // outside the pool: read page 0
+        page = 0;
+      }
+    }
+    return page * a.Hkv + g;  // num_pages * Hkv fits 31 bits
+  };
+  uint4(*mine)[2 * NV][32] = ring[warp];
+  const auto request = [&](int step, int blocks) {
+    const int block = __shfl_sync(0xffffffffu, blocks, (step & 3) * 8 + gr);
+    if (step < steps) {
+      const uint8_t *src = a.bounds + static_cast<int64_t>(block) * 2 * DH + t * (DH / 4);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        cp_async16(&mine[step % kStages][i][lane], src + i * 16);
+        cp_async16(&mine[step % kStages][NV + i][lane], src + DH + i * 16);
+      }
+    }
+    cp_async_commit();
+  };
+  const int block0 = block_at(0);
+  int block = block_at(1), block_ahead = block_at(2);  // of the next batch, and of the one after
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) request(s, block0);
+  float ps = a.k_scale[block0], ps_next = a.k_scale[block];
 
   uint32_t qp[MT][STEPS][4], qn[MT][STEPS][4];
   float row_scale[MT][2];
@@ -98,15 +105,11 @@ __global__ void __launch_bounds__(kScoreWarps * 32) kv8_score_kernel(SelectArgs 
         if (there)
           x[c] = __ldg(reinterpret_cast<const uint4 *>(
               a.q + ((static_cast<int64_t>(b) * a.n + node) * a.Hq + g * a.G + h) * DH + t * (DH / 4) + c * 8));
-        float f[8];
-        VecTraits<__nv_bfloat16>::unpack(x[c], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(finite_or_zero(f[e])));
+        amax = fmaxf(amax, finite_amax8(x[c]));
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // amax / 2^e in [64, 128)
-      const int e = amax > 0.f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 6, -32), 32) : 0;
+      const int e = whole_exponent(amax);
       const float f = exponent_scale(-e);
       row_scale[m][r] = exponent_scale(e);
 #pragma unroll
@@ -120,26 +123,26 @@ __global__ void __launch_bounds__(kScoreWarps * 32) kv8_score_kernel(SelectArgs 
       }
     }
 
-  const int32_t *table = a.block_table + static_cast<int64_t>(b) * a.max_pages;
-  for (int p0 = p_begin + pw * 8; p0 < p_end; p0 += page_warps * 8) {
-    // lane (gr, t): columns t * DH/4 .. of page p0 + gr
-    int page = p0 + gr < p_end ? table[p0 + gr] : 0;
-    if (page < 0 || page >= a.num_pages) {
-      report(a.status, EAGLE_ERR_INVALID);  // outside the pool: read page 0
-      page = 0;
+  for (int step = 0; step < steps; ++step) {
+    if (step && (step & 3) == 0) {  // the next batch
+      ps = ps_next;
+      block = block_ahead;
+      ps_next = a.k_scale[block];
+      block_ahead = block_at((step >> 2) + 2);
     }
-    const int64_t block = static_cast<int64_t>(page) * a.Hkv + g;
-    const uint8_t *src = a.bounds + block * 2 * DH + t * (DH / 4);
+    cp_async_wait<kStages - 1>();
+    const int p0 = p_first + step * p_step;
     uint4 lo[NV], hi[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      lo[i] = __ldg(reinterpret_cast<const uint4 *>(src + i * 16));
-      hi[i] = __ldg(reinterpret_cast<const uint4 *>(src + DH + i * 16));
+      lo[i] = mine[step % kStages][i][lane];
+      hi[i] = mine[step % kStages][NV + i][lane];
     }
-    const float ps = exponent_scale(scale_exponent(a.k_scale[block]));
-    float c[MT][4];
+    float c[MT][4], cn[MT][4];  // two chains of MMAs
 #pragma unroll
-    for (int m = 0; m < MT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[m][e] = cn[m][e] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const uint32_t l[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w}, h[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
@@ -150,17 +153,21 @@ __global__ void __launch_bounds__(kScoreWarps * 32) kv8_score_kernel(SelectArgs 
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           mma_f16(c[m], qp[m][i * 4 + w], h0, h1);
-          mma_f16(c[m], qn[m][i * 4 + w], l0, l1);
+          mma_f16(cn[m], qn[m][i * 4 + w], l0, l1);
         }
       }
     }
+    request(step + kStages, block);  // into the stage just read: kStages is a batch
     // columns 2t, 2t + 1 of the result are pages p0 + 2t, p0 + 2t + 1
-    const float s0 = __shfl_sync(0xffffffffu, ps, 8 * t), s1 = __shfl_sync(0xffffffffu, ps, 8 * t + 4);
+    const float scale = exponent_scale(scale_exponent(ps));
+    const float s0 = __shfl_sync(0xffffffffu, scale, (step & 3) * 8 + 2 * t), s1 = __shfl_sync(0xffffffffu, scale, (step & 3) * 8 + 2 * t + 1);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int h = ((tile + m) * 16 + gr + 8 * r) & ((1 << a.log_g) - 1);
+        c[m][2 * r] += cn[m][2 * r];
+        c[m][2 * r + 1] += cn[m][2 * r + 1];
         c[m][2 * r] = h < a.G ? c[m][2 * r] * row_scale[m][r] * s0 : -INFINITY;
         c[m][2 * r + 1] = h < a.G ? c[m][2 * r + 1] * row_scale[m][r] * s1 : -INFINITY;
         for (int o = 0; o < min(a.log_g, 3); ++o) {  // the heads of a node: rows gr that share its upper bits
@@ -338,6 +345,13 @@ static cudaError_t launch_choose(const SelectArgs &a, cudaStream_t st) {
   return launch_chained(kv8_choose_kernel<T, V>, grid, dim3(THREADS), 0, st, a, rows);
 }
 
+// kv8_score_tc.cu
+cudaError_t launch_kv8_score_tc(const SelectArgs &a, int dh, int num_sms, cudaStream_t st);
+
+// Padded rows of a sequence and KV head from which the scores are computed on
+// tcgen05 tiles of 128 pages by up to 256 rows.
+constexpr int kTileRows = 64;
+
 cudaError_t launch_kv8_select(const void *q, const uint8_t *bounds, const float *k_scale, const int32_t *block_table,
                               int max_pages, int page_size, int num_pages, const int32_t *kv_len, int B, int n, int Hq,
                               int Hkv, int dh, int top, int first, int last, int32_t *sel, float *score, void *ws,
@@ -349,7 +363,8 @@ cudaError_t launch_kv8_select(const void *q, const uint8_t *bounds, const float 
                         reinterpret_cast<float *>(ws), sel, score, status, B, n, Hq, Hkv, Hq / Hkv, log_g,
                         log_page, max_pages, num_pages, score_stride(max_pages), top, first, last};
   cudaError_t e;
-  if (dh == 128) e = log_g == 5 ? launch_score<128, 2>(a, num_sms, st) : launch_score<128, 1>(a, num_sms, st);
+  if ((n << log_g) >= kTileRows) e = launch_kv8_score_tc(a, dh, num_sms, st);
+  else if (dh == 128) e = log_g == 5 ? launch_score<128, 2>(a, num_sms, st) : launch_score<128, 1>(a, num_sms, st);
   else e = log_g == 5 ? launch_score<64, 2>(a, num_sms, st) : launch_score<64, 1>(a, num_sms, st);
   if (e != cudaSuccess) return e;
   if (max_pages <= 512) return launch_choose<32, 16>(a, st);
