@@ -836,7 +836,7 @@ int eagle_kv8_bounds(const uint8_t *k_pages, const int32_t *block_table,
  *              (page 0's bounds are read in its place)
  * Workspace: the scores of all pages, one float for each node, KV head and page.
  * Limits: dtype EAGLE_BF16, dh in {64, 128}, Hq/Hkv <= 32, max_pages and top <=
- * 16384, B*Hkv <= 65535, B*n*Hkv <= 2^24, num_pages*Hkv < 2^31 (else
+ * 16384, B*Hkv <= 65535, B*n*Hkv <= 2^24, num_pages*Hkv < 2^30 (else
  * EAGLE_ERR_UNSUPPORTED); 1 <= n <= 4096; 0 <= first, last; first + last <= top;
  * page rules as for eagle_tree_attn_paged; workspace 16-byte aligned. */
 size_t eagle_kv8_select_workspace_size(int dtype, int B, int n, int Hq, int Hkv,

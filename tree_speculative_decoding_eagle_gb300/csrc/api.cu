@@ -600,7 +600,7 @@ int eagle_kv8_select(const void *q, int dtype, const uint8_t *k_bounds, const fl
   const int rc = check_nodes(B, n, Hq, Hkv, dh);
   if (rc != EAGLE_OK) return rc;
   if (dtype != EAGLE_BF16 || max_pages > kMaxSelectPages || top > kMaxSelectPages ||
-      static_cast<int64_t>(num_pages) * Hkv > INT32_MAX)
+      static_cast<int64_t>(num_pages) * Hkv > (1 << 30) - 1)  // lines of 128 bytes are numbered in 31 bits
     return EAGLE_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_bounds) || !aligned16(workspace)) return EAGLE_ERR_INVALID;
   if (!workspace || workspace_bytes < kv8_select_workspace_bytes(B, n, Hkv, max_pages)) return EAGLE_ERR_WORKSPACE;

@@ -36,4 +36,10 @@ __device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t pair) {
   return r;
 }
 
+// Largest magnitude of eight packed bf16 numbers.
+__device__ __forceinline__ float amax8(const uint4 &v) {
+  const uint4 a = make_uint4(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+  return vec_max<__nv_bfloat16>(a);
+}
+
 }  // namespace eagle

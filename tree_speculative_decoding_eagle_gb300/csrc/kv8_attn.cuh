@@ -42,12 +42,6 @@ __device__ __forceinline__ uint32_t bf16x2_to_half2(uint32_t w, float f) {
   const __half2 h = __floats2half2_rn(bf16_lo(w) * f, bf16_hi(w) * f);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-// Largest magnitude of eight packed bf16 numbers.
-__device__ __forceinline__ float amax8(const uint4 &v) {
-  const uint4 a = make_uint4(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
-  return vec_max<__nv_bfloat16>(a);
-}
-
 // Columns 4c..4c+3 of query row rho of (b, g): out = o / l, lse from (m, l).
 template <int DH>
 __device__ __forceinline__ void kv8_write_out(const Kv8Args &a, int bg, int rho, int c, float4 o, float m, float l) {

@@ -10,8 +10,8 @@
 //
 // What bounds it: HBM for prompts (one byte read an element), latency for single
 // tokens.  A warp takes a page of a head: a lane looks after 16 neighbouring columns
-// of every fourth (or eighth) row, 16 bytes a request with up to 16 requests in
-// flight, as f16 pairs (e4m3 to f16 is exact, and f16 has packed minima and maxima);
+// of every fourth (or eighth) row, 16 bytes a request with up to eight requests
+// in flight, as f16 pairs (e4m3 to f16 is exact, and f16 has packed minima and maxima);
 // the lanes of a column then hand their results down, halving the columns that a
 // lane still looks after at each step.
 #include "kv8.cuh"
@@ -38,9 +38,9 @@ __device__ __forceinline__ uint32_t half2_to_e4m3(uint32_t w) {
 }
 
 template <int DH>
-__global__ void __launch_bounds__(kBoundWarps * 32) kv8_bounds_kernel(BoundArgs a) {
+__global__ void __launch_bounds__(kBoundWarps * 32, 8) kv8_bounds_kernel(BoundArgs a) {
   constexpr int LANES = DH / 16, ROWS = 32 / LANES;  // lanes a row, rows a request
-  constexpr int AHEAD = 64 / ROWS;                   // requests in flight: 64 rows
+  constexpr int AHEAD = 32 / ROWS;                   // requests in flight: 32 rows
   const int b = blockIdx.y, lane = threadIdx.x & 31, col = lane % LANES, sub = lane / LANES;
   const int P = 1 << a.log_page;
   pdl_wait();

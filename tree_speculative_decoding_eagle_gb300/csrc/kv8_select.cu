@@ -13,188 +13,13 @@
 // decoding token by token with selected pages would have produced.
 // The node's score of a page is the largest over the heads that share the KV head.
 //
-// Two kernels.  Scores: a tile of 16 rows (nodes by heads, the heads padded to a
-// power of two) against 8 pages a step on warp-level f16 MMAs, q' and the bounds
-// being exact in f16; a lane's 16-byte pieces of the bounds are B fragments once
-// converted, because the order of the columns in the sum is free.  Choice: a row's
-// scores as ordered 32-bit keys in registers, bisection on the key that `top` of
-// them reach, ties to the lower pages, one prefix sum for the places.
+// Two kernels.  Scores: kv8_score.cu.  Choice (here): a row's scores as ordered
+// 32-bit keys in registers, a search for the greatest key that `top` of them reach
+// (by interpolation on the counts, every third step by halving), ties to the lower
+// pages, one prefix sum for the places.
 #include "kv8_select.cuh"
 
 namespace eagle {
-
-constexpr int kScoreWarps = 4;
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Scores of a tile of rows against the pages of a chunk, eight a step.  blockIdx.x:
-// chunk of pages, blockIdx.y: (sequence, KV head), blockIdx.z: tiles of rows.
-// Row r of tile T of 16: padded row T * 16 + r = node << log_g | head.  With more
-// than 16 heads a node's two tiles belong to one warp (MT = 2).
-// The bounds come through a ring of asynchronous copies, kStages steps ahead; a lane
-// reads back what it copied itself, so no lane waits for another.  Page numbers and
-// scales are read for four steps (a batch) at a time, a batch ahead of the copies.
-constexpr int kStages = 4;
-
-template <int DH, int MT>
-__global__ void __launch_bounds__(kScoreWarps * 32) kv8_score_kernel(SelectArgs a, int row_warps, int pages_per_cta) {
-  constexpr int STEPS = DH / 16, NV = DH / 64;  // MMA steps a bound, 16-byte pieces of a lane
-  __shared__ uint4 ring[kScoreWarps][kStages][2 * NV][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
-  const int bg = blockIdx.y, b = bg / a.Hkv, g = bg % a.Hkv;
-  const int rw = warp % row_warps, pw = warp / row_warps, page_warps = kScoreWarps / row_warps;
-  const int tile = (blockIdx.z * row_warps + rw) * MT;
-  const int rows = a.n << a.log_g;
-  pdl_wait();
-  const int np = live_pages(a, b);
-  const int p_begin = blockIdx.x * pages_per_cta, p_end = min(np, p_begin + pages_per_cta);
-  const int p_first = p_begin + pw * 8, p_step = page_warps * 8;  // this warp's steps
-  if (p_first >= p_end || tile * 16 >= rows) return;
-  const int steps = (p_end - p_first + p_step - 1) / p_step;
-
-  // lane 8 s + i of batch k looks after page i of step 4 k + s: its block of the pool
-  const int32_t *table = a.block_table + static_cast<int64_t>(b) * a.max_pages;
-  const auto block_at = [&](int batch) {
-    const int p = p_first + (batch * 4 + (lane >> 3)) * p_step + (lane & 7);
-    int page = 0;
-    if (p < p_end) {
-      page = table[p];
-      if (page < 0 || page >= a.num_pages) {
-        report(a.status, EAGLE_ERR_INVALID);  // outside the pool: read page 0
-        page = 0;
-      }
-    }
-    return page * a.Hkv + g;  // num_pages * Hkv fits 31 bits
-  };
-  uint4(*mine)[2 * NV][32] = ring[warp];
-  const auto request = [&](int step, int blocks) {
-    const int block = __shfl_sync(0xffffffffu, blocks, (step & 3) * 8 + gr);
-    if (step < steps) {
-      const uint8_t *src = a.bounds + static_cast<int64_t>(block) * 2 * DH + t * (DH / 4);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        cp_async16(&mine[step % kStages][i][lane], src + i * 16);
-        cp_async16(&mine[step % kStages][NV + i][lane], src + DH + i * 16);
-      }
-    }
-    cp_async_commit();
-  };
-  const int block0 = block_at(0);
-  int block = block_at(1), block_ahead = block_at(2);  // of the next batch, and of the one after
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) request(s, block0);
-  float ps = a.k_scale[block0], ps_next = a.k_scale[block];
-
-  uint32_t qp[MT][STEPS][4], qn[MT][STEPS][4];
-  float row_scale[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int rho = (tile + m) * 16 + gr + 8 * r, node = rho >> a.log_g, h = rho & ((1 << a.log_g) - 1);
-      const bool there = rho < rows && h < a.G;
-      uint4 x[DH / 32];
-      float amax = 0.f;
-#pragma unroll
-      for (int c = 0; c < DH / 32; ++c) {
-        x[c] = make_uint4(0, 0, 0, 0);
-        if (there)
-          x[c] = __ldg(reinterpret_cast<const uint4 *>(
-              a.q + ((static_cast<int64_t>(b) * a.n + node) * a.Hq + g * a.G + h) * DH + t * (DH / 4) + c * 8));
-        amax = fmaxf(amax, finite_amax8(x[c]));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int e = whole_exponent(amax);
-      const float f = exponent_scale(-e);
-      row_scale[m][r] = exponent_scale(e);
-#pragma unroll
-      for (int c = 0; c < DH / 32; ++c) {
-        const uint32_t w[4] = {whole_half2(x[c].x, f), whole_half2(x[c].y, f), whole_half2(x[c].z, f), whole_half2(x[c].w, f)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qp[m][2 * c + (i >> 1)][2 * (i & 1) + r] = half2_max0(w[i]);
-          qn[m][2 * c + (i >> 1)][2 * (i & 1) + r] = half2_min0(w[i]);
-        }
-      }
-    }
-
-  for (int step = 0; step < steps; ++step) {
-    if (step && (step & 3) == 0) {  // the next batch
-      ps = ps_next;
-      block = block_ahead;
-      ps_next = a.k_scale[block];
-      block_ahead = block_at((step >> 2) + 2);
-    }
-    cp_async_wait<kStages - 1>();
-    const int p0 = p_first + step * p_step;
-    uint4 lo[NV], hi[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      lo[i] = mine[step % kStages][i][lane];
-      hi[i] = mine[step % kStages][NV + i][lane];
-    }
-    float c[MT][4], cn[MT][4];  // two chains of MMAs
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[m][e] = cn[m][e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t l[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w}, h[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t h0 = e4m3_to_half2(h[w] & 0xffffu), h1 = e4m3_to_half2(h[w] >> 16);
-        const uint32_t l0 = e4m3_to_half2(l[w] & 0xffffu), l1 = e4m3_to_half2(l[w] >> 16);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma_f16(c[m], qp[m][i * 4 + w], h0, h1);
-          mma_f16(cn[m], qn[m][i * 4 + w], l0, l1);
-        }
-      }
-    }
-    request(step + kStages, block);  // into the stage just read: kStages is a batch
-    // columns 2t, 2t + 1 of the result are pages p0 + 2t, p0 + 2t + 1
-    const float scale = exponent_scale(scale_exponent(ps));
-    const float s0 = __shfl_sync(0xffffffffu, scale, (step & 3) * 8 + 2 * t), s1 = __shfl_sync(0xffffffffu, scale, (step & 3) * 8 + 2 * t + 1);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int h = ((tile + m) * 16 + gr + 8 * r) & ((1 << a.log_g) - 1);
-        c[m][2 * r] += cn[m][2 * r];
-        c[m][2 * r + 1] += cn[m][2 * r + 1];
-        c[m][2 * r] = h < a.G ? c[m][2 * r] * row_scale[m][r] * s0 : -INFINITY;
-        c[m][2 * r + 1] = h < a.G ? c[m][2 * r + 1] * row_scale[m][r] * s1 : -INFINITY;
-        for (int o = 0; o < min(a.log_g, 3); ++o) {  // the heads of a node: rows gr that share its upper bits
-          c[m][2 * r] = fmaxf(c[m][2 * r], __shfl_xor_sync(0xffffffffu, c[m][2 * r], 4 << o));
-          c[m][2 * r + 1] = fmaxf(c[m][2 * r + 1], __shfl_xor_sync(0xffffffffu, c[m][2 * r + 1], 4 << o));
-        }
-      }
-    if (a.log_g >= 4) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        c[m][0] = fmaxf(c[m][0], c[m][2]);
-        c[m][1] = fmaxf(c[m][1], c[m][3]);
-      }
-    }
-    if constexpr (MT == 2) {
-      c[0][0] = fmaxf(c[0][0], c[1][0]);
-      c[0][1] = fmaxf(c[0][1], c[1][1]);
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {  // a node's first row writes; MT = 2: one node a pair of tiles
-      const int rho = tile * 16 + gr + 8 * r;
-      if (rho >= rows || (rho & ((1 << a.log_g) - 1))) continue;
-      float *dst = a.scores + ((static_cast<int64_t>(b) * a.n + (rho >> a.log_g)) * a.Hkv + g) * a.stride + p0 + 2 * t;
-      *reinterpret_cast<float2 *>(dst) = make_float2(c[0][2 * r], c[0][2 * r + 1]);
-    }
-  }
-}
 
 // T threads (a power of two, 32 or more) a row, V neighbouring scores a thread.
 template <int T, int V>
@@ -251,14 +76,39 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArg
       lo = hi;
       reach = forced;
     } else {
-      while (reach != K && hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
+      // the least and the greatest key without the forced ones
+      uint32_t least = 0xffffffffu, most = 0u;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (key[j]) least = min(least, key[j]);
+        if (key[j] != 0xffffffffu) most = max(most, key[j]);
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if constexpr (WARPS > 1) {
+        __syncthreads();
+        if (lane == 0) { part[0][warp] = static_cast<int>(least); part[1][warp] = static_cast<int>(most); }
+        __syncthreads();
+        least = __reduce_min_sync(0xffffffffu, lane < WARPS ? static_cast<uint32_t>(part[0][lane]) : 0xffffffffu);
+        most = __reduce_max_sync(0xffffffffu, lane < WARPS ? static_cast<uint32_t>(part[1][lane]) : 0u);
+        __syncthreads();
+      }
+      lo = least;      // all reach it
+      hi = most + 1u;  // the forced ones alone do
+      int above = forced;
+      for (int step = 1; reach != K && hi - lo > 1; ++step) {
+        uint32_t mid = lo + (hi - lo) / 2;
+        if (step % 3) {
+          const float share = (static_cast<float>(reach - K) + 0.5f) / static_cast<float>(reach - above);
+          mid = min(max(lo + static_cast<uint32_t>(static_cast<float>(hi - lo) * share), lo + 1), hi - 1);
+        }
         const int c = count(mid);
         if (c >= K) {
           lo = mid;
           reach = c;
         } else {
           hi = mid;
+          above = c;
         }
       }
     }
@@ -321,22 +171,6 @@ size_t kv8_select_workspace_bytes(int B, int n, int Hkv, int max_pages) {
   return static_cast<size_t>(B) * n * Hkv * score_stride(max_pages) * sizeof(float);
 }
 
-template <int DH, int MT>
-static cudaError_t launch_score(const SelectArgs &a, int num_sms, cudaStream_t st) {
-  // Row tiles over a CTA's warps first, so that they share the bounds in L1; what
-  // warps are left split the pages.  Pages are cut into chunks until every SM has
-  // eight CTAs, a chunk being at least one step of each warp.
-  const int tiles = ((a.n << a.log_g) + 16 * MT - 1) / (16 * MT);
-  int row_warps = 1;
-  while (row_warps < kScoreWarps && row_warps < tiles) row_warps *= 2;
-  const int z = (tiles + row_warps - 1) / row_warps, step = 8 * (kScoreWarps / row_warps);
-  const int64_t base = static_cast<int64_t>(a.B) * a.Hkv * z, want = (8ll * num_sms + base - 1) / base;
-  const int most = (a.max_pages + step - 1) / step, chunks = static_cast<int>(want < most ? want : most);
-  const int per = ((a.max_pages + chunks - 1) / chunks + step - 1) / step * step;
-  const dim3 grid((a.max_pages + per - 1) / per, a.B * a.Hkv, z);
-  return launch_chained(kv8_score_kernel<DH, MT>, grid, dim3(kScoreWarps * 32), 0, st, a, row_warps, per);
-}
-
 template <int T, int V>
 static cudaError_t launch_choose(const SelectArgs &a, cudaStream_t st) {
   constexpr int THREADS = T < 128 ? 128 : T;
@@ -345,12 +179,8 @@ static cudaError_t launch_choose(const SelectArgs &a, cudaStream_t st) {
   return launch_chained(kv8_choose_kernel<T, V>, grid, dim3(THREADS), 0, st, a, rows);
 }
 
-// kv8_score_tc.cu
-cudaError_t launch_kv8_score_tc(const SelectArgs &a, int dh, int num_sms, cudaStream_t st);
-
-// Padded rows of a sequence and KV head from which the scores are computed on
-// tcgen05 tiles of 128 pages by up to 256 rows.
-constexpr int kTileRows = 64;
+// kv8_score.cu
+cudaError_t launch_kv8_score(const SelectArgs &a, int dh, int num_sms, cudaStream_t st);
 
 cudaError_t launch_kv8_select(const void *q, const uint8_t *bounds, const float *k_scale, const int32_t *block_table,
                               int max_pages, int page_size, int num_pages, const int32_t *kv_len, int B, int n, int Hq,
@@ -362,10 +192,7 @@ cudaError_t launch_kv8_select(const void *q, const uint8_t *bounds, const float 
   const SelectArgs a = {reinterpret_cast<const __nv_bfloat16 *>(q), bounds, k_scale, block_table, kv_len,
                         reinterpret_cast<float *>(ws), sel, score, status, B, n, Hq, Hkv, Hq / Hkv, log_g,
                         log_page, max_pages, num_pages, score_stride(max_pages), top, first, last};
-  cudaError_t e;
-  if ((n << log_g) >= kTileRows) e = launch_kv8_score_tc(a, dh, num_sms, st);
-  else if (dh == 128) e = log_g == 5 ? launch_score<128, 2>(a, num_sms, st) : launch_score<128, 1>(a, num_sms, st);
-  else e = log_g == 5 ? launch_score<64, 2>(a, num_sms, st) : launch_score<64, 1>(a, num_sms, st);
+  const cudaError_t e = launch_kv8_score(a, dh, num_sms, st);
   if (e != cudaSuccess) return e;
   if (max_pages <= 512) return launch_choose<32, 16>(a, st);
   if (max_pages <= 2048) return launch_choose<128, 16>(a, st);
