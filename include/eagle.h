@@ -860,8 +860,10 @@ int eagle_kv8_select(const void *q, int dtype, const uint8_t *k_bounds,
  *              does not ascend (the rows of that node and head are unspecified then;
  *              nothing is read out of range)
  * Everything else, what is rounded and a row without any key included, is as for
- * eagle_tree_attn_kv8; only the nodes that a row's own mask names share its
- * powers of two.
+ * eagle_tree_attn_kv8.  A NaN of the cache reaches the rows of the nodes that list
+ * its page; rows of other nodes of the same sequence and KV head may become NaN too,
+ * where they share a kernel's tile with those.
+ * Workspace: for many rows the union of the nodes' lists, and partial results.
  * Limits: those of eagle_tree_attn_kv8; Hq/Hkv <= 32 and B*n*Hkv <= 2^24 (else
  * EAGLE_ERR_UNSUPPORTED); top >= 1, top * page_size <= 2^24. */
 size_t eagle_tree_attn_kv8_pages_workspace_size(int dtype, int B, int n, int Hq,

@@ -109,6 +109,33 @@ def test_long_prefixes(n, Hq, Hkv, dh, top, L):
     Listed([L], n, Hq, Hkv, dh, 64, top, seed=L, full=True).run()
 
 
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("n,Hq", [(17, 4), (61, 2), (61, 16), (140, 4)])
+def test_trees_of_many_rows(P, dh, n, Hq):
+    """One, two and several groups of rows, whose nodes share lists."""
+    Listed([0, 1, 15, 17, 64, 129, 255, 700], n, Hq, 2, dh, P, 5, seed=P).run()
+    Listed([1500], n, Hq, 2, dh, P, 40, seed=P, full=True).run()
+
+
+def test_nodes_that_share_no_page():
+    """Each node lists pages of its own: the union is most of the prefix, in several words of bits."""
+    c = Listed([61 * 32 + 7], 61, 16, 2, 128, 16, 2, full=True)
+    c.sel[0] = (2 * torch.arange(61)[:, None, None] + torch.arange(2)).to(torch.int32).expand(61, 2, 2)
+    c.sel[0, 60, :, 1] = 122
+    c.run()
+    c.sel[0, 1::2] = -1
+    c.run()
+
+
+def test_one_head_of_a_tree_lists_nothing():
+    c = Listed([300, 40], 61, 16, 2, 64, 16, 4)
+    c.sel[:, :, 1] = -1
+    c.run()
+    c.sel[0] = -1
+    c.run()
+
+
 def test_many_sequences_of_all_lengths():
     g = np.random.default_rng(0)
     Listed(g.integers(0, 2000, 70).tolist(), 1, 16, 8, 128, 32, 9).run()
@@ -189,10 +216,11 @@ def test_a_nan_reaches_the_rows_that_list_it():
         c.pools[pool][0][int(c.table[0, 1]), 1, 3, 7] = code
 
 
-def test_lists_that_are_not_lists():
+@pytest.mark.parametrize("n,Hq", [(3, 4), (61, 8)])
+def test_lists_that_are_not_lists(n, Hq):
     """Pages past the prefix count for nothing, whatever else stands in the list
     stays in range; both are reported."""
-    c = Listed([100, 40], 3, 4, 2, 128, 16, 6)
+    c = Listed([100, 40], n, Hq, 2, 128, 16, 6)
     c.sel[:] = -1
     c.sel[0, ..., :3] = torch.tensor([0, 2, 6], dtype=torch.int32)
     want, want_lse = c.run()

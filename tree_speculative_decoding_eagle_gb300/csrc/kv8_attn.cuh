@@ -28,6 +28,13 @@ struct Kv8Args {
   int slot_rows;
 };
 
+// What the few-row kernel has beside for selected pages: B and n of Kv8Args are B *
+// nodes and 1 there.
+struct Kv8SelArgs : Kv8Args {
+  const int32_t *sel;
+  int top, nodes;
+};
+
 // 2^e in float32 for any int e that a sum of exponents can give, kept away
 // from 0 and infinity (0 * inf must not arise from finite inputs).
 __device__ __forceinline__ float pow2_clamped(int e) { return exponent_scale(min(max(e, -120), 120)); }

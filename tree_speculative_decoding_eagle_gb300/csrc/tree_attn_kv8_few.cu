@@ -52,12 +52,6 @@ __device__ __forceinline__ int o_chunk(int r, int c) {
   return r * (DH / 4) + (c ^ key);
 }
 
-// What the launch with selected pages has beside: B and n of Kv8Args are B * nodes
-// and 1 there.
-struct Kv8SelArgs : Kv8Args {
-  const int32_t *sel;
-  int top, nodes;
-};
 template <bool SEL> struct FewArgs { using type = Kv8Args; };
 template <> struct FewArgs<true> { using type = Kv8SelArgs; };
 
@@ -611,33 +605,9 @@ cudaError_t launch_tree_attn_kv8_few(Kv8Args a, const void *k_pages, const void 
   return launch_few<false>(a, k_pages, v_pages, dh, a.max_pages * a.page_size, ws, num_sms, st);
 }
 
-// Positions a node's list holds at most.
-static int listed_positions(int top, int max_pages, int page_size) { return (top < max_pages ? top : max_pages) * page_size; }
-
-size_t attn_kv8_pages_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int top, int max_pages, int page_size, int num_sms) {
-  return attn_kv8_few_workspace_bytes(B * n, 1, Hq, Hkv, dh, listed_positions(top, max_pages, page_size), num_sms);
-}
-
-cudaError_t launch_tree_attn_kv8_pages(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
-                                       const float *v_scale, const int32_t *block_table, int max_pages, int page_size,
-                                       int num_pages, const int32_t *kv_len, const void *k_tree, const void *v_tree,
-                                       const uint64_t *mask, const int32_t *sel, int top, int B, int n, int Hq, int Hkv,
-                                       int dh, float scale, void *out, float *lse, void *ws, int32_t *status, int num_sms,
-                                       cudaStream_t st) {
-  Kv8SelArgs a = {};
-  a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
-  a.k_tree = reinterpret_cast<const __nv_bfloat16 *>(k_tree);
-  a.v_tree = reinterpret_cast<const __nv_bfloat16 *>(v_tree);
-  a.k_scale = k_scale; a.v_scale = v_scale;
-  a.block_table = block_table; a.kv_len = kv_len; a.mask = mask;
-  a.B = B * n; a.n = 1; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.W = (n + 63) / 64;
-  a.page_size = page_size; a.max_pages = max_pages; a.num_pages = num_pages;
-  while ((1 << a.log_page) < page_size) ++a.log_page;
-  a.scale_log2 = scale * kLog2e;
-  a.out = reinterpret_cast<__nv_bfloat16 *>(out);
-  a.lse = lse; a.status = status;
-  a.sel = sel; a.top = top; a.nodes = n;
-  return launch_few<true>(a, k_pages, v_pages, dh, listed_positions(top, max_pages, page_size), ws, num_sms, st);
+cudaError_t launch_tree_attn_kv8_pages_few(const Kv8SelArgs &a, const void *k_pages, const void *v_pages, int dh, int Lmax, void *ws,
+                                           int num_sms, cudaStream_t st) {
+  return launch_few<true>(a, k_pages, v_pages, dh, Lmax, ws, num_sms, st);
 }
 
 }  // namespace eagle
