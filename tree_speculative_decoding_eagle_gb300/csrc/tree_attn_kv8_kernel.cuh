@@ -673,15 +673,21 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
         if (lane == 0) mbar_arrive(&s_free[t]);  // S has been read
         __syncwarp();  // or lane 0 would work on apart from the others
       };
+      // SEL: a warp none of whose rows counts a page of the tile has weights of zero
+      bool busy = warp_live;
+      if constexpr (SEL) {
+        const int pages = NK >> a.log_page;  // of a tile; 0: a page is longer
+        busy = warp_live && __any_sync(0xffffffffu, row_ok && (taken & ((2u << max(pages - 1, 0)) - 1u)));
+      }
       float tmax = -INFINITY;
-      if (NH == 2 && warp_live) {
+      if (NH == 2 && busy) {
         tmem_ld32x2(tS, sv[0], sv[1]);
         if (unlikely(!dense)) mask_half(0);
         tmax = half_max(0);
       }
-      if (warp_live) tmem_ld32x2(tS + 64 * (NH - 1), sv[0], sv[1]);
+      if (busy) tmem_ld32x2(tS + 64 * (NH - 1), sv[0], sv[1]);
       if (NH == 1) release();
-      if (warp_live) {
+      if (busy) {
         if (unlikely(!dense)) mask_half(NH - 1);
         tmax = fmaxf(tmax, half_max(NH - 1));
       }
@@ -732,11 +738,20 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
           sum = fmaf(a0 + a1, __uint_as_float(sc[0].x << 16), sum);
         }
       };
-      if (warp_live) exp_half(NH - 1);
+      if (busy) exp_half(NH - 1);
+      if constexpr (SEL) {
+        if (warp_live && !busy) {
+          float zeros[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) zeros[c] = 0.f;
+#pragma unroll
+          for (int c = 0; c < NK / 2; c += 16) tmem_st16_async(tP + c, zeros);
+        }
+      }
       if constexpr (NH == 2) {
-        if (warp_live) tmem_ld32x2(tS, sv[0], sv[1]);
+        if (busy) tmem_ld32x2(tS, sv[0], sv[1]);
         release();
-        if (warp_live) {
+        if (busy) {
           if (unlikely(!dense)) mask_half(0);
           exp_half(0);
         }
