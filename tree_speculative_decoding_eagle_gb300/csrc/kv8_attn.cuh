@@ -119,6 +119,19 @@ __global__ void __launch_bounds__(256) tree_attn_kv8_merge_kernel(Kv8Args a, int
   if (item < nr * NV) kv8_merge_item<DH>(a, bg, mg, MT, item / NV, item % NV);
 }
 
+// The merge where B * Hkv passes a grid's z dimension: the items of all (b, g) in one row.
+template <int DH>
+__global__ void __launch_bounds__(256) tree_attn_kv8_merge_flat_kernel(Kv8Args a) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int per = a.n * a.G * (DH / 4);
+  pdl_wait();  // the partial results come from the attention kernel
+  const int64_t bg = item / per;
+  if (bg < static_cast<int64_t>(a.B) * a.Hkv) {
+    const int at = static_cast<int>(item - bg * per);
+    kv8_merge_item<DH>(a, static_cast<int>(bg), 0, 1, at / (DH / 4), at % (DH / 4));
+  }
+}
+
 // A pool [num_pages * Hkv, page_size, dh] of bytes in boxes of page_box rows,
 // plain or with the swizzle of a row's width.  Three dimensions, so no
 // coordinate passes 32 bits however long the pool.

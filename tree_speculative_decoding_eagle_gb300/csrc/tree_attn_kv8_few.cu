@@ -537,19 +537,6 @@ size_t attn_kv8_few_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int L
   return p.S <= 1 ? 0 : static_cast<size_t>(B) * Hkv * p.S * ((rows + 7) / 8 * 8) * (dh + 2) * sizeof(float);
 }
 
-// The merge where B * Hkv passes a grid's z dimension: the items of all (b, g) in one row.
-template <int DH>
-__global__ void __launch_bounds__(256) tree_attn_kv8_merge_flat_kernel(Kv8Args a) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int per = a.n * a.G * (DH / 4);
-  pdl_wait();  // the partial results come from the attention kernel
-  const int64_t bg = item / per;
-  if (bg < static_cast<int64_t>(a.B) * a.Hkv) {
-    const int at = static_cast<int>(item - bg * per);
-    kv8_merge_item<DH>(a, static_cast<int>(bg), 0, 1, at / (DH / 4), at % (DH / 4));
-  }
-}
-
 template <int DH, int RG, int MERGE, bool SEL>
 static cudaError_t launch_few_v(const CUtensorMap *maps, const typename FewArgs<SEL>::type &a, cudaStream_t st) {
   static std::atomic<unsigned long long> configured{0};

@@ -1,9 +1,9 @@
 // Attention over selected pages of the 8-bit cache: the prefix of node i and KV head
 // g is the pages that its list names.
 //
-// Few query rows a KV head (single tokens, small trees): the few-row kernel takes a
-// node and KV head as a sequence of its own, its rows the grouped heads, its block
-// table the list.
+// Few query rows a KV head (single tokens, small trees): a node and KV head is taken
+// as a sequence of its own, its rows the grouped heads, its block table the list
+// (tree_attn_kv8_tokens.cu up to eight heads, the few-row kernel beyond).
 //
 // Many rows (trees, prompt chunks): nodes of one tree choose much the same pages, and
 // a key tile costs the tensor-core kernel the same for one row and for 256.  So a
@@ -23,6 +23,11 @@ namespace eagle {
 size_t attn_kv8_few_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int Lmax, int num_sms);
 cudaError_t launch_tree_attn_kv8_pages_few(const Kv8SelArgs &a, const void *k_pages, const void *v_pages, int dh, int Lmax, void *ws,
                                            int num_sms, cudaStream_t st);
+
+// tree_attn_kv8_tokens.cu
+size_t attn_kv8_tokens_workspace_bytes(int64_t nodes, int Hkv, int dh, int positions, int num_sms);
+cudaError_t launch_tree_attn_kv8_tokens(Kv8SelArgs a, const void *k_pages, const void *v_pages, int dh, int positions, void *ws,
+                                        int num_sms, cudaStream_t st);
 
 constexpr int kUnionPages = 16384;  // pages of a request that a group's map holds
 constexpr int kUnionWarps = 8;
@@ -144,7 +149,9 @@ static ListPlan list_plan(int B, int n, int Hq, int Hkv, int dh, int top, int ma
   const int G = Hq / Hkv, rows = n * G;
   l.lists = rows >= kListRows && max_pages <= kUnionPages;
   if (!l.lists) {
-    l.bytes = attn_kv8_few_workspace_bytes(B * n, 1, Hq, Hkv, dh, listed_positions(top, max_pages, page_size), num_sms);
+    const int positions = listed_positions(top, max_pages, page_size);
+    l.bytes = G <= 8 ? attn_kv8_tokens_workspace_bytes(static_cast<int64_t>(B) * n, Hkv, dh, positions, num_sms)
+                     : attn_kv8_few_workspace_bytes(B * n, 1, Hq, Hkv, dh, positions, num_sms);
     return l;
   }
   // The lists' lengths are known on the device alone: the KV split is chosen for
@@ -193,7 +200,9 @@ cudaError_t launch_tree_attn_kv8_pages(const void *q, const uint8_t *k_pages, co
     static_cast<Kv8Args &>(s) = a;
     s.B = B * n; s.n = 1;
     s.sel = sel; s.top = top; s.nodes = n;
-    return launch_tree_attn_kv8_pages_few(s, k_pages, v_pages, dh, listed_positions(top, max_pages, page_size), ws, num_sms, st);
+    const int positions = listed_positions(top, max_pages, page_size);
+    return a.G <= 8 ? launch_tree_attn_kv8_tokens(s, k_pages, v_pages, dh, positions, ws, num_sms, st)
+                    : launch_tree_attn_kv8_pages_few(s, k_pages, v_pages, dh, positions, ws, num_sms, st);
   }
   if (!ws) return cudaErrorInvalidValue;
   unsigned char *base = reinterpret_cast<unsigned char *>(ws);
