@@ -18,7 +18,8 @@
 // rows of 128 bytes, in the 128-byte swizzle that the MMAs read, a ring of kRing tiles;
 // eight, because a warp issues one gather in some 70 cycles: one producer took 2.2 us
 // a tile), one thread for the MMAs, four warps that take D from tensor memory (two
-// buffers) to the scores.  All but the MMAs' warp make B ready first.
+// buffers) to the scores (eight with 256 rows).  All but the MMAs' warp make B ready
+// first.
 //
 // What bounds it: HBM with few rows (NR = 32: two CTAs an SM), latency for one request.
 //
@@ -34,7 +35,9 @@ using namespace sm100;
 
 template <int DH, int NR>
 struct ScoreShape {
-  static constexpr int kPages = 128, kThreads = 416;
+  static constexpr int kPages = 128;
+  static constexpr int kScorers = NR <= 32 ? 4 : 8;          // warps that take D to the scores
+  static constexpr int kThreads = 32 * (kScorers + 9);
   static constexpr int kLines = DH / 64;                     // lines of 128 bytes that a page's two bounds take
   static constexpr int kOcc = NR <= 32 ? 2 : 1;              // CTAs an SM
   static constexpr int kTileBytes = kLines * kPages * 128;   // [line][page][128 bytes]
@@ -97,10 +100,10 @@ __device__ __forceinline__ uint2 negative_bytes(const uint4 &x) {
 }
 
 template <int DH, int LG, int NR>
-__global__ void __launch_bounds__(416, ScoreShape<DH, NR>::kOcc)
+__global__ void __launch_bounds__(ScoreShape<DH, NR>::kThreads, ScoreShape<DH, NR>::kOcc)
     kv8_score_kernel(const __grid_constant__ CUtensorMap map, SelectArgs a, int pages_per_cta) {
   using Sh = ScoreShape<DH, NR>;
-  constexpr int kProducerWarp = 4, kProducers = 8, kMmaWarp = 12, LINES = Sh::kLines;
+  constexpr int kScorers = Sh::kScorers, kProducerWarp = kScorers, kProducers = 8, kMmaWarp = kScorers + 8, LINES = Sh::kLines;
   extern __shared__ unsigned char score_smem[];
   const uint32_t gap = (1024u - (smem_u32(score_smem) & 1023u)) & 1023u;
   unsigned char *sm = score_smem + gap;
@@ -123,9 +126,9 @@ __global__ void __launch_bounds__(416, ScoreShape<DH, NR>::kOcc)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_free[i], 4);
+      mbar_init(&d_free[i], kScorers);
     }
-    mbar_init(b_full, 12);
+    mbar_init(b_full, kScorers + kProducers);
     mbar_init(teardown, 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -265,11 +268,13 @@ __global__ void __launch_bounds__(416, ScoreShape<DH, NR>::kOcc)
   } else {
     if (tiles) build_rows();
     // ------------------------------------------------------- D to the scores
-    const uint32_t tD = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    // warps 0 .. 3 have D's rows 32 w .., with eight each has every other run of columns
+    const int quarter = warp & 3, run0 = warp >> 2;
+    const uint32_t tD = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int node0 = row0 >> LG;
     float *out = a.scores + ((static_cast<int64_t>(b) * a.n + node0) * a.Hkv + g) * a.stride;
     const int64_t per_node = static_cast<int64_t>(a.Hkv) * a.stride;
-    int p = p_begin + warp * 32 + lane;
+    int p = p_begin + quarter * 32 + lane;
     float ks = a.k_scale[block_of(page_at(p), false)];
     int page = page_at(p + Sh::kPages);  // a tile ahead of its scale
     const bool ready = tiles && wait_bounded(b_full, 0, abort_flag);  // all warps' column scales
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(416, ScoreShape<DH, NR>::kOcc)
       page = page_at(p + 2 * Sh::kPages);
       if (!wait_bounded(&d_full[j & 1], (j / 2) & 1, abort_flag)) break;
       tc_fence_after();
-      for (int c0 = 0; c0 < cols; c0 += 32) {
+      for (int c0 = 32 * run0; c0 < cols; c0 += 8 * kScorers) {
         float v[32];
         tmem_ld32(tD + (j & 1) * NR + c0, v);
 #pragma unroll

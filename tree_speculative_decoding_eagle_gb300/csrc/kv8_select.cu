@@ -21,22 +21,23 @@
 
 namespace eagle {
 
-// T threads (a power of two, 32 or more) a row, V neighbouring scores a thread.
+// T threads (32, or whole CTAs of 128 and more) a row; a warp takes 32 V neighbouring
+// pages, lane by lane, so that a vote gives the places of 32 of them.
 template <int T, int V>
 __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArgs a, int64_t row_count) {
   constexpr int THREADS = T < 128 ? 128 : T, WARPS = T / 32;
   __shared__ int part[2][THREADS / 32];
-  const int tid = threadIdx.x % T, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x % T) >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / T) + threadIdx.x / T;
   pdl_wait();
   pdl_trigger();
   if (row >= row_count) return;  // whole warps: T < 128 has one warp a row
   const int b = static_cast<int>(row / (static_cast<int64_t>(a.n) * a.Hkv));
   const int np = live_pages(a, b), K = min(a.top, np);
-  const float *src = a.scores + row * a.stride;
-  // sum over the row's threads (and, with `before`, of the threads before this one)
+  const int p0 = warp * 32 * V + lane;  // this lane's pages: p0, p0 + 32, ..
+  const float *src = a.scores + row * a.stride + p0;
   int turn = 0;
-  const auto row_sum = [&](int x) {
+  const auto row_sum = [&](int x) {  // over the row's threads
     x = __reduce_add_sync(0xffffffffu, x);
     if constexpr (WARPS > 1) {
       if (lane == 0) part[turn][warp] = x;
@@ -47,22 +48,18 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArg
     return x;
   };
   float s[V];
-  uint32_t key[V];
+  uint32_t key[V];  // 0 past the prefix, the greatest number where a page is selected without its score
 #pragma unroll
-  for (int j = 0; j < V; j += 4) {
-    const int p = tid * V + j;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p < np) x = *reinterpret_cast<const float4 *>(src + p);
-    s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
+  for (int j = 0; j < V; ++j) s[j] = p0 + 32 * j < np ? src[32 * j] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = p + i;
-      // (a score is finite unless the bounds hold NaN; its key stays between)
-      key[j + i] = at >= np ? 0u : (at < a.first || at >= np - a.last) ? 0xffffffffu : max(ordered_u32(s[j + i]), 1u);
-    }
+  for (int j = 0; j < V; ++j) {
+    const int at = p0 + 32 * j;
+    // (a score is finite unless the bounds hold NaN; its key stays between the two)
+    const uint32_t by_score = min(max(ordered_u32(s[j]), 1u), 0xfffffffeu);
+    key[j] = at >= np ? 0u : (at < a.first || at >= np - a.last) ? 0xffffffffu : by_score;
   }
   // The greatest key that at least K of them reach: count(lo) >= K > count(hi).
-  uint32_t lo = 1u, hi = 0xffffffffu;  // live keys lie in between; first + last <= top, so hi + 1 is reached by fewer
+  uint32_t lo = 1u, hi = 0xffffffffu;
   int reach = np;
   if (K < np) {
     const auto count = [&](uint32_t bar) {
@@ -71,30 +68,29 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArg
       for (int j = 0; j < V; ++j) c += key[j] >= bar;
       return row_sum(c);
     };
-    const int forced = count(hi);
+    const int forced = min(np, a.first + a.last);  // below K where K < np and first + last < top
     if (forced >= K) {
       lo = hi;
-      reach = forced;
+      reach = count(hi);
     } else {
       // the least and the greatest key without the forced ones
       uint32_t least = 0xffffffffu, most = 0u;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (key[j]) least = min(least, key[j]);
-        if (key[j] != 0xffffffffu) most = max(most, key[j]);
+        least = min(least, key[j] - 1u);  // no page: the greatest number
+        most = max(most, key[j] + 1u);    // forced: 0
       }
       least = __reduce_min_sync(0xffffffffu, least);
       most = __reduce_max_sync(0xffffffffu, most);
       if constexpr (WARPS > 1) {
-        __syncthreads();
         if (lane == 0) { part[0][warp] = static_cast<int>(least); part[1][warp] = static_cast<int>(most); }
         __syncthreads();
         least = __reduce_min_sync(0xffffffffu, lane < WARPS ? static_cast<uint32_t>(part[0][lane]) : 0xffffffffu);
         most = __reduce_max_sync(0xffffffffu, lane < WARPS ? static_cast<uint32_t>(part[1][lane]) : 0u);
         __syncthreads();
       }
-      lo = least;      // all reach it
-      hi = most + 1u;  // the forced ones alone do
+      lo = least + 1u;  // all reach it
+      hi = most;        // the forced ones alone do
       int above = forced;
       for (int step = 1; reach != K && hi - lo > 1; ++step) {
         uint32_t mid = lo + (hi - lo) / 2;
@@ -113,52 +109,47 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArg
       }
     }
   }
-  // more than K reach lo: those equal to it in order of their pages, after all greater ones
-  int spare = 0, mine = 0, equal = 0;
+  // Taken: all that pass lo and, of those equal to it, `ties` in order of their pages
+  // (all of them where just K reach lo).
+  int greater = 0, equal = 0;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    mine += key[j] > lo;
+    greater += key[j] > lo;
     equal += key[j] == lo;
   }
-  if (reach == K) {
-    mine += equal;
-    equal = 0;
-  } else {
-    spare = K - row_sum(mine);
-  }
-  // places: exclusive sums over the threads before of (taken for sure, equal)
-  int x = mine, y = equal;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int ax = __shfl_up_sync(0xffffffffu, x, o), ay = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) { x += ax; y += ay; }
-  }
+  greater = __reduce_add_sync(0xffffffffu, greater);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  int place = 0, tied = 0, passed = greater;  // taken for sure and equal before this warp; taken for sure of the row
   if constexpr (WARPS > 1) {
     __syncthreads();
-    if (lane == 31) { part[0][warp] = x; part[1][warp] = y; }
+    if (lane == 0) { part[0][warp] = greater; part[1][warp] = equal; }
     __syncthreads();
-    int px = lane < warp ? part[0][lane] : 0, py = lane < warp ? part[1][lane] : 0;
-    px = __reduce_add_sync(0xffffffffu, px);
-    py = __reduce_add_sync(0xffffffffu, py);
-    x += px;
-    y += py;
+    const int x = lane < WARPS ? part[0][lane] : 0, y = lane < WARPS ? part[1][lane] : 0;
+    passed = __reduce_add_sync(0xffffffffu, x);
+    place = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+    tied = __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
   }
-  int at = x - mine, same = y - equal;  // taken before this thread's first page: at + min(same, spare)
+  const int ties = K - passed;
+  place += min(tied, ties);
   int32_t *dst = a.sel + row * a.top;
   float *dst_s = a.sel_score ? a.sel_score + row * a.top : nullptr;
+  const uint32_t below = (1u << lane) - 1u;
+  if (greater || tied < ties) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const bool tie = reach != K && key[j] == lo;
-    const bool take = key[j] > lo || (key[j] == lo && (reach == K || same < spare));
-    if (take) {
-      const int place = at + min(same, spare);
-      dst[place] = tid * V + j;
-      if (dst_s) dst_s[place] = s[j];
-      if (!tie) ++at;
+    for (int j = 0; j < V; ++j) {
+      const uint32_t eq = __ballot_sync(0xffffffffu, key[j] == lo);
+      const bool take = key[j] > lo || (key[j] == lo && tied + __popc(eq & below) < ties);
+      const uint32_t on = __ballot_sync(0xffffffffu, take);
+      if (take) {
+        const int at = place + __popc(on & below);
+        dst[at] = p0 + 32 * j;
+        if (dst_s) dst_s[at] = s[j];
+      }
+      place += __popc(on);
+      tied += __popc(eq);
     }
-    if (tie) ++same;
   }
-  for (int i = K + tid; i < a.top; i += T) {
+  for (int i = K + warp * 32 + lane; i < a.top; i += T) {
     dst[i] = -1;
     if (dst_s) dst_s[i] = -INFINITY;
   }
