@@ -14,9 +14,8 @@
 // The node's score of a page is the largest over the heads that share the KV head.
 //
 // Two kernels.  Scores: kv8_score.cu.  Choice (here): a row's scores as ordered
-// 32-bit keys in registers, a search for the greatest key that `top` of them reach
-// (by interpolation on the counts, every third step by halving), ties to the lower
-// pages, one prefix sum for the places.
+// 32-bit keys in registers, a search by halving for the greatest key that `top` of
+// them reach, ties to the lower pages, places by votes.
 #include "kv8_select.cuh"
 
 namespace eagle {
@@ -47,15 +46,14 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArg
     }
     return x;
   };
-  float s[V];
   uint32_t key[V];  // 0 past the prefix, the greatest number where a page is selected without its score
 #pragma unroll
-  for (int j = 0; j < V; ++j) s[j] = p0 + 32 * j < np ? src[32 * j] : 0.f;
+  for (int j = 0; j < V; ++j) key[j] = p0 + 32 * j < np ? __float_as_uint(src[32 * j]) : 0u;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int at = p0 + 32 * j;
     // (a score is finite unless the bounds hold NaN; its key stays between the two)
-    const uint32_t by_score = min(max(ordered_u32(s[j]), 1u), 0xfffffffeu);
+    const uint32_t by_score = min(max(ordered_u32(__uint_as_float(key[j])), 1u), 0xfffffffeu);
     key[j] = at >= np ? 0u : (at < a.first || at >= np - a.last) ? 0xffffffffu : by_score;
   }
   // The greatest key that at least K of them reach: count(lo) >= K > count(hi).
@@ -91,60 +89,67 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArg
       }
       lo = least + 1u;  // all reach it
       hi = most;        // the forced ones alone do
-      int above = forced;
-      for (int step = 1; reach != K && hi - lo > 1; ++step) {
-        uint32_t mid = lo + (hi - lo) / 2;
-        if (step % 3) {
-          const float share = (static_cast<float>(reach - K) + 0.5f) / static_cast<float>(reach - above);
-          mid = min(max(lo + static_cast<uint32_t>(static_cast<float>(hi - lo) * share), lo + 1), hi - 1);
-        }
+      // 7 halvings on average for 16 of 512 pages, 9 for 32 of 2048 (12 and 13 by
+      // interpolation on the counts: the greatest scores lie far apart)
+      while (reach != K && hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
         const int c = count(mid);
         if (c >= K) {
           lo = mid;
           reach = c;
         } else {
           hi = mid;
-          above = c;
         }
       }
     }
   }
-  // Taken: all that pass lo and, of those equal to it, `ties` in order of their pages
-  // (all of them where just K reach lo).
-  int greater = 0, equal = 0;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    greater += key[j] > lo;
-    equal += key[j] == lo;
-  }
-  greater = __reduce_add_sync(0xffffffffu, greater);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  int place = 0, tied = 0, passed = greater;  // taken for sure and equal before this warp; taken for sure of the row
-  if constexpr (WARPS > 1) {
-    __syncthreads();
-    if (lane == 0) { part[0][warp] = greater; part[1][warp] = equal; }
-    __syncthreads();
-    const int x = lane < WARPS ? part[0][lane] : 0, y = lane < WARPS ? part[1][lane] : 0;
-    passed = __reduce_add_sync(0xffffffffu, x);
-    place = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
-    tied = __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
-  }
-  const int ties = K - passed;
-  place += min(tied, ties);
   int32_t *dst = a.sel + row * a.top;
   float *dst_s = a.sel_score ? a.sel_score + row * a.top : nullptr;
   const uint32_t below = (1u << lane) - 1u;
-  if (greater || tied < ties) {
+  const auto take = [&](int at, int j) {
+    dst[at] = p0 + 32 * j;
+    if (dst_s) dst_s[at] = src[32 * j];  // again: a few of many
+  };
+  // of the warps before this one (whole CTAs only)
+  const auto before = [&](int x) {
+    if constexpr (WARPS > 1) {
+      x = __reduce_add_sync(0xffffffffu, x);
+      __syncthreads();
+      if (lane == 0) part[0][warp] = x;
+      __syncthreads();
+      return __reduce_add_sync(0xffffffffu, lane < warp ? part[0][lane] : 0);
+    }
+    return 0;
+  };
+  if (reach == K) {
+    int mine = 0, place = 0;
+    if constexpr (WARPS > 1) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) mine += key[j] >= lo;
+      place = before(mine);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t on = __ballot_sync(0xffffffffu, key[j] >= lo);
+      if (!on) continue;
+      if (key[j] >= lo) take(place + __popc(on & below), j);
+      place += __popc(on);
+    }
+  } else {  // all that pass lo and, of those equal to it, the first `ties`
+    int greater = 0, equal = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      greater += key[j] > lo;
+      equal += key[j] == lo;
+    }
+    const int ties = K - row_sum(greater);
+    int tied = before(equal), place = before(greater) + min(tied, ties);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const uint32_t eq = __ballot_sync(0xffffffffu, key[j] == lo);
-      const bool take = key[j] > lo || (key[j] == lo && tied + __popc(eq & below) < ties);
-      const uint32_t on = __ballot_sync(0xffffffffu, take);
-      if (take) {
-        const int at = place + __popc(on & below);
-        dst[at] = p0 + 32 * j;
-        if (dst_s) dst_s[at] = s[j];
-      }
+      const bool mine = key[j] > lo || (key[j] == lo && tied + __popc(eq & below) < ties);
+      const uint32_t on = __ballot_sync(0xffffffffu, mine);
+      if (mine) take(place + __popc(on & below), j);
       place += __popc(on);
       tied += __popc(eq);
     }
