@@ -611,7 +611,7 @@ int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B,
  * give zeros.  A head that holds an infinity or NaN gives NaN in its own columns
  * alone.
  * Limits: those of eagle_rope; eps > 0 and finite, weight_offset finite, weights
- * 16-byte aligned; B*n*(Hq + 2 Hkv) <= 2^30. */
+ * 16-byte aligned. */
 int eagle_qk_norm_rope(const void *q, const void *k, const void *v, int dtype,
                        int B, int n, int Hq, int Hkv, int dh, int64_t ld_q,
                        int64_t ld_k, int64_t ld_v, const void *q_weight,

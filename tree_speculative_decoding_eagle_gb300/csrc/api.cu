@@ -450,8 +450,6 @@ int eagle_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, i
   constexpr float kMax = std::numeric_limits<float>::max();  // no NaN, no infinity
   if (!(eps > 0.f && eps <= kMax) || !(weight_offset >= -kMax && weight_offset <= kMax)) return EAGLE_ERR_INVALID;
   if (!aligned16(q_weight) || !aligned16(k_weight)) return EAGLE_ERR_INVALID;
-  // heads are numbered in 31 bits
-  if (static_cast<int64_t>(B) * n * (static_cast<int64_t>(Hq) + 2ll * Hkv) > (1ll << 30)) return EAGLE_ERR_UNSUPPORTED;
   return from_cuda(launch_qk_norm_rope(q, k, v, dtype, B, n, Hq, Hkv, dh, ld_q, ld_k, ld_v, q_weight, k_weight,
                                        weight_offset, eps, inv_freq, rot_dim, interleaved, factor, pos_base, pos_off,
                                        shift, q_out, k_tree, v_tree, current_num_sms(),

@@ -8,185 +8,154 @@
 // head's lanes in a fixed order, so a head's result does not depend on the launch.
 //
 // What bounds it: HBM (each element read once and written once), latency for one
-// tree.  Heads are numbered node by node and a CTA takes a run of them, whatever
-// their nodes: no place for a head stays empty.  A group of lanes holds a head's
-// 16-byte vectors in registers between the sum and the rotation, so the head is
-// read once; a thread has up to four heads' vectors on their way while the turns of
-// the run's nodes and the weights are made ready in shared memory.
+// tree.  A group of lanes holds a head's 16-byte vectors in registers between the sum
+// and the rotation, so the head is read once.  A thread stays with one node and takes
+// up to four of its heads, their vectors on their way together while the node's turns
+// and the weights are made ready in shared memory; the block is as large as the
+// node's heads need.
 #include "rope.cuh"
 
 namespace eagle {
 
 constexpr int kNormThreads = 256;
 
-// x / d for x < 2^31 by a product: s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
-struct Divisor {
-  uint32_t d, m;
-  int s;
-  explicit Divisor(uint32_t of) : d(of), s(0) {
-    while ((1ull << s) < d) ++s;
-    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return (__umulhi(m, x) + x) >> s; }
-};
-
 struct NormArgs {
   RopeArgs r;
   const void *q_weight, *k_weight;  // [dh] of the same type, or NULL: ones
   float eps, offset, mean;          // mean: 1 / dh
-  uint32_t heads;                   // B * n * (Hq + Hkv, and Hkv of v), below 2^31
-  Divisor per_node, per_seq;        // heads of a node, nodes of a sequence
+  int nodes, heads;                 // B * n; of a node: Hq + Hkv, and Hkv of v
 };
 
-// The run of heads a CTA takes: its first node, the first head's place in that
-// node, and the nodes it touches.
-struct HeadRun {
-  uint32_t base, node0, rem, nodes;
-  __device__ __forceinline__ HeadRun(const NormArgs &a, uint32_t count) {
-    base = blockIdx.x * count;
-    node0 = a.per_node(base);
-    rem = base - node0 * a.per_node.d;
-    nodes = a.per_node(min(base + count, a.heads) - 1) - node0 + 1;
-  }
-};
-// cos and sin of the run's nodes (node k's pair j at cs[k * half + j]).  A thread
-// keeps its pair: the float64 operations are once a pair and CTA.
-__device__ __forceinline__ void run_turns(const NormArgs &a, const HeadRun &run, float2 *cs) {
-  for (int j = threadIdx.x; j < a.r.half; j += kNormThreads) {
+// cos and sin of `count` neighbouring nodes (node k's pair j at cs[k * half + j]).  A
+// thread keeps its pair: the float64 operations are once a pair and CTA.
+__device__ __forceinline__ void run_turns(const NormArgs &a, int node0, int count, float2 *cs) {
+  for (int j = threadIdx.x; j < a.r.half; j += blockDim.x) {
     const uint64_t inc = turn_step(a.r.inv_freq[j]);
-    for (uint32_t k = 0; k < run.nodes; ++k) {
-      const uint32_t node = run.node0 + k, b = a.per_seq(node);
-      cs[k * a.r.half + j] = turn_at(inc, position_of(a.r, node, b, node - b * a.per_seq.d), a.r.factor);
+    for (int k = 0; k < count && node0 + k < a.nodes; ++k) {
+      const int node = node0 + k, b = node / a.r.n;
+      cs[k * a.r.half + j] = turn_at(inc, position_of(a.r, node, b, node - b * a.r.n), a.r.factor);
     }
   }
 }
 
 // 16-byte vectors, `lanes` threads a head, NI items a lane (an item as in rope.cu:
 // two vectors half of rot_dim apart, one vector of whole pairs, or one that does
-// not turn), U heads a thread with their loads in flight together.
+// not turn), U heads a thread with their loads in flight together.  blockIdx.x: nb
+// nodes, each with `per_node` threads; blockIdx.y: a run of U * per_node / lanes heads.
 template <typename T, bool INTER, int NI, int U>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_vec_kernel(NormArgs a, int log_lanes, int items) {
+__global__ void __launch_bounds__(512) norm_rope_vec_kernel(NormArgs a, int log_lanes, int items, int per_node, int nb) {
   constexpr int E = VecTraits<T>::kElems;
   extern __shared__ float4 norm_smem[];
   float *ws = reinterpret_cast<float *>(norm_smem);  // q's weights, then k's
-  const int dh = a.r.dh, half = a.r.half;
+  const int dh = a.r.dh, half = a.r.half, Hq = a.r.Hq, Hkv = a.r.Hkv;
   float2 *turns = reinterpret_cast<float2 *>(ws + 2 * dh);
-  const int lanes = 1 << log_lanes, slots = kNormThreads >> log_lanes;
-  const int lane = threadIdx.x & (lanes - 1), slot = threadIdx.x >> log_lanes;
-  const HeadRun run(a, U * slots);
-  const int turning = INTER ? 2 * half / E : half / E;  // items that turn
+  const int lanes = 1 << log_lanes, slots = per_node >> log_lanes;
+  const int near = threadIdx.x / per_node, slot = (threadIdx.x - near * per_node) >> log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int node = blockIdx.x * nb + near, h0 = blockIdx.y * U * slots + slot;
+  // heads of this thread: none in the last warp's spare lanes and the last CTA's spare nodes
+  const int heads = near < nb && node < a.nodes ? a.heads : 0;
+  // An item's columns from c[k] and, where it turns in two halves, c[k] + half; v is
+  // copied in the same pieces.
+  int c[NI];
+  bool live[NI], turns_here[NI];
+#pragma unroll
+  for (int k = 0; k < NI; ++k) {
+    const int it = lane + k * lanes, turning = INTER ? 2 * half / E : half / E;
+    live[k] = it < items;
+    turns_here[k] = it < turning;
+    c[k] = INTER || it < turning ? it * E : 2 * half + (it - turning) * E;
+  }
   pdl_wait();
+  const int b = node / a.r.n, i = node - b * a.r.n;
+  const T *src_q = reinterpret_cast<const T *>(a.r.q) + node * a.r.ld_q, *src_k = reinterpret_cast<const T *>(a.r.k) + node * a.r.ld_k,
+          *src_v = reinterpret_cast<const T *>(a.r.v) + node * a.r.ld_v;
+  const int64_t tree = (static_cast<int64_t>(b) * Hkv * a.r.n + i) * dh, per_head = static_cast<int64_t>(a.r.n) * dh;
+  T *dst_q = reinterpret_cast<T *>(a.r.q_out) + static_cast<int64_t>(node) * Hq * dh, *dst_k = reinterpret_cast<T *>(a.r.k_tree) + tree,
+    *dst_v = reinterpret_cast<T *>(a.r.v_tree) + tree;
   uint4 x[U][NI][2];
-  T *dst[U];
-  uint32_t near[U];  // the head's node within the run
-  bool normed[U], is_q[U];
-  // columns of item number it: c1 < 0 for an item of one vector
-  const auto columns = [&](int it, bool is_v, int &c0, int &c1) {
-    c1 = -1;
-    if (is_v) {
-      c0 = it * E;
-      if (!INTER && (it + items) * E < dh) c1 = (it + items) * E;  // interleaved, the items are the vectors
-    } else if (it < turning) {
-      c0 = it * E;
-      if (!INTER) c1 = half + it * E;
-    } else {
-      c0 = 2 * half + (it - turning) * E;
-    }
-  };
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t at = run.rem + u * slots + slot;
-    dst[u] = nullptr;
-    normed[u] = is_q[u] = false;
-    near[u] = 0;
-    if (run.base + u * slots + slot >= a.heads) continue;
-    near[u] = a.per_node(at);
-    const int h = at - near[u] * a.per_node.d, node = run.node0 + near[u], b = a.per_seq(node);
-    const T *src;
-    normed[u] = head_of(a.r, node, b, node - b * a.r.n, h, src, dst[u]);
-    is_q[u] = h < a.r.Hq;
+    const int h = h0 + u * slots;
+    if (h >= heads) continue;
+    const T *src = h < Hq ? src_q + h * dh : h < Hq + Hkv ? src_k + (h - Hq) * dh : src_v + (h - Hq - Hkv) * dh;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int it = lane + i * lanes;
-      if (it >= items) continue;
-      int c0, c1;
-      columns(it, !normed[u], c0, c1);
-      x[u][i][0] = __ldcs(reinterpret_cast<const uint4 *>(src + c0));  // coherent: q may be turned in place
-      if (!INTER && c1 >= 0) x[u][i][1] = __ldcs(reinterpret_cast<const uint4 *>(src + c1));
+    for (int k = 0; k < NI; ++k) {
+      if (!live[k]) continue;
+      x[u][k][0] = __ldcs(reinterpret_cast<const uint4 *>(src + c[k]));  // coherent: q may be turned in place
+      if (!INTER && turns_here[k]) x[u][k][1] = __ldcs(reinterpret_cast<const uint4 *>(src + c[k] + half));
     }
   }
-  for (int c = threadIdx.x; c < 2 * dh; c += kNormThreads) {
-    const T *wt = reinterpret_cast<const T *>(c < dh ? a.q_weight : a.k_weight);
-    ws[c] = wt ? static_cast<float>(wt[c < dh ? c : c - dh]) + a.offset : 1.f;
+  for (int e = threadIdx.x; e < 2 * dh; e += blockDim.x) {
+    const T *wt = reinterpret_cast<const T *>(e < dh ? a.q_weight : a.k_weight);
+    ws[e] = wt ? static_cast<float>(wt[e < dh ? e : e - dh]) + a.offset : 1.f;
   }
-  run_turns(a, run, turns);
+  run_turns(a, blockIdx.x * nb, nb, turns);
   __syncthreads();
   pdl_trigger();
+  const float2 *cs = turns + near * half;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * slots;
+    const bool normed = h < Hq + Hkv;
     // the head's sum of squares: every lane of the warp takes part in the exchange
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int it = lane + i * lanes;
-      if (!normed[u] || it >= items) continue;
+    for (int k = 0; k < NI; ++k) {
+      if (!live[k] || h >= heads) continue;
       float f[E];
-      VecTraits<T>::unpack(x[u][i][0], f);
+      VecTraits<T>::unpack(x[u][k][0], f);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum = fmaf(f[e], f[e], sum);
-      if (!INTER && it < turning) {
-        VecTraits<T>::unpack(x[u][i][1], f);
+      if (!INTER && turns_here[k]) {
+        VecTraits<T>::unpack(x[u][k][1], f);
 #pragma unroll
         for (int e = 0; e < E; ++e) sum = fmaf(f[e], f[e], sum);
       }
     }
     for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!dst[u]) continue;
+    if (h >= heads) continue;
     const float r = rsqrtf(fmaf(sum, a.mean, a.eps));
-    const float2 *cs = turns + near[u] * half;
-    const float *w = ws + (is_q[u] ? 0 : dh);
-    const auto scaled = [&](const uint4 &xv, int c, float (&y)[E]) {
+    const float *w = ws + (h < Hq ? 0 : dh);
+    T *dst = h < Hq ? dst_q + h * dh : (normed ? dst_k + (h - Hq) * per_head : dst_v + (h - Hq - Hkv) * per_head);
+    const auto scaled = [&](const uint4 &xv, int col, float (&y)[E]) {
       VecTraits<T>::unpack(xv, y);
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(w + c + e);
+        const float4 f = *reinterpret_cast<const float4 *>(w + col + e);
         y[e] *= r * f.x; y[e + 1] *= r * f.y; y[e + 2] *= r * f.z; y[e + 3] *= r * f.w;
       }
     };
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int it = lane + i * lanes;
-      if (it >= items) continue;
-      int c0, c1;
-      columns(it, !normed[u], c0, c1);
-      if (normed[u]) {
+    for (int k = 0; k < NI; ++k) {
+      if (!live[k]) continue;
+      if (normed) {
         float f0[E], f1[E];
-        scaled(x[u][i][0], c0, f0);
-        if (it >= turning) {
-          x[u][i][0] = pack_vec<T>(f0);
+        scaled(x[u][k][0], c[k], f0);
+        if (!turns_here[k]) {
+          x[u][k][0] = pack_vec<T>(f0);
         } else if constexpr (INTER) {
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
-            const float2 t = cs[c0 / 2 + e / 2];
+            const float2 t = cs[c[k] / 2 + e / 2];
             f1[e] = f0[e] * t.x - f0[e + 1] * t.y;
             f1[e + 1] = f0[e + 1] * t.x + f0[e] * t.y;
           }
-          x[u][i][0] = pack_vec<T>(f1);
+          x[u][k][0] = pack_vec<T>(f1);
         } else {
-          scaled(x[u][i][1], c1, f1);
+          scaled(x[u][k][1], c[k] + half, f1);
           float r0[E], r1[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float2 t = cs[c0 + e];
+            const float2 t = cs[c[k] + e];
             r0[e] = f0[e] * t.x - f1[e] * t.y;
             r1[e] = f1[e] * t.x + f0[e] * t.y;
           }
-          x[u][i][0] = pack_vec<T>(r0);
-          x[u][i][1] = pack_vec<T>(r1);
+          x[u][k][0] = pack_vec<T>(r0);
+          x[u][k][1] = pack_vec<T>(r1);
         }
       }
-      *reinterpret_cast<uint4 *>(dst[u] + c0) = x[u][i][0];
-      if (!INTER && c1 >= 0) *reinterpret_cast<uint4 *>(dst[u] + c1) = x[u][i][1];
+      *reinterpret_cast<uint4 *>(dst + c[k]) = x[u][k][0];
+      if (!INTER && turns_here[k]) *reinterpret_cast<uint4 *>(dst + c[k] + half) = x[u][k][1];
     }
   }
 }
@@ -197,16 +166,14 @@ template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_pair_kernel(NormArgs a) {
   constexpr int E = VecTraits<T>::kElems, kWarps = kNormThreads / 32;
   extern __shared__ float4 norm_smem[];
-  float2 *turns = reinterpret_cast<float2 *>(norm_smem);
-  const HeadRun run(a, kWarps);
+  float2 *cs = reinterpret_cast<float2 *>(norm_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int node = blockIdx.x, b = node / a.r.n, h = blockIdx.y * kWarps + warp;
   pdl_wait();
-  run_turns(a, run, turns);
+  run_turns(a, node, 1, cs);
   __syncthreads();
   pdl_trigger();
-  if (run.base + warp >= a.heads) return;
-  const uint32_t at = run.rem + warp, near = a.per_node(at);
-  const int h = at - near * a.per_node.d, node = run.node0 + near, b = a.per_seq(node);
+  if (h >= a.heads) return;
   const T *src;
   T *dst;
   const bool normed = head_of(a.r, node, b, node - b * a.r.n, h, src, dst);
@@ -222,7 +189,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_pair_kernel(NormArgs a
     }
     r = rsqrtf(fmaf(warp_sum(sum), a.mean, a.eps));
   }
-  const float2 *cs = turns + near * a.r.half;
   for (int j = lane; j < a.r.dh / 2; j += 32) {
     const bool rot = normed && j < a.r.half;
     const int c0 = rot ? (a.r.interleaved ? 2 * j : j) : 2 * j;
@@ -241,17 +207,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_pair_kernel(NormArgs a
   }
 }
 
-// Shared memory for the turns of `count` neighbouring heads.
-static size_t turns_bytes(int count, int H, int half) {
-  return static_cast<size_t>((count + H - 2) / H + 1) * half * sizeof(float2);
-}
-
 template <typename T, bool INTER, int NI, int U>
-static cudaError_t launch_norm_v(const NormArgs &a, int log_lanes, int items, cudaStream_t st) {
-  const int count = U * (kNormThreads >> log_lanes);
-  const size_t smem = 2 * a.r.dh * sizeof(float) + turns_bytes(count, a.per_node.d, a.r.half);
-  return launch_chained(norm_rope_vec_kernel<T, INTER, NI, U>, dim3((a.heads + count - 1) / count), dim3(kNormThreads), smem, st,
-                        a, log_lanes, items);
+static cudaError_t launch_norm_v(const NormArgs &a, int log_lanes, int items, int most_threads, cudaStream_t st) {
+  // a node's heads over runs (blockIdx.y) of equal size, several nodes to a CTA where
+  // one has fewer than 128 threads to do
+  const int lanes = 1 << log_lanes, runs = (a.heads * lanes + U * most_threads - 1) / (U * most_threads);
+  const int slots = (a.heads + U * runs - 1) / (U * runs), per_node = slots * lanes;
+  const int nb = per_node >= 128 ? 1 : 128 / per_node;
+  const int threads = (nb * per_node + 31) / 32 * 32;
+  const size_t smem = 2 * a.r.dh * sizeof(float) + static_cast<size_t>(nb) * a.r.half * sizeof(float2);
+  const dim3 grid((a.nodes + nb - 1) / nb, (a.heads + U * slots - 1) / (U * slots));
+  return launch_chained(norm_rope_vec_kernel<T, INTER, NI, U>, grid, dim3(threads), smem, st, a, log_lanes, items, per_node, nb);
 }
 
 template <typename T, bool INTER>
@@ -259,12 +225,14 @@ static cudaError_t launch_norm_vec(const NormArgs &a, int items, int num_sms, cu
   int log_lanes = 0;
   while (log_lanes < 5 && (1 << log_lanes) < items) ++log_lanes;
   const int ni = (items + (1 << log_lanes) - 1) >> log_lanes;
-  if (ni > 2) return launch_norm_v<T, INTER, 4, 1>(a, log_lanes, items, st);
-  if (ni > 1) return launch_norm_v<T, INTER, 2, 1>(a, log_lanes, items, st);
-  // four heads a thread where that leaves each SM two CTAs or more, else one
-  const uint32_t slots = kNormThreads >> log_lanes;
-  return a.heads >= 8u * slots * num_sms ? launch_norm_v<T, INTER, 1, 4>(a, log_lanes, items, st)
-                                         : launch_norm_v<T, INTER, 1, 1>(a, log_lanes, items, st);
+  if (ni > 2) return launch_norm_v<T, INTER, 4, 1>(a, log_lanes, items, 512, st);
+  if (ni > 1) return launch_norm_v<T, INTER, 2, 1>(a, log_lanes, items, 512, st);
+  // several heads a thread where that leaves each SM four warps' worth of threads or
+  // more, else one and smaller blocks: latency counts
+  const int64_t work = static_cast<int64_t>(a.nodes) * a.heads << log_lanes;
+  constexpr int MANY = INTER ? 4 : 2;  // (f32, 120 heads of 128: 249, 208, 186, 183 us with one to four of one vector)
+  return work >= 512ll * MANY * num_sms ? launch_norm_v<T, INTER, 1, MANY>(a, log_lanes, items, INTER ? 256 : 512, st)
+                                        : launch_norm_v<T, INTER, 1, 1>(a, log_lanes, items, 256, st);
 }
 
 template <typename T>
@@ -276,8 +244,8 @@ static cudaError_t launch_norm_t(const NormArgs &a, int num_sms, cudaStream_t st
     return a.r.interleaved ? launch_norm_vec<T, true>(a, a.r.dh / E, num_sms, st)
                            : launch_norm_vec<T, false>(a, half / E + (a.r.dh - 2 * half) / E, num_sms, st);
   constexpr int kWarps = kNormThreads / 32;
-  return launch_chained(norm_rope_pair_kernel<T>, dim3((a.heads + kWarps - 1) / kWarps), dim3(kNormThreads),
-                        turns_bytes(kWarps, a.per_node.d, half), st, a);
+  return launch_chained(norm_rope_pair_kernel<T>, dim3(a.nodes, (a.heads + kWarps - 1) / kWarps), dim3(kNormThreads),
+                        half * sizeof(float2), st, a);
 }
 
 cudaError_t launch_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int B, int n, int Hq, int Hkv,
@@ -286,11 +254,10 @@ cudaError_t launch_qk_norm_rope(const void *q, const void *k, const void *v, int
                                 int rot_dim, int interleaved, float factor, const int32_t *pos_base,
                                 const int32_t *pos_off, int shift, void *q_out, void *k_tree, void *v_tree, int num_sms,
                                 cudaStream_t st) {
-  const uint32_t H = Hq + (v ? 2 : 1) * Hkv;
   const NormArgs a = {{q, k, v, q_out, k_tree, v_tree, B, n, Hq, Hkv, dh, rot_dim / 2, interleaved, shift, ld_q, ld_k, ld_v,
                        inv_freq, pos_base, pos_off, factor},
-                      q_weight, k_weight, eps, weight_offset, 1.f / static_cast<float>(dh),
-                      static_cast<uint32_t>(B) * n * H, Divisor(H), Divisor(n)};
+                      q_weight, k_weight, eps, weight_offset, 1.f / static_cast<float>(dh), B * n,
+                      Hq + (v ? 2 : 1) * Hkv};
   return dtype == EAGLE_BF16 ? launch_norm_t<__nv_bfloat16>(a, num_sms, st) : launch_norm_t<float>(a, num_sms, st);
 }
 
