@@ -608,8 +608,7 @@ int eagle_rope(const void *q, const void *k, const void *v, int dtype, int B,
  *              (weight_offset counts for nothing then)
  * The other arguments are eagle_rope's.  Everything between the element read and
  * the one written is float32, rounded once; sums of squares past float32's range
- * give zeros.  A head that holds an infinity or NaN gives NaN in its own columns
- * alone.
+ * give zeros.  A head that holds an infinity or NaN spoils no other.
  * Limits: those of eagle_rope; eps > 0 and finite, weight_offset finite, weights
  * 16-byte aligned. */
 int eagle_qk_norm_rope(const void *q, const void *k, const void *v, int dtype,
@@ -801,7 +800,9 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages,
  *              the page's k_scale: over the page's rows, the least number of each
  *              column rounded down to a multiple of 1/2, then the greatest rounded
  *              up (both are e4m3 numbers); -448 and 448 where a row holds NaN.
- *              Pages that are not touched keep theirs
+ *              Pages that are not touched keep theirs.  A request that is cut short
+ *              keeps the wider bounds of its last page until a call with a from_len
+ *              below its new length
  *   status     EAGLE_ERR_INVALID for a block-table entry outside [0, num_pages)
  *              on a touched page (it is skipped).  A page belongs to one request:
  *              the bounds of one that two requests touch are unspecified

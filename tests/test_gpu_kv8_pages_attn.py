@@ -159,6 +159,12 @@ def test_all_pages_is_the_whole_prefix():
     Case.check(c, out, lse)
 
 
+def test_tables_too_wide_for_shared_lists():
+    """More pages a request than a group's map holds: many rows node by node."""
+    Listed([40, 300], 20, 4, 2, 64, 16, 3, extra_pages=16400).run()
+    Listed([40, 300], 5, 24, 2, 64, 16, 3, extra_pages=16400).run()
+
+
 def test_long_chains_of_nodes():
     for n in (200, 517):
         Listed([0, 75], n, 4, 2, 64, 16, 3, keep=torch.ones((2, n, n)).tril().bool()).run()

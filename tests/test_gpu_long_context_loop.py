@@ -60,7 +60,7 @@ def one_step(cache, mirror, step, g, freqs, w):
         q, kt, vt = norm_rope(qkv, freqs, w, pos_base=cache.kv_len, pos_off=step.tree["depth"])
         out, lse = step.attend_kv8(cache, layer, q, kt, vt, top=TOP, first=FIRST, last=LAST)
         trees.append((kt, vt))
-        sel = step.sel.tolist()
+        sel = step.sels[TOP].tolist()
         qn = f64(q)
         for b in range(B):
             pages, lo, hi, scale = boxes(mirror, layer, b)
@@ -211,3 +211,88 @@ def test_a_step_in_a_graph():
         for name in ("k_pages", "v_pages", "k_bounds"):
             assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(getattr(a, name), getattr(b, name)))
     assert int(caches[0].status) == 0 and caches[0].kv_len.tolist() == [70 + 18, 5 + 6, 51 + 24]
+
+
+def test_two_calls_at_once():
+    """Selection and attention of two layers on two streams, a workspace each: what
+    one after the other gives."""
+    g = torch.Generator().manual_seed(11)
+    cache = KV8Cache(2, 2, 128, 16, 700, 330, layers=2, bounds=True)
+    new = i32([5000, 3333])
+    slots = torch.empty(8333, dtype=torch.int32, device="cuda")
+    cache.reserve(new, slots)
+    for layer in range(2):
+        kv = torch.randn((2, 8333, 2, 128), generator=g).to(bf).cuda()
+        cache.append(layer, kv[0], kv[1], slots)
+    cache.grow(new)
+    for n, heads in ((1, 8), (40, 8), (40, 32)):
+        q, kt, vt = (torch.randn(s, generator=g).to(bf).cuda() for s in ((2, n, heads, 128), (2, 2, n, 128), (2, 2, n, 128)))
+        mask = eg.tree_mask(i32([[-1] + list(range(n - 1))] * 2))
+
+        def run(layer, ws, out, lse):
+            sel = cache.select(layer, q, 12, workspace=ws)
+            return cache.attend_pages(layer, q, kt, vt, mask, sel, out=out, lse=lse, workspace=ws)
+
+        spaces = [eg.Workspace("cuda") for _ in range(2)]
+        want = [tuple(t.clone() for t in run(layer, spaces[layer], None, None)) for layer in range(2)]
+        torch.cuda.synchronize()
+        side = [torch.cuda.Stream() for _ in range(2)]
+        outs = [(torch.zeros_like(want[0][0]), torch.zeros_like(want[0][1])) for _ in range(2)]
+        for _ in range(20):
+            for layer in range(2):
+                with torch.cuda.stream(side[layer]):
+                    run(layer, spaces[layer], *outs[layer])
+        torch.cuda.synchronize()
+        for layer in range(2):
+            assert torch.equal(outs[layer][0], want[layer][0]) and torch.equal(outs[layer][1], want[layer][1])
+    assert int(cache.status) == 0
+
+
+def test_bounds_after_a_cut():
+    """kv_len set back: the last page's bounds stay wider until the request grows."""
+    g = torch.Generator().manual_seed(12)
+    cache = KV8Cache(1, 1, 64, 16, 8, 8, bounds=True)
+    x = torch.randn((40, 1, 64), generator=g).to(bf).cuda()
+    slots = torch.empty(40, dtype=torch.int32, device="cuda")
+    cache.reserve(i32([40]), slots)
+    cache.append(0, x, x, slots)
+    cache.grow(40)
+    cache.kv_len.fill_(19)
+    cache.trim()
+    slot = torch.empty(1, dtype=torch.int32, device="cuda")
+    cache.reserve(i32([1]), slot)
+    cache.append(0, x[:1] * 3, x[:1], slot)
+    cache.grow(1)
+    page = int(cache.block_table[0, 1])
+    rows = okv8.decode(cache.k_pages[0].view(torch.uint8).cpu().numpy()[page, 0, :4])
+    got = okv8.decode(cache.k_bounds[0].view(torch.uint8).cpu().numpy()[page, 0])
+    np.testing.assert_array_equal(got, np.stack(oselect.bounds(rows)))
+
+
+def test_a_cache_with_bounds_checks_its_head_dimension():
+    with pytest.raises(eg.EagleError):
+        KV8Cache(1, 1, 80, 16, 4, 4, bounds=True)
+
+
+def test_steps_of_two_sizes_keep_their_lists():
+    """attend_kv8 with another `top` does not take the list of a captured one away."""
+    g = torch.Generator().manual_seed(13)
+    cache = KV8Cache(B, Hkv, dh, P, N, MP, bounds=True)
+    slots = torch.empty(150, dtype=torch.int32, device="cuda")
+    cache.reserve(i32([50] * B), slots)
+    x = torch.randn((150, Hkv, dh), generator=g).to(bf).cuda()
+    cache.append(0, x, x, slots)
+    cache.grow(50)
+    step = TreeStep(B, D, k, m, V, Hq, Hkv, dh, MP * P)
+    step.draft((torch.randn((B, D, k, V), generator=g) * 4).cuda())
+    step.build()
+    q, kt, vt = (torch.randn(s, generator=g).to(bf).cuda() for s in ((B, m + 1, Hq, dh), (B, Hkv, m + 1, dh), (B, Hkv, m + 1, dh)))
+    want = [t.clone() for t in step.attend_kv8(cache, 0, q, kt, vt, top=2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.attend_kv8(cache, 0, q, kt, vt, top=2)
+    step.attend_kv8(cache, 0, q, kt, vt, top=4)
+    assert step.sels[2].shape[-1] == 2 and step.sels[4].shape[-1] == 4
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(step.attn_out, want[0]) and torch.equal(step.lse, want[1])

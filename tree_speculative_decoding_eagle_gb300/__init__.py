@@ -529,14 +529,16 @@ def _heads(t, name, B, n, dh, dtype, device):
     are evenly spaced."""
     if t.get_device() != device or t.dtype != dtype:
         raise EagleError(f"{name} must be a {dtype} CUDA tensor on device {device}")
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != dh:
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != n or shape[3] != dh:
         raise EagleError(f"{name} must be [B, n, heads, dh]")
+    heads = shape[2]
     sb, sn, sh, sd = t.stride()
     if n == 1 and B > 1:
         sn = sb                # the one node's stride says nothing
     elif n == 1:
-        sn = max(sn, t.shape[2] * dh)
-    if sd != 1 or (t.shape[2] > 1 and sh != dh) or (B > 1 and sb != n * sn):
+        sn = max(sn, heads * dh)
+    if sd != 1 or (heads > 1 and sh != dh) or (B > 1 and sb != n * sn):
         raise EagleError(f"{name} must have dense heads and evenly spaced nodes")
     return sn
 

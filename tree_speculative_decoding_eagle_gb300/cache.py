@@ -13,6 +13,8 @@ and for long contexts, in a cache made with bounds=True:
     select   -> eagle_kv8_select    the pages that each node and KV head attends to
     attend_pages -> eagle_tree_attn_kv8_pages   draft nodes or single tokens over those
 whose bounds (eagle_kv8_bounds) grow() and commit() renew for the pages they touched.
+A request whose kv_len is set back keeps the wider bounds of its last page until it
+grows again.
 kv_len counts the positions before the tree's root, which is node 0 of the tree,
 at position kv_len.  So one step over a tree of depth D is
     reserve(D + 1) -> rope(pos_base=kv_len, pos_off=depth) -> attend -> verify
@@ -50,6 +52,8 @@ class KV8Cache:
     def __init__(self, B, Hkv, dh, page_size, num_pages, max_pages, layers=1, device="cuda", bounds=False):
         if layers < 1:
             raise EagleError("a cache needs a layer")
+        if bounds and dh not in (64, 128):
+            raise EagleError("bounds are kept for head dimensions of 64 and 128")
         i32 = dict(dtype=torch.int32, device=device)
         self.page_size = page_size
         shape = (num_pages, Hkv, page_size, dh)

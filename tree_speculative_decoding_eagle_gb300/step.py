@@ -42,7 +42,7 @@ class TreeStep:
         self.ws_attn = Workspace(device)
         self.ws_verify = Workspace(device)
         self.attn_out = None
-        self.sel = None
+        self.sels = {}     # by `top`: a captured step keeps the address of its own
 
     def draft(self, draft_logits):
         draft_topk(draft_logits, self.k, self.tok, self.conf, self.stats, self.ws_draft, self.status)
@@ -60,15 +60,15 @@ class TreeStep:
         """attend() over one layer of a KV8Cache (cache.py): the prefix in
         e4m3 pages, or (top given, a cache with bounds) the first `first`, the
         last `last` and the best other pages of it, `top` in all, that each
-        node and KV head selects.  Returns (out, lse)."""
+        node and KV head selects (left in sels[top]).  Returns (out, lse)."""
         if self.attn_out is None or self.attn_out.shape != q.shape or self.attn_out.dtype != q.dtype:
             self.attn_out = torch.empty_like(q)
         if top is not None:
-            shape = (self.B, self.m + 1, self.Hkv, top)
-            if self.sel is None or self.sel.shape != shape:
-                self.sel = torch.empty(shape, dtype=torch.int32, device=q.device)
-            cache.select(layer, q, top, first, last, out=self.sel)
-            return cache.attend_pages(layer, q, k_tree, v_tree, self.tree["mask"], self.sel, scale, self.attn_out, self.lse)
+            sel = self.sels.get(top)
+            if sel is None:
+                sel = self.sels[top] = torch.empty((self.B, self.m + 1, self.Hkv, top), dtype=torch.int32, device=q.device)
+            cache.select(layer, q, top, first, last, out=sel)
+            return cache.attend_pages(layer, q, k_tree, v_tree, self.tree["mask"], sel, scale, self.attn_out, self.lse)
         return cache.attend(layer, q, k_tree, v_tree, self.tree["mask"], scale, self.attn_out, self.lse)
 
     def commit_kv8(self, cache, k_trees, v_trees):
