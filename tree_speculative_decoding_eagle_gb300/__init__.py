@@ -35,6 +35,7 @@ library is missing or a call reports an error, an exception is raised.
                    in one call, or recorded once as a graph and replayed)
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -449,6 +450,15 @@ def _device_of(t, name):
     return dev
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_size(name, dev, *sizes):
+    """Bytes that the named query asks for on CUDA device number dev: a number
+    of the sizes alone, kept because asking takes a microsecond of a call that
+    takes fourteen."""
+    with torch.cuda.device(dev):
+        return getattr(load_library(), name)(*sizes)
+
+
 def _call(what, fn, dev, stream, *args):
     """fn(*args, stream) with device number `dev` current, on its current stream
     unless one is given."""
@@ -761,7 +771,7 @@ def kv8_select(q, k_bounds, k_scale, block_table, kv_len, page_size, top, first=
     if out is None:
         out = torch.empty((B, n, Hkv, top), dtype=i32, device=q.device)
     code = _dtype_code(q)
-    need = lib.eagle_kv8_select_workspace_size(code, B, n, Hq, Hkv, dh, max_pages, page_size)
+    need = _workspace_size("eagle_kv8_select_workspace_size", dev, code, B, n, Hq, Hkv, dh, max_pages, page_size)
     buf, nbytes = (workspace or Workspace(q.device)).get(need)
     if buf is not None and buf.get_device() != dev:
         raise EagleError(f"the workspace must be on device {dev}, not on {buf.device}")
@@ -796,7 +806,7 @@ def tree_attn_kv8_pages(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_l
     code = _dtype_code(q)
     if k_pages.shape[3] != dh:
         raise EagleError("q must have the pages' head dimension")
-    need = lib.eagle_tree_attn_kv8_pages_workspace_size(code, B, n, Hq, Hkv, dh, top, max_pages, page_size)
+    need = _workspace_size("eagle_tree_attn_kv8_pages_workspace_size", dev, code, B, n, Hq, Hkv, dh, top, max_pages, page_size)
     buf, nbytes = (workspace or Workspace(q.device)).get(need)
     if buf is not None and buf.get_device() != dev:
         raise EagleError(f"the workspace must be on device {dev}, not on {buf.device}")
