@@ -23,18 +23,18 @@ namespace eagle {
 // T threads (32, or whole CTAs of 128 and more) a row; a warp takes 32 V neighbouring
 // pages, lane by lane, so that a vote gives the places of 32 of them.
 template <int T, int V>
-__global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArgs a, int64_t row_count) {
-  constexpr int THREADS = T < 128 ? 128 : T, WARPS = T / 32;
+__global__ void __launch_bounds__(T < 128 ? 64 : T, T < 128 ? 20 : 1) kv8_choose_kernel(SelectArgs a, int row_count) {
+  constexpr int THREADS = T < 128 ? 64 : T, WARPS = T / 32;
   __shared__ int part[2][THREADS / 32];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x % T) >> 5;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / T) + threadIdx.x / T;
+  const int row = blockIdx.x * (THREADS / T) + threadIdx.x / T;  // B * n * Hkv is at most 2^24
   pdl_wait();
   pdl_trigger();
   if (row >= row_count) return;  // whole warps: T < 128 has one warp a row
-  const int b = static_cast<int>(row / (static_cast<int64_t>(a.n) * a.Hkv));
+  const int b = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.n * a.Hkv);
   const int np = live_pages(a, b), K = min(a.top, np);
   const int p0 = warp * 32 * V + lane;  // this lane's pages: p0, p0 + 32, ..
-  const float *src = a.scores + row * a.stride + p0;
+  const float *src = a.scores + static_cast<int64_t>(row) * a.stride + p0;
   int turn = 0;
   const auto row_sum = [&](int x) {  // over the row's threads
     x = __reduce_add_sync(0xffffffffu, x);
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv8_choose_kernel(SelectArg
       }
     }
   }
-  int32_t *dst = a.sel + row * a.top;
-  float *dst_s = a.sel_score ? a.sel_score + row * a.top : nullptr;
+  int32_t *dst = a.sel + static_cast<int64_t>(row) * a.top;
+  float *dst_s = a.sel_score ? a.sel_score + static_cast<int64_t>(row) * a.top : nullptr;
   const uint32_t below = (1u << lane) - 1u;
   const auto take = [&](int at, int j) {
     dst[at] = p0 + 32 * j;
@@ -169,9 +169,9 @@ size_t kv8_select_workspace_bytes(int B, int n, int Hkv, int max_pages) {
 
 template <int T, int V>
 static cudaError_t launch_choose(const SelectArgs &a, cudaStream_t st) {
-  constexpr int THREADS = T < 128 ? 128 : T;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.n * a.Hkv;
-  const dim3 grid(static_cast<unsigned>((rows * T + THREADS - 1) / THREADS));
+  constexpr int THREADS = T < 128 ? 64 : T;
+  const int rows = a.B * a.n * a.Hkv, per_cta = THREADS / T;
+  const dim3 grid((rows + per_cta - 1) / per_cta);
   return launch_chained(kv8_choose_kernel<T, V>, grid, dim3(THREADS), 0, st, a, rows);
 }
 
