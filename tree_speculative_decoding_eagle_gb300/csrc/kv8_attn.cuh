@@ -67,10 +67,10 @@ __device__ __forceinline__ void kv8_write_out(const Kv8Args &a, int bg, int rho,
 // slots: out = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m).
 // Eight splits' values are in flight at a time.
 template <int DH>
-__device__ __forceinline__ void kv8_merge_item(const Kv8Args &a, int bg, int mg, int MT, int rr, int c) {
+__device__ __forceinline__ void kv8_merge_item(const Kv8Args &a, int bg, int mg, int mgroups, int MT, int rr, int c) {
   constexpr int NV = DH / 4;
   const int64_t slot_floats = static_cast<int64_t>(a.slot_rows) * (DH + 2);
-  const float *slots = a.part + (static_cast<int64_t>(bg) * gridDim.y + mg) * a.S * slot_floats;
+  const float *slots = a.part + (static_cast<int64_t>(bg) * mgroups + mg) * a.S * slot_floats;
   float M = -INFINITY, Ls = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < a.S; s0 += 8) {
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) tree_attn_kv8_merge_kernel(Kv8Args a, int
   const int nr = max(0, min(a.n * a.G - mg * MT * 128, MT * 128));
   const int item = blockIdx.x * blockDim.x + threadIdx.x;
   pdl_wait();  // the partial results come from the attention kernel
-  if (item < nr * NV) kv8_merge_item<DH>(a, bg, mg, MT, item / NV, item % NV);
+  if (item < nr * NV) kv8_merge_item<DH>(a, bg, mg, gridDim.y, MT, item / NV, item % NV);
 }
 
 // The merge where B * Hkv passes a grid's z dimension: the items of all (b, g) in one row.
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(256) tree_attn_kv8_merge_flat_kernel(Kv8Args a
   const int64_t bg = item / per;
   if (bg < static_cast<int64_t>(a.B) * a.Hkv) {
     const int at = static_cast<int>(item - bg * per);
-    kv8_merge_item<DH>(a, static_cast<int>(bg), 0, 1, at / (DH / 4), at % (DH / 4));
+    kv8_merge_item<DH>(a, static_cast<int>(bg), 0, 1, 1, at / (DH / 4), at % (DH / 4));
   }
 }
 

@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(128, 3)
     if (*abort_flag) return;
     const int share = (rows_total * NV + a.S - 1) / a.S, i0 = static_cast<int>(cluster_ctarank()) * share;
     for (int item = i0 + tid; item < min(rows_total * NV, i0 + share); item += 128)
-      kv8_merge_item<DH>(a, bg, 0, 1, item / NV, item % NV);
+      kv8_merge_item<DH>(a, bg, 0, 1, 1, item / NV, item % NV);
   }
 }
 

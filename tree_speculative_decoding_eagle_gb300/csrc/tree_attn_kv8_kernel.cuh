@@ -208,13 +208,17 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
   signed char *q_exp = reinterpret_cast<signed char *>(named + 4 * Sh::kNamedWords) + (ONE ? 32 : 0);  // [MT * QR]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.x, mg = blockIdx.y;
-  const int bg = blockIdx.z, b = bg / a.Hkv, g = bg % a.Hkv;
+  // SEL: every sequence's full M-groups come first; the last ones, which have fewer
+  // rows, then fill what those leave of the last wave (16 x 49 nodes with 8 heads, 1.7
+  // waves: 131 -> 126 us; 64 x 61 nodes, 6.7 waves, whose two groups then find less of
+  // each other's pages in L2: 321 -> 323; a choice at run time costs both 2 %).
+  const int split = blockIdx.x, mg = SEL ? blockIdx.z : blockIdx.y, mgroups = SEL ? gridDim.z : gridDim.y;
+  const int bg = SEL ? blockIdx.y : blockIdx.z, b = bg / a.Hkv, g = bg % a.Hkv;
   const int n = a.n;
   constexpr int kConvertWarp = MT * 4, kProducerWarp = kConvertWarp + 4 * Sh::kConvertGroups, kMmaWarp = kProducerWarp + 2;
 
   const int32_t *len_at = a.kv_len + b;
-  if constexpr (SEL) len_at = a.lens + static_cast<int64_t>(bg) * gridDim.y + mg;
+  if constexpr (SEL) len_at = a.lens + static_cast<int64_t>(bg) * mgroups + mg;
   if (tid == 0) prefetch_l2(len_at);
   if (tid == 32) {
     for (int i = 0; i < 2 * S8; ++i) {
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
       const auto page_at = [&](int batch) {
         const int key = p0 * NK + (batch * 32 + lane) * 16;
         if (key >= key_end) return 0;
-        if constexpr (SEL) return a.pages[(static_cast<int64_t>(bg) * gridDim.y + mg) * a.list_stride + (key >> a.log_page)];
+        if constexpr (SEL) return a.pages[(static_cast<int64_t>(bg) * mgroups + mg) * a.list_stride + (key >> a.log_page)];
         const int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + (key >> a.log_page)];
         if (page >= 0 && page < a.num_pages) return page;
         report(a.status, EAGLE_ERR_INVALID);  // outside the pool: read page 0
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     int bit_at = -1;
     uint32_t bit_word = 0;
     if constexpr (SEL)
-      bit_row = a.bits + ((static_cast<int64_t>(bg) * gridDim.y + mg) * a.group_nodes + (row_ok ? i - mg * MT * 128 / a.G : 0)) * a.bit_words;
+      bit_row = a.bits + ((static_cast<int64_t>(bg) * mgroups + mg) * a.group_nodes + (row_ok ? i - mg * MT * 128 / a.G : 0)) * a.bit_words;
     // m is the exponent base of this row's P' and O; it is raised only when the
     // row maximum exceeds it by more than 8, so O is rescaled rarely.
     float m = -INFINITY, l = 0.f;
@@ -863,7 +867,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     tc_fence_before();
     __syncthreads();
     constexpr int NV = DH / 4;
-    const int64_t cl = static_cast<int64_t>(bg) * gridDim.y + mg;
+    const int64_t cl = static_cast<int64_t>(bg) * mgroups + mg;
     float *slot = a.part + (cl * a.S + split) * static_cast<int64_t>(a.slot_rows) * (DH + 2);
     for (int idx = tid; idx < nr * NV; idx += Sh::kThreads) {
       const int r = idx / NV, c = idx % NV;
@@ -883,7 +887,7 @@ __global__ void __launch_bounds__((MT == 1 ? 4 : MT + 2) * 128, OCC)
     const int per = (nr + a.S - 1) / a.S;
     const int q0 = min(nr, static_cast<int>(cluster_ctarank()) * per), q1 = min(nr, q0 + per);
     for (int item = tid; item < (q1 - q0) * (DH / 4); item += Sh::kThreads)
-      kv8_merge_item<DH>(a, bg, mg, MT, q0 + item / (DH / 4), item % (DH / 4));
+      kv8_merge_item<DH>(a, bg, mg, mgroups, MT, q0 + item / (DH / 4), item % (DH / 4));
   }
 }
 
@@ -947,7 +951,7 @@ static cudaError_t launch_kv8_v(const CUtensorMap *maps, const typename Kv8Kerne
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != Sh::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const dim3 grid(p.S, p.mgroups, a.B * a.Hkv);
+  const dim3 grid(p.S, SEL ? a.B * a.Hkv : p.mgroups, SEL ? p.mgroups : a.B * a.Hkv);
   if constexpr (MERGE == 2) {
     e = launch_chained(kernel, grid, dim3(Sh::kThreads), Sh::kSmem, st, maps[0], maps[1], a);
     if (e != cudaSuccess) return e;
