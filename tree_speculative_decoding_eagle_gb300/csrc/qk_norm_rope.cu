@@ -13,6 +13,11 @@
 // up to four of its heads, their vectors on their way together while the node's turns
 // and the weights are made ready in shared memory; the block is as large as the
 // node's heads need.
+// Measured, on the device: 8191 nodes of 40 + 40 heads of 128, a quarter turned, f32,
+// 184 us (1.0 GB, 82 % of the copy rate); 64 x 61 nodes of 64 + 8 heads of 64, bf16, 21.3
+// us (80 MB, 56 %; rope.cu without the norm 17.6: four tenths more instructions, and the
+// barrier before the turns is waited at twice as long); 61 nodes of 32 + 32 heads of 128
+// 3.5 us.  The arithmetic in packed pairs (f32x2): 20.7 and 3.3 us, but 191 in f32.
 #include "rope.cuh"
 
 namespace eagle {

@@ -15,6 +15,16 @@
 // few-row kernel (10.5 against 4.3 ns of the device at dh 64, pages of 128; 9.2 and 3.1
 // at dh 128, pages of 64), so the lists win unless hardly two nodes share a page, and
 // cost no more than the attention to the whole prefix at the worst.
+//
+// What bounds the attention over lists: each M-tile's chain S - softmax - P - O, as
+// for a whole prefix, although two fifths of the warps have no row that counts a page
+// of the tile (issue slots 44 %, tensor pipe 41 % of active cycles), and the last wave.
+// Measured, on the device, lists included: 16 x 49 nodes, 64 heads on 8 of 128, 16 of 64
+// to 128 pages of 64 126 us (a group lists 45 and 40; the lists take 5; 314 with every node
+// a sequence of its own); 64 x 61 nodes, 64 heads on 8 of 64, 8 of 64 pages of 128 322
+// us (a group lists 24; 1074; the whole prefix 690).  An M-tile that passes over the tiles
+// it does not count (a fifth and a seventh of them) makes the roles' hand-overs
+// irregular: 150 and 380 us.
 #include "tree_attn_kv8_kernel.cuh"
 
 namespace eagle {
