@@ -247,6 +247,33 @@ def test_lists_that_are_not_lists(n, Hq):
     assert int(c.status) == -1 and torch.isfinite(out.float()).all()
 
 
+def test_the_most_sequences():
+    """65535 sequences of a KV head, with few rows and with many.  Rows are weighted
+    means of values up to vmax, each side's off by at most (2^-8 + 2^-10) vmax."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    B, dh, N = 65535, 64, 300
+    k, v = (torch.randn(N, 1, 16, dh, generator=g, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    ones = torch.ones(N, 1, device="cuda")
+    table = torch.randint(0, N, (B, 9), generator=g, device="cuda", dtype=torch.int32)
+    kv = torch.randint(0, 9 * 16 + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    for n in (1, 33):
+        q = torch.randn(B, n, 1, dh, generator=g, device="cuda").to(torch.bfloat16)
+        kt, vt = (torch.randn(B, 1, n, dh, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        mask = (torch.ones(n, dtype=torch.int64, device="cuda") << torch.arange(n, device="cuda")).expand(B, n)[..., None].contiguous()
+        sel = torch.randint(0, 9, (B, n, 1, 2), generator=g, device="cuda", dtype=torch.int32).sort(-1).values
+        sel[..., 1] += 1                           # ascending; past the prefix: counts for nothing
+        sel = torch.where(sel * 16 < kv[:, None, None, None], sel, -1).to(torch.int32)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = eg.tree_attn_kv8_pages(q, k, v, ones, ones, table, kv, kt, vt, mask, sel, status=status)
+        assert int(status) == 0
+        for part in (slice(0, 50), slice(65485, 65535)):
+            cut = [x[part].contiguous() for x in (table, kv, kt, vt, mask, sel)]
+            got, got_lse = eg.tree_attn_kv8_pages(q[part].contiguous(), k, v, ones, ones, *cut)
+            vmax = float(max(v.float().abs().max(), vt.float().abs().max()))
+            assert float((got.float() - out[part].float()).abs().max()) <= 2 * (2.0 ** -8 + 2.0 ** -10) * vmax
+            assert float((got_lse - lse[part]).abs().max()) <= 1e-4
+
+
 def test_offsets_past_31_bits():
     """A pool of more than 2^31 bytes, its last pages in use."""
     Listed([200, 70], 2, 4, 2, 128, 256, 1, num_pages=40000).run()

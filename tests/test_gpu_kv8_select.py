@@ -167,6 +167,38 @@ def test_a_query_selects_the_same_alone_and_in_any_batch():
         assert (sel[0, 0] == whole[b, i]).all() and (s[0, 0] == score[b, i]).all()
 
 
+def test_scores_past_31_bits_of_offset():
+    """4096 nodes, 40 KV heads, 16384 pages: 2.7e9 scores in the workspace."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    Hkv, pages, dh = 40, 16384, 64
+    q = torch.randn(1, 4096, Hkv, dh, generator=g, device="cuda").to(torch.bfloat16)
+    numbers = torch.randint(-40, 41, (pages, Hkv, 2, dh), generator=g, device="cuda").float() / 2
+    bounds = torch.sort(numbers, dim=2).values.to(torch.float8_e4m3fn)
+    scale = torch.ones(pages, Hkv, device="cuda")
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    kv = i32([pages * 16 - 3])
+    sel = eg.kv8_select(q, bounds, scale, table, kv, 16, 7)
+    for i in (0, 1, 2047, 3277, 4094, 4095):
+        one = eg.kv8_select(q[:, i:i + 1].contiguous(), bounds, scale, table, kv, 16, 7)
+        assert torch.equal(one[0, 0], sel[0, i]), i
+    torch.cuda.empty_cache()
+
+
+def test_the_most_sequences():
+    """65535 sequences of a KV head, with few rows and with many."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    B, dh, N = 65535, 64, 300
+    bounds = torch.sort(torch.randint(-40, 41, (N, 1, 2, dh), generator=g, device="cuda").float() / 2, dim=2).values.to(torch.float8_e4m3fn)
+    scale = torch.ones(N, 1, device="cuda")
+    table = torch.randint(0, N, (B, 9), generator=g, device="cuda", dtype=torch.int32)
+    kv = torch.randint(0, 9 * 16 + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    for n in (1, 33):
+        q = torch.randn(B, n, 1, dh, generator=g, device="cuda").to(torch.bfloat16)
+        sel = eg.kv8_select(q, bounds, scale, table, kv, 16, 3)
+        for part in (slice(0, 50), slice(65485, 65535)):
+            assert torch.equal(eg.kv8_select(q[part].contiguous(), bounds, scale, table[part].contiguous(), kv[part].contiguous(), 16, 3), sel[part])
+
+
 def test_page_numbers_outside_the_pool():
     """Page 0's bounds are read in their place; entries past the prefix are not looked at."""
     c = Case([40 * 16, 90], 2, 4, 2, 64, 16)
