@@ -108,6 +108,22 @@ def test_ties_go_to_the_lower_pages():
     c.check(2000, 0, 0)
 
 
+@pytest.mark.parametrize("n", [3, 49])
+def test_zeros_of_either_sign_are_ties(n):
+    """Products of a zero query, or with zero bounds, are zeros of both signs."""
+    c = Case([40 * 16], n, 4, 2, 64, 16)
+    number = np.random.default_rng(3).integers(1, 9, c.codes.shape) / 2.0
+    number[c.table[0, ::2]] *= -1                  # pages of negative bounds alone, and of positive ones alone
+    c.codes = kv8.encode(np.sort(number, axis=2))
+    c.q[:, 0] = 0
+    c.q[:, 1] = -0.0
+    c.q[:, 2, :, 1:] = 0                           # one column counts; its bounds are zeros of either sign
+    c.codes[..., 0] = np.where(np.arange(c.N) % 2, 0x80, 0)[:, None, None]
+    sel = c.check(7, 0, 0)
+    for i in range(3):
+        assert sel[0, i, 0].tolist() == list(range(7))
+
+
 def test_the_largest_sums_are_exact():
     """All columns at the edge: sums up to 128 * 128 * 448, neighbours half a unit apart."""
     for dh in (64, 128):

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(ScoreShape<DH, NR>::kThreads, ScoreShape<DH, N
 #pragma unroll
           for (int h = 1; h < (1 << LG); ++h) best = fmaxf(best, v[c + h]);
           const int node = (c0 + c) >> LG;
-          if (p < p_end && node0 + node < a.n) out[node * per_node + p] = best * page_scale;
+          if (p < p_end && node0 + node < a.n) out[node * per_node + p] = fmaf(best, page_scale, 0.f);  // a zero is +0: keys are ordered by bits
         }
       }
       tc_fence_before();
