@@ -789,8 +789,11 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages,
  *
  * eagle_kv8_bounds renews the bounds of every page that holds positions
  * from_len[b] .. kv_len[b]-1 of a request, from all of the page's rows before
- * kv_len[b]: after an append or a commit, with the length before it (a call that
- * re-encoded a page's earlier rows touched that page).
+ * kv_len[b]: after an append or a commit, with the length before it.  An append that
+ * gives a page a larger scale leaves its bounds in the old one's units until this
+ * call, also where the new rows are not counted in the end: a from_len of the length
+ * before less one always renews the last page, and eagle_kv8_select comes before the
+ * append or after this call.
  *   k_pages    as in eagle_kv8_append; block_table, max_pages, page_size,
  *              num_pages as in eagle_tree_attn_paged
  *   from_len, kv_len   device int32 [B]; nothing is done where kv_len <= from_len;

@@ -12,9 +12,10 @@ all on the device, and calls the library's entry points on the current stream:
 and for long contexts, in a cache made with bounds=True:
     select   -> eagle_kv8_select    the pages that each node and KV head attends to
     attend_pages -> eagle_tree_attn_kv8_pages   draft nodes or single tokens over those
-whose bounds (eagle_kv8_bounds) grow() and commit() renew for the pages they touched.
-A request whose kv_len is set back keeps the wider bounds of its last page until it
-grows again.
+whose bounds (eagle_kv8_bounds) grow() and commit() renew, from each request's last
+page on: append() may re-encode that page, so select() of a layer comes before its
+append() or after grow().  Rows that are not counted in the end, and a kv_len that
+is set back, need a grow() too (grow(0) counts nothing), before the next select().
 kv_len counts the positions before the tree's root, which is node 0 of the tree,
 at position kv_len.  So one step over a tree of depth D is
     reserve(D + 1) -> rope(pos_base=kv_len, pos_off=depth) -> attend -> verify
@@ -65,7 +66,7 @@ class KV8Cache:
         if bounds:
             shape = (num_pages, Hkv, 2, dh)
             self.k_bounds = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(layers)]
-            self._before = torch.zeros(B, **i32)      # the lengths before grow() or commit()
+            self._renew_from = torch.zeros(B, **i32)  # each request's last position before grow() or commit()
         self.block_table = torch.full((B, max_pages), -1, **i32)
         self.page_count = torch.zeros(B, **i32)
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)      # page 0 on top
@@ -94,19 +95,25 @@ class KV8Cache:
     def grow(self, new_len):
         """new_len [B] (or one number) tokens have been appended; counts nothing
         where the last reservation was refused, since append() wrote none.
-        Renews the bounds of the pages they are in, where the cache has bounds."""
-        if self.k_bounds is not None:
-            self._before.copy_(self.kv_len)
+        Where the cache has bounds, renews those of each request's last page
+        and of the pages it grew into."""
+        self._mark()
         if torch.is_tensor(new_len):
             self.kv_len.addcmul_(self.granted, new_len.to(torch.int32))
         else:
             torch.add(self.kv_len, self.granted, alpha=new_len, out=self.kv_len)
         self._renew_bounds()
 
+    def _mark(self):
+        # the page of the last position before: rows that joined it may have changed its
+        # scale, whether or not they are counted, and a length set back leaves it too wide
+        if self.k_bounds is not None:
+            torch.sub(self.kv_len, 1, out=self._renew_from)
+
     def _renew_bounds(self):
         if self.k_bounds is not None:
             for pages, bounds in zip(self.k_pages, self.k_bounds):
-                kv8_bounds(pages, self.block_table, self._before, self.kv_len, bounds, status=self.status)
+                kv8_bounds(pages, self.block_table, self._renew_from, self.kv_len, bounds, status=self.status)
 
     def attend(self, layer, q, k_tree, v_tree, mask, scale=None, out=None, lse=None, workspace=None):
         return tree_attn_kv8(q, *self._pools(layer), self.block_table, self.kv_len, k_tree, v_tree, mask, scale=scale,
@@ -134,8 +141,7 @@ class KV8Cache:
         last = len(self.k_pages) - 1
         if len(k_trees) != last + 1 or len(v_trees) != last + 1:
             raise EagleError("commit takes the tree K/V of every layer")
-        if self.k_bounds is not None:
-            self._before.copy_(self.kv_len)
+        self._mark()
         for layer, (k, v) in enumerate(zip(k_trees, v_trees)):
             lens = self.kv_len
             if layer < last:
