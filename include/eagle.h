@@ -782,10 +782,16 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages,
  * Three calls: bounds of each page's keys, kept beside the pages; the pages whose
  * bounds allow a query the greatest products; the attention over those pages and
  * the tree.  A query is a node of the tree and a KV head (the heads that share it
- * choose together), and what it selects depends on nothing but itself and the
- * cache: not on the tree around it, the batch or the launch.  So a verification
- * over selected pages accepts what decoding token by token over selected pages
- * would produce.
+ * choose together), and what it selects depends on nothing but itself, kv_len, the
+ * prefix's scales and bounds: not on the tree around it, the batch or the launch.
+ * Verification over selected pages is not decoding token by token over selected
+ * pages: a node attends to the tree's path beside its `top` pages, a token decoded
+ * alone has that path in pages that take places of `top`.  Node i of a path selects
+ * the pages that its token selects alone (with kv_len + i, the path's rows stored)
+ * where last >= 1 and positions kv_len - 1 .. kv_len + i - 1 lie in one page; the keys
+ * are then the same, the path's own up to their rounding to e4m3.  A path that
+ * goes on into another page (any node but the root, where kv_len is a multiple of
+ * page_size), or last = 0, may give other lists, and so other tokens.
  *
  * eagle_kv8_bounds renews the bounds of every page that holds positions
  * from_len[b] .. kv_len[b]-1 of a request, from all of the page's rows before

@@ -8,9 +8,10 @@
 //   u = sum_c max(q'_c, 0) hi_c + min(q'_c, 0) lo_c
 // is a sum of at most 128 multiples of 1/2 up to 128 * 448: below 2^23, so a float32
 // sum of it is exact whatever its order.  The score u 2^(e + page scale's exponent)
-// is exact too, and the pages chosen for a node are the same in a tree, alone, in
-// any batch and on any launch shape: verification with selected pages accepts what
-// decoding token by token with selected pages would have produced.
+// is exact too, and the pages chosen for a query over one prefix are the same in a
+// tree, alone, in any batch and on any launch shape.  (A token decoded after its
+// path has been stored has another prefix: its list is the same while `last` >= 1
+// and the path stays in the prefix's last page.)
 // The node's score of a page is the largest over the heads that share the KV head.
 //
 // Two kernels.  Scores: kv8_score.cu.  Choice (here): a row's scores as ordered

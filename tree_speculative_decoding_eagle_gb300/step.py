@@ -60,7 +60,9 @@ class TreeStep:
         """attend() over one layer of a KV8Cache (cache.py): the prefix in
         e4m3 pages, or (top given, a cache with bounds) the first `first`, the
         last `last` and the best other pages of it, `top` in all, that each
-        node and KV head selects (left in sels[top]).  Returns (out, lse)."""
+        node and KV head selects (left in sels[top]): what the token decoded
+        alone would select too while last >= 1 and the node's path stays in
+        the prefix's last page.  Returns (out, lse)."""
         if self.attn_out is None or self.attn_out.shape != q.shape or self.attn_out.dtype != q.dtype:
             self.attn_out = torch.empty_like(q)
         if top is not None:
