@@ -780,8 +780,8 @@ int eagle_tree_attn_kv8(const void *q, const uint8_t *k_pages,
 /* ------------------------------------------------------------------------
  * Long contexts: attention to the pages that a query selects.
  * Three calls: bounds of each page's keys, kept beside the pages; the pages whose
- * bounds allow a query the greatest products; the attention over those pages and
- * the tree.  A query is a node of the tree and a KV head (the heads that share it
+ * bounds allow a query, rounded to 8 bits, the greatest products; the attention over
+ * those pages and the tree.  A query is a node of the tree and a KV head (the heads that share it
  * choose together), and what it selects depends on nothing but itself, kv_len, the
  * prefix's scales and bounds: not on the tree around it, the batch or the launch.
  * Verification over selected pages is not decoding token by token over selected
@@ -831,7 +831,10 @@ int eagle_kv8_bounds(const uint8_t *k_pages, const int32_t *block_table,
  * score of a page with bounds lo, hi and scale s is
  *   max over the heads h of g of  2^e s (sum over q'_c > 0 of q'_c hi_c
  *                                        + sum over q'_c < 0 of q'_c lo_c),
- * the greatest product with q' of any key within the bounds.
+ * the greatest product with q' of any key within the bounds.  It ranks pages by the
+ * rounded row, and is no bound for q itself: q' is off by up to 2^(e-1) a column, the
+ * score by up to 2^(e-1) s times the sum of max(|lo|, |hi|), and columns below 1/256 of
+ * the row's largest count for nothing.
  * Every score is exact in float32, in any order of the sum.  Selected are the first
  * `first` and the last `last` pages of the prefix, then the greatest scores, ties to
  * the lower page; all of them where the prefix has no more than `top`.

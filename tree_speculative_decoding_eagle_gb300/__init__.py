@@ -759,7 +759,8 @@ def kv8_select(q, k_bounds, k_scale, block_table, kv_len, page_size, top, first=
     k_scale float32 [num_pages, Hkv], block_table int32 [B, max_pages] -> sel int32
     [B, n, Hkv, top], logical pages in ascending order, then -1: the first `first` and
     the last `last` pages of the prefix and those whose bounds allow the greatest
-    product with the query.  `score` float32 of the same shape receives theirs."""
+    product with the query, each row of it rounded to whole numbers of at most 128
+    times a power of two.  `score` float32 of the same shape receives theirs."""
     if stream is not None:     # what is allocated here belongs to that stream
         with torch.cuda.stream(stream):
             return kv8_select(q, k_bounds, k_scale, block_table, kv_len, page_size, top, first, last, out, score, workspace, status)

@@ -1,6 +1,6 @@
 // The pages of the 8-bit cache that a query is to attend to: for each node, KV head
-// and page the greatest product that the page's bounds allow, and the `top` pages
-// with the greatest.
+// and page the greatest product that the page's bounds allow with the query rounded to
+// 8 bits, and the `top` pages with the greatest.
 //
 // A query row (node i, head h) is taken as whole numbers q' = rint(q 2^-e), e the
 // power of two that puts its largest magnitude into [64, 128], |q'| <= 128.  With
