@@ -13,8 +13,10 @@
 // row gives the keys of pages without its bit weights of 2^-inf.  A listed page costs
 // an M-group about what two and a half nodes pay for a page of their own in the
 // few-row kernel (10.5 against 4.3 ns of the device at dh 64, pages of 128; 9.2 and 3.1
-// at dh 128, pages of 64), so the lists win unless hardly two nodes share a page, and
-// cost no more than the attention to the whole prefix at the worst.
+// at dh 128, pages of 64), so the lists win unless hardly two nodes share a page.  Where
+// none do and the lists together are the prefix, they cost more than the attention to
+// all of it: 285 against 277 us for 16 x 49 nodes, 28 against 22 for one such tree with
+// 132 pages of 16, at the worst measured 77 against 44 (256 nodes, 1024 pages of 16).
 //
 // What bounds the attention over lists: each M-tile's chain S - softmax - P - O, as
 // for a whole prefix, although two fifths of the warps have no row that counts a page
@@ -164,8 +166,14 @@ static ListPlan list_plan(int B, int n, int Hq, int Hkv, int dh, int top, int ma
                      : attn_kv8_few_workspace_bytes(B * n, 1, Hq, Hkv, dh, positions, num_sms);
     return l;
   }
-  // The lists' lengths are known on the device alone: the KV split is chosen for
-  // groups whose nodes name twice what one of them does.
+  // The lists' lengths are known on the device alone.  Where the groups fill the SMs,
+  // the KV split is chosen for groups whose nodes name twice what one of them does, else
+  // for the longest list there can be: SMs that idle cost nothing, and nodes that share
+  // no page would leave each group alone with a long list.  Measured (us on the device,
+  // chosen by twice one node's / by the longest; nodes that agree, half agree, share
+  // nothing): 49 nodes of 64 heads on 8 of 128, 4 of 132 pages of 16 19 / 23, 26 / 24,
+  // 51 / 28; 61 nodes, 32 heads with keys of their own, 4 of 256 pages 18 / 27, 31 / 29,
+  // 92 / 43; 256 nodes, 8 heads of 64, 8 of 1024 pages of 16 44 / 45, 71 / 50, 271 / 77.
   const int64_t guess = min(static_cast<int64_t>(max_pages), static_cast<int64_t>(2) * top);
   l.p = kv8_plan(B, n, Hq, Hkv, dh, static_cast<int>(guess * page_size), num_sms);
   const int group_rows = l.p.MT * 128;
@@ -173,6 +181,8 @@ static ListPlan list_plan(int B, int n, int Hq, int Hkv, int dh, int top, int ma
   l.list_stride = static_cast<int>(min(static_cast<int64_t>(max_pages), static_cast<int64_t>(l.group_nodes) * top));
   l.bit_words = (l.list_stride + 31) / 32;
   const size_t groups = static_cast<size_t>(B) * Hkv * l.p.mgroups;
+  if (groups < static_cast<size_t>(num_sms) * l.p.ctas_per_sm)
+    l.p = kv8_plan(B, n, Hq, Hkv, dh, l.list_stride * page_size, num_sms);
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   l.pages_off = up(groups * sizeof(int32_t));
   l.bits_off = l.pages_off + up(groups * l.list_stride * sizeof(int32_t));
