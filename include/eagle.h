@@ -847,7 +847,8 @@ int eagle_kv8_bounds(const uint8_t *k_pages, const int32_t *block_table,
  *              of pages that are selected without one, then -inf
  *   status     EAGLE_ERR_INVALID for a block-table entry outside [0, num_pages)
  *              (page 0's bounds are read in its place)
- * Workspace: the scores of all pages, one float for each node, KV head and page.
+ * Workspace: the scores of all pages, one float for each node, KV head and page of the
+ * table (max_pages, whatever the lengths): 2.1 GB for 4096 nodes, 8 heads, 16384 pages.
  * Limits: dtype EAGLE_BF16, dh in {64, 128}, Hq/Hkv <= 32, max_pages and top <=
  * 16384, B*Hkv <= 65535, B*n*Hkv <= 2^24, num_pages*Hkv < 2^30 (else
  * EAGLE_ERR_UNSUPPORTED); 1 <= n <= 4096; 0 <= first, last; first + last <= top;

@@ -74,7 +74,7 @@ cudaError_t launch_kv8_select(const void *q, const uint8_t *bounds, const float 
                               int max_pages, int page_size, int num_pages, const int32_t *kv_len, int B, int n, int Hq,
                               int Hkv, int dh, int top, int first, int last, int32_t *sel, float *score, void *ws,
                               int32_t *status, int num_sms, cudaStream_t st);
-// tree_attn_kv8_few.cu
+// tree_attn_kv8_pages.cu
 size_t attn_kv8_pages_workspace_bytes(int B, int n, int Hq, int Hkv, int dh, int top, int max_pages, int page_size, int num_sms);
 cudaError_t launch_tree_attn_kv8_pages(const void *q, const uint8_t *k_pages, const uint8_t *v_pages, const float *k_scale,
                                        const float *v_scale, const int32_t *block_table, int max_pages, int page_size,

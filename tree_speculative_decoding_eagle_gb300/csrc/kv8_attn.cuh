@@ -1,4 +1,4 @@
-// What the two kernels of the attention over the 8-bit cache share: their
+// What the kernels of the attention over the 8-bit cache share: their
 // arguments, the powers of two, and the merge of a KV split.
 #pragma once
 
@@ -28,8 +28,8 @@ struct Kv8Args {
   int slot_rows;
 };
 
-// What the few-row kernel has beside for selected pages: B and n of Kv8Args are B *
-// nodes and 1 there.
+// What the few-row kernel and the one for tokens have beside for selected pages: B
+// and n of Kv8Args are B * nodes and 1 there.
 struct Kv8SelArgs : Kv8Args {
   const int32_t *sel;
   int top, nodes;

@@ -25,7 +25,8 @@
 // with many rows what a CTA does before its first tile and after its last (rows to B,
 // scores out; issue slots 51 %) and the last wave.  Measured (alone, caches cold): 64
 // tokens, 64 heads on 8 of 128, pages of 64, 32768 to 131072 keys 40 us (165 MB, 62 % of
-// the copy rate); 16 x 49 nodes, the same heads, 512 pages 29 us (tensor pipe 26 %, ALU
+// the copy rate: 512 CTAs on 304 places; a further whole wave of 304 equal ones, 159 MB,
+// takes 30 us with its choice, 79 %); 16 x 49 nodes, the same heads, 512 pages 29 us (tensor pipe 26 %, ALU
 // 39 % of active cycles, 1.7 waves of CTAs; tiles of 128 rows, two CTAs an SM: 4 us
 // more); one token, 32 heads, 2048 pages 12 us.
 //

@@ -3,28 +3,28 @@
 //
 // Few query rows a KV head (single tokens, small trees): a node and KV head is taken
 // as a sequence of its own, its rows the grouped heads, its block table the list
-// (tree_attn_kv8_tokens.cu up to eight heads, the few-row kernel beyond).
+// (tree_attn_kv8_tokens.cu up to eight heads, the few-row kernel beyond: 64 tokens, 64
+// heads on 4 of 128, 32 pages of 64 43 us, 134 MB, 46 % of the copy rate).
 //
 // Many rows (trees, prompt chunks): nodes of one tree choose much the same pages, and
 // a key tile costs the tensor-core kernel the same for one row and for 256.  So a
 // first kernel makes, for each M-group of query rows, the ascending list of the pages
 // that any of its nodes names, and for each node a bit a listed page; the kernel of
 // tree_attn_kv8_kernel.cuh then runs over that list as it does over a prefix, and a
-// row gives the keys of pages without its bit weights of 2^-inf.  A listed page costs
-// an M-group about what two and a half nodes pay for a page of their own in the
-// few-row kernel (10.5 against 4.3 ns of the device at dh 64, pages of 128; 9.2 and 3.1
-// at dh 128, pages of 64), so the lists win unless hardly two nodes share a page.  Where
-// none do and the lists together are the prefix, they cost more than the attention to
-// all of it: 285 against 277 us for 16 x 49 nodes, 28 against 22 for one such tree with
-// 132 pages of 16, at the worst measured 77 against 44 (256 nodes, 1024 pages of 16).
+// row gives the keys of pages without its bit weights of 2^-inf.
+// What that gains depends on the nodes of a group and on how far they agree, which is
+// known on the device alone: figures at kListRows.  Where no two nodes share a page
+// and the lists together are the prefix, lists cost more than the attention to all of
+// it: 285 against 277 us for 16 x 49 nodes, 28 against 22 for one such tree with 132 pages
+// of 16, at the worst measured 77 against 44 (256 nodes, 1024 pages of 16).
 //
 // What bounds the attention over lists: each M-tile's chain S - softmax - P - O, as
 // for a whole prefix, although two fifths of the warps have no row that counts a page
 // of the tile (issue slots 44 %, tensor pipe 41 % of active cycles), and the last wave.
 // Measured, on the device, lists included: 16 x 49 nodes, 64 heads on 8 of 128, 16 of 64
-// to 128 pages of 64 126 us (a group lists 45 and 40; the lists take 5; 314 with every node
-// a sequence of its own); 64 x 61 nodes, 64 heads on 8 of 64, 8 of 64 pages of 128 322
-// us (a group lists 24; 1074; the whole prefix 690).  An M-tile that passes over the tiles
+// to 128 pages of 64 126 us (a group lists 45 and 40; the lists take 5; 219 with every node
+// a sequence of its own); 64 x 61 nodes, 64 heads on 8 of 64, 8 of 64 pages of 128 323
+// us (a group lists 24; 829; the whole prefix 690).  An M-tile that passes over the tiles
 // it does not count (a fifth and a seventh of them) makes the roles' hand-overs
 // irregular: 150 and 380 us.
 #include "tree_attn_kv8_kernel.cuh"
@@ -44,7 +44,18 @@ cudaError_t launch_tree_attn_kv8_tokens(Kv8SelArgs a, const void *k_pages, const
 constexpr int kUnionPages = 16384;  // pages of a request that a group's map holds
 constexpr int kUnionWarps = 8;
 // Query rows of a KV head from which nodes share lists: more than a CTA of the
-// few-row kernel holds.
+// few-row kernel holds.  Measured (us on the device, lists / every node alone by
+// tree_attn_kv8_tokens.cu; nodes that agree, half agree, share nothing), 512 heads of
+// sequences in all, 8192 keys:
+//   dh 128, 16 pages of 64:  5 nodes of 8 heads 81 / 95, 139 / 96, 266 / 119; 9 of 8 108 / 162,
+//     195 / 163, 497 / 181; 10 of 4 82 / 174, 164 / 174, 420 / 185; 40 of 1 89 / 663, 219 / 663,
+//     447 / 666; 49 of 8 (128 heads) 72 / 221, 140 / 221, 285 / 221
+//   dh 64, 8 pages of 128:   5 of 8 67 / 79, 116 / 80, 223 / 82; 9 of 8 70 / 130, 138 / 131,
+//     343 / 134; 10 of 4 68 / 141, 144 / 142, 354 / 144; 40 of 1 75 / 534, 190 / 534, 379 / 535;
+//     61 of 8 174 / 824, 351 / 824, 716 / 824
+// So lists win for nodes that agree, and for many nodes whether they do or not; five to
+// ten nodes of 4 or 8 heads that half agree or less are faster alone, which this rule on
+// rows does not see.
 constexpr int kListRows = 33;
 
 struct UnionArgs {
